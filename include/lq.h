@@ -65,7 +65,8 @@ typedef enum {
   LQ_ERR_CUDA = -4,        /* a CUDA runtime call failed (message in lq_last_error)              */
   LQ_ERR_TIMEOUT = -5,     /* device: a bounded wait inside a kernel gave up                       */
   LQ_ERR_PHASE = -6,       /* device: a head-state's record count differs from the stated phase    */
-  LQ_ERR_STATE = -7        /* device: the state buffer was not initialised with this config/size  */
+  LQ_ERR_STATE = -7,       /* device: the state buffer was not initialised with this config/size  */
+  LQ_ERR_PARENT = -8       /* device: a beam's parent lies outside its group                        */
 } lq_status;
 
 /* lq_decode_step's `phase` when head-states may sit at different window positions. */
@@ -312,6 +313,130 @@ int lq_export_state(const lq_config* cfg, const void* state, int64_t n_states, f
  */
 int lq_fp32_decode_step(const lq_config* cfg, float* S, int64_t n_states, const float* q, const float* k,
                         const float* v, const float* alpha, const float* beta, float* o, lq_stream_t stream);
+
+/* ------------------------------------------------------------------------------
+ * Generation: prompts in, tokens out, several hypotheses.
+ *
+ * Linear attention with a decay for each head (no delta rule):
+ *   S_t = alpha_t S_{t-1} + v_t k_t^T,   o_t = S_t q_t,
+ * on fp32 states S [d_v][d_k] (row = value channel, as everywhere in this header),
+ * over whole prompts (lq_la_prefill) and for single tokens (lq_la_decode_step);
+ * the selection of beam search (lq_beam_select) and the states that follow the
+ * chosen hypotheses (lq_state_reorder, lq_fp32_state_reorder).
+ * ------------------------------------------------------------------------------ */
+
+/* Element types of q, k, v, o and of beam search's logits. Decays, states and scores are fp32. */
+typedef enum { LQ_F32 = 0, LQ_BF16 = 1, LQ_F16 = 2 } lq_dtype;
+
+typedef struct {
+  int32_t d_k, d_v;         /* 128 and 128 in this build                                           */
+  int32_t heads, key_heads; /* heads of v, o, alpha and S; heads of q and k. Head h reads key head  */
+                            /* h / (heads / key_heads); heads must be a multiple of key_heads       */
+  int32_t dtype;            /* lq_dtype of q, k, v and o                                             */
+  int32_t reserved;         /* 0                                                                     */
+  int64_t q_stride, k_stride, v_stride, o_stride; /* elements from one token to the next: at least   */
+                            /* heads x 128 (key_heads x 128 for q, k), a multiple of 16 bytes; the   */
+                            /* heads of a token and their channels are dense, so rows of one fused   */
+                            /* projection can be passed as they are                                  */
+  int64_t alpha_stride;     /* fp32 elements between tokens' decays: at least heads, or 0 for a decay */
+                            /* that is the same for every token                                      */
+} lq_la_config;
+
+/* Dense token arrays: strides heads x 128, key_heads x 128 and heads; d_k = d_v = 128. */
+void lq_la_config_default(lq_la_config* cfg, int32_t heads, int32_t key_heads, int32_t dtype);
+
+/*
+ * Bytes of workspace lq_la_prefill needs for n_seqs sequences with n_tokens tokens
+ * in all, the longest of max_len (0: not known); 0 when it needs none or when an
+ * argument is invalid. Host only. Up to 64 KB per head and segment of a sequence
+ * that is split; the call never needs more for fewer tokens at the same max_len.
+ */
+size_t lq_la_workspace_bytes(const lq_la_config* cfg, int64_t n_seqs, int64_t n_tokens, int64_t max_len);
+
+/*
+ * Linear attention over prompts: sequence b is tokens cu_seqlens[b] ..
+ * cu_seqlens[b+1]-1 of the packed arrays; it starts from S0[b] (zero if S0 is
+ * NULL) and leaves its last state in S_out[b] (not written if S_out is NULL).
+ * S_out in the order [n_seqs][heads] can be handed to lq_state_init_range,
+ * lq_fp32_decode_step or lq_la_decode_step as it is.
+ *   cu_seqlens int32 [n_seqs + 1] on the device, or NULL for one sequence of
+ *              n_tokens; a sequence may be empty (its S_out is then its S0). A
+ *              sequence whose bounds are not 0 <= begin <= end <= n_tokens, or
+ *              that is longer than a stated max_len, is treated as empty.
+ *   q, k       [n_tokens][key_heads][128], v, o [n_tokens][heads][128], of cfg->dtype
+ *   alpha      fp32 [n_tokens][heads]. Any value is taken as the recurrence takes
+ *              it; 0 forgets the state.
+ *   S0, S_out  fp32 [n_seqs][heads][128][128]; S_out may be S0 itself (in place)
+ *   max_len    the longest sequence, or 0 if the caller does not know it
+ *   workspace  256-byte aligned, lq_la_workspace_bytes(...) bytes for the same
+ *              arguments (NULL if that is 0); its contents need not be kept.
+ * States are kept in fp32 and their products are taken to fp32's accuracy whatever the
+ * type of the tokens; o is rounded once to cfg->dtype (with 16-bit types, products
+ * that only o needs are taken to that type's accuracy).
+ * A token's value, however large, infinite or NaN, reaches its own and later tokens
+ * of its sequence only. Tokens that belong to no sequence get no output. o must not
+ * overlap an input. Errors: LQ_ERR_INVALID_ARG, LQ_ERR_UNSUPPORTED; nothing is
+ * reported from the device.
+ */
+int lq_la_prefill(const lq_la_config* cfg, int64_t n_seqs, int64_t n_tokens, int64_t max_len,
+                  const int32_t* cu_seqlens, const void* q, const void* k, const void* v, const float* alpha,
+                  const float* S0, float* S_out, void* o, void* workspace, size_t workspace_bytes,
+                  lq_stream_t stream);
+
+/*
+ * The recurrent form: one token for each of n_seqs sequences on fp32 states
+ * S [n_seqs][heads][128][128], read and written in place. Token arrays as above with
+ * one token per sequence (strides between sequences). Errors: as lq_la_prefill.
+ */
+int lq_la_decode_step(const lq_la_config* cfg, float* S, int64_t n_seqs, const void* q, const void* k, const void* v,
+                      const float* alpha, void* o, lq_stream_t stream);
+
+/* Bytes of workspace lq_beam_select needs (0 if an argument is invalid). Host only. */
+size_t lq_beam_workspace_bytes(int64_t batch, int32_t beams, int64_t vocab, int32_t n_best);
+
+/*
+ * The selection of beam search: for each of `batch` requests the n_best
+ * continuations of its `beams` hypotheses, by
+ *   score(b, t) = scores[b] + logits[b][t] - log sum_t' exp(logits[b][t']),
+ * best first; equal scores go to the lowest b * vocab + t.
+ *   logits     [batch][beams][vocab] of dtype; row_stride elements from one
+ *              hypothesis' row to the next (>= vocab; any alignment)
+ *   scores     fp32 [batch][beams], the hypotheses' scores so far
+ *   out_scores fp32 [batch][n_best]; out_parent, out_token int32 [batch][n_best]:
+ *              the hypothesis continued (0..beams-1) and its token
+ *   beams 1..32, n_best 1..64 and at most beams * vocab, vocab 1..2^31-1 / beams
+ * A masked token (logit -inf) scores -inf. So does every token of a hypothesis
+ * whose score or log-sum-exp is not finite (a dead hypothesis, a row that is all
+ * -inf, a NaN or +inf logit): they are chosen only when the finite candidates run
+ * out, in the order of their index. Log-sum-exps and scores are compared in 64 bits.
+ * workspace: 256-byte aligned, lq_beam_workspace_bytes(...) bytes; contents need
+ * not be kept. Outputs must not overlap the inputs or each other.
+ */
+int lq_beam_select(int32_t dtype, int64_t batch, int32_t beams, int64_t vocab, int32_t n_best, const void* logits,
+                   int64_t row_stride, const float* scores, float* out_scores, int32_t* out_parent,
+                   int32_t* out_token, void* workspace, size_t workspace_bytes, lq_stream_t stream);
+
+/*
+ * Let the head-states of a state buffer follow the hypotheses chosen: afterwards
+ * beam b of group g holds what beam parent[g * beams + b] held before, in place.
+ * The buffer's head-states are ordered
+ *   s = ((x * groups + g) * beams + b) * inner + i,  x < outer, i < inner,
+ * e.g. outer 1, inner = layers * heads for [request][beam][layer][head], or
+ * outer = layers, inner = heads for [layer][request][beam][head]; the parents
+ * (int32 [groups][beams] on the device) hold for every x and i, and
+ * n_states = outer * groups * beams * inner. A beam that keeps its place is not
+ * touched; of the others the boundary and the records held move. parent = 0 for
+ * every b forks a group's first beam. beams 1..32.
+ * On the device: LQ_ERR_PARENT for a parent outside 0..beams-1, LQ_ERR_STATE for a
+ * buffer or record count that is not valid; that group is left unchanged.
+ */
+int lq_state_reorder(const lq_config* cfg, void* state, int64_t n_states, int64_t outer, int64_t groups,
+                     int32_t beams, int64_t inner, const int32_t* parent, lq_stream_t stream);
+
+/* The same for fp32 states S [n_states][128][128]. A group with a parent outside
+ * 0..beams-1 is left unchanged; there is no status word to say so. */
+int lq_fp32_state_reorder(float* S, int64_t n_states, int64_t outer, int64_t groups, int32_t beams, int64_t inner,
+                          const int32_t* parent, lq_stream_t stream);
 
 /*
  * Synchronize `stream`, then read the state buffer's status word: LQ_OK or the

@@ -277,6 +277,130 @@ int check_tokens(const lq_config* cfg, int64_t n, int dev, const float* q, const
   return LQ_OK;
 }
 
+// ---- linear attention with a decay per head, beam search
+
+int check_la(const lq_la_config* c) {
+  if (!c) return fail(LQ_ERR_INVALID_ARG, "cfg is NULL");
+  if (c->d_k != kD || c->d_v != kD)
+    return fail(LQ_ERR_UNSUPPORTED, "only d_k = d_v = 128 is built (got d_k=%d d_v=%d)", c->d_k, c->d_v);
+  if (c->dtype != LQ_F32 && c->dtype != LQ_BF16 && c->dtype != LQ_F16)
+    return fail(LQ_ERR_INVALID_ARG, "dtype must be LQ_F32, LQ_BF16 or LQ_F16 (got %d)", c->dtype);
+  if (c->reserved != 0) return fail(LQ_ERR_INVALID_ARG, "reserved must be 0");
+  if (c->heads < 1 || c->heads > 65535 || c->key_heads < 1 || c->heads % c->key_heads != 0)
+    return fail(LQ_ERR_INVALID_ARG, "heads must be 1..65535 and a multiple of key_heads (got %d, %d)", c->heads,
+                c->key_heads);
+  const int64_t per16 = c->dtype == LQ_F32 ? 4 : 8;
+  const int64_t st[4] = {c->q_stride, c->k_stride, c->v_stride, c->o_stride};
+  const char* names[4] = {"q", "k", "v", "o"};
+  for (int i = 0; i < 4; ++i) {
+    const int64_t least = (int64_t)(i < 2 ? c->key_heads : c->heads) * kD;
+    if (st[i] < least || st[i] % per16 != 0 || st[i] > ((int64_t)1 << 40))
+      return fail(LQ_ERR_INVALID_ARG, "%s_stride must be at least %lld and a multiple of 16 bytes (got %lld)", names[i],
+                  (long long)least, (long long)st[i]);
+  }
+  if (c->alpha_stride != 0 && (c->alpha_stride < c->heads || c->alpha_stride > ((int64_t)1 << 40)))
+    return fail(LQ_ERR_INVALID_ARG, "alpha_stride must be 0 or at least heads (got %lld)", (long long)c->alpha_stride);
+  return LQ_OK;
+}
+
+size_t la_size(int32_t dtype) { return dtype == LQ_F32 ? 4 : 2; }
+
+// Bytes from the first element of a strided token array to the end of its last token.
+size_t la_extent(int64_t tokens, int64_t stride, int64_t row, size_t size) {
+  return tokens ? ((size_t)(tokens - 1) * (size_t)stride + (size_t)row) * size : 0;
+}
+
+// The token arrays of a call, on the host: NULL, alignment, and o overlapping an input or a state.
+int check_la_tokens(const lq_la_config* c, int64_t n, const void* q, const void* k, const void* v, const float* alpha,
+                    const void* o) {
+  int rc;
+  if ((rc = check_addr(q, "q", 16)) || (rc = check_addr(k, "k", 16)) || (rc = check_addr(v, "v", 16)) ||
+      (rc = check_addr(alpha, "alpha", 4)) || (rc = check_addr(o, "o", 16)))
+    return rc;
+  const size_t e = la_size(c->dtype);
+  const int64_t kr = (int64_t)c->key_heads * kD, vr = (int64_t)c->heads * kD;
+  const size_t no = la_extent(n, c->o_stride, vr, e);
+  if (overlaps(o, no, q, la_extent(n, c->q_stride, kr, e)) || overlaps(o, no, k, la_extent(n, c->k_stride, kr, e)) ||
+      overlaps(o, no, v, la_extent(n, c->v_stride, vr, e)) ||
+      overlaps(o, no, alpha, la_extent(n, c->alpha_stride, c->heads, 4)))
+    return fail(LQ_ERR_INVALID_ARG, "o overlaps an input");
+  return LQ_OK;
+}
+
+int check_la_device(const lq_la_config*, int dev, const void* q, const void* k, const void* v, const float* alpha,
+                    const void* o) {
+  int rc;
+  if ((rc = check_ptr(q, "q", 16, dev)) || (rc = check_ptr(k, "k", 16, dev)) || (rc = check_ptr(v, "v", 16, dev)) ||
+      (rc = check_ptr(alpha, "alpha", 4, dev)) || (rc = check_ptr(o, "o", 16, dev)))
+    return rc;
+  return LQ_OK;
+}
+
+int check_prompt_sizes(const lq_la_config* c, int64_t n_seqs, int64_t n_tokens, int64_t max_len) {
+  int rc = check_la(c);
+  if (rc) return rc;
+  if (n_seqs < 0 || n_tokens < 0 || n_tokens > 0x7fffffff || max_len < 0)
+    return fail(LQ_ERR_INVALID_ARG, "n_seqs and max_len must not be negative, n_tokens must be 0..%d", 0x7fffffff);
+  if (n_seqs > kMaxStates / 8 / c->heads)
+    return fail(LQ_ERR_INVALID_ARG, "n_seqs x heads must be at most %lld", (long long)(kMaxStates / 8));
+  return LQ_OK;
+}
+
+lqi::LaParams la_params(const lq_la_config* c, const void* q, const void* k, const void* v, const float* alpha,
+                        void* o) {
+  lqi::LaParams p;
+  std::memset(&p, 0, sizeof p);
+  p.heads = c->heads;
+  p.key_heads = c->key_heads;
+  p.group = c->heads / c->key_heads;
+  p.dtype = c->dtype;
+  p.sq = c->q_stride;
+  p.sk = c->k_stride;
+  p.sv = c->v_stride;
+  p.so = c->o_stride;
+  p.sa = c->alpha_stride;
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.alpha = alpha;
+  p.o = o;
+  return p;
+}
+
+size_t la_workspace(const lq_la_config* c, int64_t slots) {
+  return align256((size_t)slots * c->heads * kD * kD * sizeof(float)) + align256((size_t)slots * c->heads * sizeof(float));
+}
+
+int check_beams(int64_t batch, int32_t beams, int64_t vocab, int32_t n_best) {
+  if (batch < 0 || beams < 1 || beams > lqi::kMaxBeams)
+    return fail(LQ_ERR_INVALID_ARG, "batch must not be negative, beams must be 1..%d (got %lld, %d)", lqi::kMaxBeams,
+                (long long)batch, beams);
+  if (vocab < 1 || vocab > 0x7fffffff / beams)
+    return fail(LQ_ERR_INVALID_ARG, "vocab must be 1..(2^31 - 1) / beams (got %lld)", (long long)vocab);
+  if (n_best < 1 || n_best > lqi::kMaxBest || n_best > beams * vocab)
+    return fail(LQ_ERR_INVALID_ARG, "n_best must be 1..%d and at most beams x vocab (got %d)", lqi::kMaxBest, n_best);
+  if (batch > kMaxStates / beams / lqi::beam_splits(LQ_F32, vocab))
+    return fail(LQ_ERR_INVALID_ARG, "batch %lld is too large", (long long)batch);
+  return LQ_OK;
+}
+
+int check_reorder(int64_t n_states, int64_t outer, int64_t groups, int32_t beams, int64_t inner) {
+  int rc = check_n(n_states);
+  if (rc) return rc;
+  if (beams < 1 || beams > lqi::kMaxBeams)
+    return fail(LQ_ERR_INVALID_ARG, "beams must be 1..%d (got %d)", lqi::kMaxBeams, beams);
+  const int64_t f[3] = {outer, groups, inner};
+  int64_t n = beams;
+  for (int64_t x : f) {
+    if (x < 0 || x > kMaxStates) return fail(LQ_ERR_INVALID_ARG, "outer, groups and inner must be 0..%lld",
+                                             (long long)kMaxStates);
+    n = (n > kMaxStates && x) ? n : n * x;  // (stays above the limit once it is; no overflow: both are below 2^31)
+  }
+  if (n != n_states)
+    return fail(LQ_ERR_INVALID_ARG, "outer x groups x beams x inner must be n_states = %lld", (long long)n_states);
+  return LQ_OK;
+}
+
 int launched(cudaError_t e, const char* what) { return e == cudaSuccess ? ok() : cuda_fail(e, what); }
 
 }  // namespace
@@ -546,6 +670,195 @@ int lq_fp32_decode_step(const lq_config* cfg, float* S, int64_t n_states, const 
   p.beta = beta;
   p.o = o;
   return launched(lqi::launch_fp32_step(p, (cudaStream_t)stream), "lq_fp32_decode_step launch");
+}
+
+void lq_la_config_default(lq_la_config* cfg, int32_t heads, int32_t key_heads, int32_t dtype) {
+  if (!cfg) return;
+  std::memset(cfg, 0, sizeof *cfg);
+  cfg->d_k = kD;
+  cfg->d_v = kD;
+  cfg->heads = heads;
+  cfg->key_heads = key_heads;
+  cfg->dtype = dtype;
+  cfg->q_stride = cfg->k_stride = (int64_t)key_heads * kD;
+  cfg->v_stride = cfg->o_stride = (int64_t)heads * kD;
+  cfg->alpha_stride = heads;
+}
+
+size_t lq_la_workspace_bytes(const lq_la_config* cfg, int64_t n_seqs, int64_t n_tokens, int64_t max_len) {
+  if (check_prompt_sizes(cfg, n_seqs, n_tokens, max_len) || n_seqs == 0) return 0;
+  int64_t seg, slots;
+  lqi::la_plan(cfg, n_seqs, n_tokens, max_len, &seg, &slots);
+  return slots ? la_workspace(cfg, slots) : 0;
+}
+
+int lq_la_prefill(const lq_la_config* cfg, int64_t n_seqs, int64_t n_tokens, int64_t max_len,
+                  const int32_t* cu_seqlens, const void* q, const void* k, const void* v, const float* alpha,
+                  const float* S0, float* S_out, void* o, void* workspace, size_t workspace_bytes,
+                  lq_stream_t stream) {
+  int rc = check_prompt_sizes(cfg, n_seqs, n_tokens, max_len);
+  if (rc) return rc;
+  if (n_seqs == 0) return ok();
+  if (!cu_seqlens && n_seqs != 1) return fail(LQ_ERR_INVALID_ARG, "cu_seqlens is NULL with n_seqs > 1");
+  if (!cu_seqlens && max_len > 0 && max_len < n_tokens)
+    return fail(LQ_ERR_INVALID_ARG, "max_len is less than n_tokens, the length of the only sequence");
+  if (cu_seqlens && (rc = check_addr(cu_seqlens, "cu_seqlens", 4))) return rc;
+  if (n_tokens && (rc = check_la_tokens(cfg, n_tokens, q, k, v, alpha, o))) return rc;
+  if (S0 && (rc = check_addr(S0, "S0", 16))) return rc;
+  if (S_out && (rc = check_addr(S_out, "S_out", 16))) return rc;
+  const size_t sb = (size_t)n_seqs * cfg->heads * kD * kD * sizeof(float), e = la_size(cfg->dtype);
+  const size_t nq = la_extent(n_tokens, cfg->q_stride, (int64_t)cfg->key_heads * kD, e);
+  const size_t nk = la_extent(n_tokens, cfg->k_stride, (int64_t)cfg->key_heads * kD, e);
+  const size_t nv = la_extent(n_tokens, cfg->v_stride, (int64_t)cfg->heads * kD, e);
+  const size_t no = la_extent(n_tokens, cfg->o_stride, (int64_t)cfg->heads * kD, e);
+  if (S_out && S_out != S0 && S0 && overlaps(S_out, sb, S0, sb))
+    return fail(LQ_ERR_INVALID_ARG, "S_out overlaps S0 (it may only be S0 itself)");
+  if (S_out && (overlaps(S_out, sb, q, nq) || overlaps(S_out, sb, k, nk) || overlaps(S_out, sb, v, nv) ||
+                overlaps(S_out, sb, o, no) ||
+                overlaps(S_out, sb, alpha, la_extent(n_tokens, cfg->alpha_stride, cfg->heads, 4))))
+    return fail(LQ_ERR_INVALID_ARG, "S_out overlaps a token array");
+  if (S0 && overlaps(S0, sb, o, no)) return fail(LQ_ERR_INVALID_ARG, "o overlaps S0");
+  lqi::LaParams p = la_params(cfg, q, k, v, alpha, o);
+  lqi::la_plan(cfg, n_seqs, n_tokens, max_len, &p.seg, &p.slots);
+  const size_t need = p.slots ? la_workspace(cfg, p.slots) : 0;
+  if (need) {
+    if ((rc = check_addr(workspace, "workspace", 256))) return rc;
+    if (workspace_bytes < need)
+      return fail(LQ_ERR_INVALID_ARG, "workspace has %zu bytes, %zu are needed", workspace_bytes, need);
+    if (overlaps(workspace, need, o, no) || (S_out && overlaps(workspace, need, S_out, sb)) ||
+        (S0 && overlaps(workspace, need, S0, sb)) || overlaps(workspace, need, q, nq) ||
+        overlaps(workspace, need, k, nk) || overlaps(workspace, need, v, nv))
+      return fail(LQ_ERR_INVALID_ARG, "workspace overlaps another argument");
+  }
+  int dev = 0;
+  if ((rc = current_device(&dev)) || (rc = check_stream(stream, dev))) return rc;
+  if (n_tokens && (rc = check_la_device(cfg, dev, q, k, v, alpha, o))) return rc;
+  if ((cu_seqlens && (rc = check_ptr(cu_seqlens, "cu_seqlens", 4, dev))) ||
+      (S0 && (rc = check_ptr(S0, "S0", 16, dev))) || (S_out && (rc = check_ptr(S_out, "S_out", 16, dev))) ||
+      (need && (rc = check_ptr(workspace, "workspace", 256, dev))))
+    return rc;
+  p.n_seqs = n_seqs;
+  p.n_tokens = n_tokens;
+  p.max_len = max_len;
+  p.cu = cu_seqlens;
+  p.S0 = S0;
+  p.S = S_out;
+  p.ws_state = static_cast<float*>(workspace);
+  p.ws_decay = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                        align256((size_t)p.slots * cfg->heads * kD * kD * sizeof(float)));
+  return launched(lqi::launch_la_prefill(p, (cudaStream_t)stream), "lq_la_prefill launch");
+}
+
+int lq_la_decode_step(const lq_la_config* cfg, float* S, int64_t n_seqs, const void* q, const void* k, const void* v,
+                      const float* alpha, void* o, lq_stream_t stream) {
+  int rc = check_prompt_sizes(cfg, n_seqs, n_seqs, 0);
+  if (rc) return rc;
+  if (n_seqs == 0) return ok();
+  if ((rc = check_addr(S, "S", 16)) || (rc = check_la_tokens(cfg, n_seqs, q, k, v, alpha, o))) return rc;
+  const size_t sb = (size_t)n_seqs * cfg->heads * kD * kD * sizeof(float), e = la_size(cfg->dtype);
+  const int64_t kr = (int64_t)cfg->key_heads * kD, vr = (int64_t)cfg->heads * kD;
+  if (overlaps(S, sb, q, la_extent(n_seqs, cfg->q_stride, kr, e)) ||
+      overlaps(S, sb, k, la_extent(n_seqs, cfg->k_stride, kr, e)) ||
+      overlaps(S, sb, v, la_extent(n_seqs, cfg->v_stride, vr, e)) ||
+      overlaps(S, sb, o, la_extent(n_seqs, cfg->o_stride, vr, e)) ||
+      overlaps(S, sb, alpha, la_extent(n_seqs, cfg->alpha_stride, cfg->heads, 4)))
+    return fail(LQ_ERR_INVALID_ARG, "S overlaps a token input or o");
+  int dev = 0;
+  if ((rc = current_device(&dev)) || (rc = check_stream(stream, dev))) return rc;
+  if ((rc = check_ptr(S, "S", 16, dev)) || (rc = check_la_device(cfg, dev, q, k, v, alpha, o))) return rc;
+  lqi::LaParams p = la_params(cfg, q, k, v, alpha, o);
+  p.n_seqs = n_seqs;
+  p.n_tokens = n_seqs;
+  p.S = S;
+  return launched(lqi::launch_la_step(p, (cudaStream_t)stream), "lq_la_decode_step launch");
+}
+
+size_t lq_beam_workspace_bytes(int64_t batch, int32_t beams, int64_t vocab, int32_t n_best) {
+  if (check_beams(batch, beams, vocab, n_best) || batch == 0) return 0;
+  return lqi::beam_workspace(batch, beams, vocab, n_best);
+}
+
+int lq_beam_select(int32_t dtype, int64_t batch, int32_t beams, int64_t vocab, int32_t n_best, const void* logits,
+                   int64_t row_stride, const float* scores, float* out_scores, int32_t* out_parent,
+                   int32_t* out_token, void* workspace, size_t workspace_bytes, lq_stream_t stream) {
+  if (dtype != LQ_F32 && dtype != LQ_BF16 && dtype != LQ_F16)
+    return fail(LQ_ERR_INVALID_ARG, "dtype must be LQ_F32, LQ_BF16 or LQ_F16 (got %d)", dtype);
+  int rc = check_beams(batch, beams, vocab, n_best);
+  if (rc) return rc;
+  if (batch == 0) return ok();
+  if (row_stride < vocab || row_stride > ((int64_t)1 << 40))
+    return fail(LQ_ERR_INVALID_ARG, "row_stride must be at least vocab (got %lld)", (long long)row_stride);
+  const size_t e = la_size(dtype);
+  if ((rc = check_addr(logits, "logits", e)) || (rc = check_addr(scores, "scores", 4)) ||
+      (rc = check_addr(out_scores, "out_scores", 4)) || (rc = check_addr(out_parent, "out_parent", 4)) ||
+      (rc = check_addr(out_token, "out_token", 4)) || (rc = check_addr(workspace, "workspace", 256)))
+    return rc;
+  const size_t need = lqi::beam_workspace(batch, beams, vocab, n_best);
+  if (workspace_bytes < need)
+    return fail(LQ_ERR_INVALID_ARG, "workspace has %zu bytes, %zu are needed", workspace_bytes, need);
+  const size_t nl = la_extent(batch * beams, row_stride, vocab, e), ns = (size_t)batch * beams * 4,
+               no = (size_t)batch * n_best * 4;
+  const void* out[4] = {out_scores, out_parent, out_token, workspace};
+  const size_t nout[4] = {no, no, no, need};
+  for (int i = 0; i < 4; ++i) {
+    if (overlaps(out[i], nout[i], logits, nl) || overlaps(out[i], nout[i], scores, ns))
+      return fail(LQ_ERR_INVALID_ARG, "an output or the workspace overlaps an input");
+    for (int j = 0; j < i; ++j)
+      if (overlaps(out[i], nout[i], out[j], nout[j]))
+        return fail(LQ_ERR_INVALID_ARG, "the outputs and the workspace overlap");
+  }
+  int dev = 0;
+  if ((rc = current_device(&dev)) || (rc = check_stream(stream, dev))) return rc;
+  if ((rc = check_ptr(logits, "logits", e, dev)) || (rc = check_ptr(scores, "scores", 4, dev)) ||
+      (rc = check_ptr(out_scores, "out_scores", 4, dev)) || (rc = check_ptr(out_parent, "out_parent", 4, dev)) ||
+      (rc = check_ptr(out_token, "out_token", 4, dev)) || (rc = check_ptr(workspace, "workspace", 256, dev)))
+    return rc;
+  lqi::BeamParams p;
+  std::memset(&p, 0, sizeof p);
+  p.dtype = dtype;
+  p.beams = beams;
+  p.n_best = n_best;
+  p.splits = lqi::beam_splits(dtype, vocab);
+  p.batch = batch;
+  p.vocab = vocab;
+  p.row_stride = row_stride;
+  p.logits = logits;
+  p.scores = scores;
+  p.out_scores = out_scores;
+  p.out_parent = out_parent;
+  p.out_token = out_token;
+  p.ws = workspace;
+  return launched(lqi::launch_beam_select(p, (cudaStream_t)stream), "lq_beam_select launch");
+}
+
+int lq_state_reorder(const lq_config* cfg, void* state, int64_t n_states, int64_t outer, int64_t groups,
+                     int32_t beams, int64_t inner, const int32_t* parent, lq_stream_t stream) {
+  int rc = check_cfg(cfg);
+  if (rc || (rc = check_reorder(n_states, outer, groups, beams, inner))) return rc;
+  if (n_states == 0) return ok();
+  if ((rc = check_addr(state, "state", 256)) || (rc = check_addr(parent, "parent", 4))) return rc;
+  if (overlaps(parent, (size_t)groups * beams * 4, state, state_size(cfg, n_states)))
+    return fail(LQ_ERR_INVALID_ARG, "parent overlaps the state buffer");
+  int dev = 0;
+  if ((rc = check_common(cfg, state, n_states, stream, &dev)) || (rc = check_ptr(parent, "parent", 4, dev))) return rc;
+  Params p = make_params(cfg, state, n_states);
+  const lqi::ReorderParams r = {outer, groups, inner, beams, parent};
+  return launched(lqi::launch_reorder(p, r, (cudaStream_t)stream), "lq_state_reorder launch");
+}
+
+int lq_fp32_state_reorder(float* S, int64_t n_states, int64_t outer, int64_t groups, int32_t beams, int64_t inner,
+                          const int32_t* parent, lq_stream_t stream) {
+  int rc = check_reorder(n_states, outer, groups, beams, inner);
+  if (rc) return rc;
+  if (n_states == 0) return ok();
+  if ((rc = check_addr(S, "S", 16)) || (rc = check_addr(parent, "parent", 4))) return rc;
+  if (overlaps(parent, (size_t)groups * beams * 4, S, (size_t)n_states * kD * kD * sizeof(float)))
+    return fail(LQ_ERR_INVALID_ARG, "parent overlaps S");
+  int dev = 0;
+  if ((rc = current_device(&dev)) || (rc = check_stream(stream, dev))) return rc;
+  if ((rc = check_ptr(S, "S", 16, dev)) || (rc = check_ptr(parent, "parent", 4, dev))) return rc;
+  const lqi::ReorderParams r = {outer, groups, inner, beams, parent};
+  return launched(lqi::launch_fp32_reorder(S, r, (cudaStream_t)stream), "lq_fp32_state_reorder launch");
 }
 
 int lq_get_status(const void* state, int64_t* bad_state, lq_stream_t stream) {

@@ -109,6 +109,56 @@ struct Fp32Params {
   float* o;
 };
 
+// Linear attention with a decay per head (lq_la_prefill, lq_la_decode_step).
+constexpr int kMaxBeams = 32;
+constexpr int kMaxBest = 64;
+
+struct LaParams {
+  int heads, key_heads, group;  // group: heads per key head
+  int dtype;
+  int64_t sq, sk, sv, so, sa;  // elements between tokens
+  int64_t n_seqs, n_tokens, max_len;
+  int64_t seg;        // tokens per segment of a split sequence; 0: sequences are not split
+  int64_t slots;      // upper bound of the segments of all sequences
+  const int32_t* cu;  // NULL: one sequence of n_tokens
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* alpha;
+  const float* S0;
+  float* S;  // prefill: final states (may be NULL); decode step: states, in place
+  void* o;
+  float* ws_state;  // [slots][heads][128][128]: what a segment adds to the state
+  float* ws_decay;  // [slots][heads]: the product of a segment's decays
+};
+
+struct BeamParams {
+  int dtype, beams, n_best, splits;
+  int64_t batch, vocab, row_stride;
+  const void* logits;
+  const float* scores;
+  float* out_scores;
+  int32_t* out_parent;
+  int32_t* out_token;
+  void* ws;
+};
+
+struct ReorderParams {
+  int64_t outer, groups, inner;
+  int beams;
+  const int32_t* parent;
+};
+
+// Tokens per segment (0: whole sequences) and the segments there can be, by size.
+void la_plan(const lq_la_config* c, int64_t n_seqs, int64_t n_tokens, int64_t max_len, int64_t* seg, int64_t* slots);
+size_t beam_workspace(int64_t batch, int beams, int64_t vocab, int n_best);
+int beam_splits(int dtype, int64_t vocab);
+
+cudaError_t launch_la_prefill(const LaParams& p, cudaStream_t st);
+cudaError_t launch_la_step(const LaParams& p, cudaStream_t st);
+cudaError_t launch_beam_select(const BeamParams& p, cudaStream_t st);
+cudaError_t launch_reorder(const Params& p, const ReorderParams& r, cudaStream_t st);
+cudaError_t launch_fp32_reorder(float* S, const ReorderParams& r, cudaStream_t st);
 cudaError_t launch_init(const Params& p, cudaStream_t st);
 cudaError_t launch_append(const Params& p, cudaStream_t st);
 cudaError_t launch_append_slist(const Params& p, cudaStream_t st);

@@ -23,15 +23,19 @@ ERR_CUDA = -4
 ERR_TIMEOUT = -5
 ERR_PHASE = -6
 ERR_STATE = -7
+ERR_PARENT = -8
+
+F32, BF16, F16 = 0, 1, 2  # lq_dtype
 
 STATUS_NAMES = {0: "LQ_OK", -1: "LQ_ERR_INVALID_ARG", -2: "LQ_ERR_UNSUPPORTED", -3: "LQ_ERR_WINDOW_FULL",
-                -4: "LQ_ERR_CUDA", -5: "LQ_ERR_TIMEOUT", -6: "LQ_ERR_PHASE", -7: "LQ_ERR_STATE"}
+                -4: "LQ_ERR_CUDA", -5: "LQ_ERR_TIMEOUT", -6: "LQ_ERR_PHASE", -7: "LQ_ERR_STATE", -8: "LQ_ERR_PARENT"}
 
 # Every symbol include/lq.h declares.
 EXPORTS = ("lq_config_default", "lq_state_bytes", "lq_layout", "lq_state_init", "lq_state_init_range", "lq_append",
            "lq_fold", "lq_decode_step", "lq_decode_step_noalloc", "lq_decode_step2", "lq_decode_step_rwkv7", "lq_export_state",
-           "lq_fp32_decode_step", "lq_get_status", "lq_clear_status", "lq_last_error", "lq_version",
-           "lq_debug_set_wait")
+           "lq_fp32_decode_step", "lq_la_config_default", "lq_la_workspace_bytes", "lq_la_prefill", "lq_la_decode_step",
+           "lq_beam_workspace_bytes", "lq_beam_select", "lq_state_reorder", "lq_fp32_state_reorder", "lq_get_status",
+           "lq_clear_status", "lq_last_error", "lq_version", "lq_debug_set_wait")
 
 
 class Config(ctypes.Structure):
@@ -47,6 +51,11 @@ class Layout(ctypes.Structure):
                                                 "full_list")] + \
                [("comp_id_stride", ctypes.c_int64), ("alpha_stride", ctypes.c_int64),
                 ("boundary_bytes_per_state", ctypes.c_int64)]
+
+
+class LaConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("d_k", "d_v", "heads", "key_heads", "dtype", "reserved")] + \
+               [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride", "o_stride", "alpha_stride")]
 
 
 class LQError(RuntimeError):
@@ -88,6 +97,15 @@ def load():
         "lq_decode_step_rwkv7": (ctypes.c_int, [cfgp, P, i64, i32, P, P, P, P, P, P, P, P]),
         "lq_export_state": (ctypes.c_int, [cfgp, P, i64, P, P]),
         "lq_fp32_decode_step": (ctypes.c_int, [cfgp, P, i64, P, P, P, P, P, P, P]),
+        "lq_la_config_default": (None, [ctypes.POINTER(LaConfig), i32, i32, i32]),
+        "lq_la_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(LaConfig), i64, i64, i64]),
+        "lq_la_prefill": (ctypes.c_int, [ctypes.POINTER(LaConfig), i64, i64, i64, P, P, P, P, P, P, P, P, P,
+                                         ctypes.c_size_t, P]),
+        "lq_la_decode_step": (ctypes.c_int, [ctypes.POINTER(LaConfig), P, i64, P, P, P, P, P, P]),
+        "lq_beam_workspace_bytes": (ctypes.c_size_t, [i64, i32, i64, i32]),
+        "lq_beam_select": (ctypes.c_int, [i32, i64, i32, i64, i32, P, i64, P, P, P, P, P, ctypes.c_size_t, P]),
+        "lq_state_reorder": (ctypes.c_int, [cfgp, P, i64, i64, i64, i32, i64, P, P]),
+        "lq_fp32_state_reorder": (ctypes.c_int, [P, i64, i64, i64, i32, i64, P, P]),
         "lq_get_status": (ctypes.c_int, [P, ctypes.POINTER(ctypes.c_int64), P]),
         "lq_clear_status": (ctypes.c_int, [P, P]),
         "lq_last_error": (ctypes.c_char_p, []),
@@ -239,6 +257,146 @@ def fp32_decode_step(cfg, S, n_states, q, k, v, alpha, beta, o, stream=None):
     _check(load().lq_fp32_decode_step(ctypes.byref(cfg), _ptr(S, "S", f), n_states, _ptr(q, "q", f), _ptr(k, "k", f),
                                       _ptr(v, "v", f), _ptr(alpha, "alpha", f), _ptr(beta, "beta", f),
                                       _ptr(o, "o", f), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------- generation
+def _dtype_id(dtype):
+    import torch
+
+    ids = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+    if dtype not in ids:
+        raise ValueError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
+    return ids[dtype]
+
+
+def la_config(heads, key_heads=None, dtype=None) -> LaConfig:
+    """Head layout and token type (bfloat16 unless given) of linear attention with a decay per head."""
+    if dtype is None:
+        import torch
+
+        dtype = torch.bfloat16
+    c = LaConfig()
+    load().lq_la_config_default(ctypes.byref(c), int(heads), int(heads if key_heads is None else key_heads),
+                                _dtype_id(dtype))
+    return c
+
+
+def la_workspace_bytes(cfg: LaConfig, n_seqs: int, n_tokens: int, max_len: int = 0) -> int:
+    return int(load().lq_la_workspace_bytes(ctypes.byref(cfg), n_seqs, n_tokens, max_len))
+
+
+def _rows(t, name, heads, tid):
+    """(address, token stride) of a token array [tokens][heads][128] whose tokens may lie apart."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if _dtype_id(t.dtype) != tid:
+        raise ValueError(f"{name} must have the configuration's dtype, got {t.dtype}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != 128:
+        raise ValueError(f"{name} must be [tokens][{heads}][128], got {tuple(shape)}")
+    if shape[0] and (stride[2] != 1 or (heads > 1 and stride[1] != 128)):
+        raise ValueError(f"{name}: a token's heads and channels must be contiguous")
+    return t.data_ptr(), (stride[0] if shape[0] > 1 else heads * 128), shape[0]
+
+
+def _la_tokens(cfg, q, k, v, alpha, o):
+    """Addresses of the token arrays and a copy of cfg with their strides."""
+    c = LaConfig.from_buffer_copy(cfg)
+    pq, c.q_stride, n = _rows(q, "q", c.key_heads, c.dtype)
+    pk, c.k_stride, nk = _rows(k, "k", c.key_heads, c.dtype)
+    pv, c.v_stride, nv = _rows(v, "v", c.heads, c.dtype)
+    po, c.o_stride, no = _rows(o, "o", c.heads, c.dtype)
+    if not (n == nk == nv == no):
+        raise ValueError(f"q, k, v and o must have the same number of tokens, got {n}, {nk}, {nv}, {no}")
+    if not alpha.is_cuda or alpha.dtype != _f32():
+        raise ValueError("alpha must be a float32 CUDA tensor")
+    shape, stride = alpha.shape, alpha.stride()
+    if len(shape) != 2 or shape[0] != n or shape[1] != c.heads or (c.heads > 1 and n and stride[1] != 1):
+        raise ValueError(f"alpha must be [{n}][{c.heads}] with contiguous heads, got {tuple(shape)}")
+    c.alpha_stride = stride[0] if n > 1 else c.heads
+    return c, pq, pk, pv, alpha.data_ptr(), po, n
+
+
+def la_prefill(cfg: LaConfig, q, k, v, alpha, o, cu_seqlens=None, max_len=0, S0=None, S_out=None, workspace=None,
+               stream=None):
+    """Linear attention over packed prompts: q, k [tokens][key_heads][128], v, o [tokens][heads][128] (strided
+    tokens allowed), alpha fp32 [tokens][heads] (``expand`` a [heads] vector for fixed decays), cu_seqlens int32
+    [n_seqs + 1] on the device (None: one sequence), S0, S_out fp32 [n_seqs][heads][128][128]. workspace:
+    uint8 tensor of ``la_workspace_bytes``."""
+    import torch
+
+    c, pq, pk, pv, pa, po, n = _la_tokens(cfg, q, k, v, alpha, o)
+    n_seqs = 1 if cu_seqlens is None else cu_seqlens.numel() - 1
+    for t, name in ((S0, "S0"), (S_out, "S_out")):
+        if t is not None and t.numel() != n_seqs * c.heads * 128 * 128:
+            raise ValueError(f"{name} must be [{n_seqs}][{c.heads}][128][128], got {tuple(t.shape)}")
+    _check(load().lq_la_prefill(ctypes.byref(c), n_seqs, n, int(max_len), _ptr(cu_seqlens, "cu_seqlens", torch.int32),
+                                pq, pk, pv, pa, _ptr(S0, "S0", torch.float32), _ptr(S_out, "S_out", torch.float32),
+                                po, _ptr(workspace, "workspace"), 0 if workspace is None else workspace.nbytes,
+                                _stream(stream)))
+
+
+def la_decode_step(cfg: LaConfig, S, q, k, v, alpha, o, stream=None):
+    """One token for each sequence on fp32 states S [n_seqs][heads][128][128], in place; token arrays as
+    ``la_prefill`` with one token per sequence."""
+    c, pq, pk, pv, pa, po, n = _la_tokens(cfg, q, k, v, alpha, o)
+    if S.numel() != n * c.heads * 128 * 128:
+        raise ValueError(f"S must be [{n}][{c.heads}][128][128], got {tuple(S.shape)}")
+    _check(load().lq_la_decode_step(ctypes.byref(c), _ptr(S, "S", _f32()), n, pq, pk, pv, pa, po, _stream(stream)))
+
+
+def beam_workspace_bytes(batch: int, beams: int, vocab: int, n_best: int) -> int:
+    return int(load().lq_beam_workspace_bytes(batch, beams, vocab, n_best))
+
+
+def beam_select(logits, scores, out_scores, out_parent, out_token, workspace, stream=None):
+    """The n_best = out_scores.shape[1] continuations of each request: logits [batch][beams][vocab] (rows may be
+    padded), scores fp32 [batch][beams]; out_scores fp32, out_parent and out_token int32 [batch][n_best].
+    workspace: uint8 tensor of ``beam_workspace_bytes``."""
+    import torch
+
+    batch, beams, vocab = logits.shape
+    s0, s1, s2 = logits.stride()
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
+    if beams == 1:
+        s1 = s0 if batch > 1 else max(vocab, 1)
+    if logits.numel() and (s2 != 1 and vocab > 1 or batch > 1 and s0 != beams * s1):
+        raise ValueError("logits: a row must be contiguous and all rows evenly spaced")
+    n_best = out_scores.shape[1]
+    if tuple(scores.shape) != (batch, beams):
+        raise ValueError(f"scores must be [{batch}][{beams}], got {tuple(scores.shape)}")
+    for t, name in ((out_scores, "out_scores"), (out_parent, "out_parent"), (out_token, "out_token")):
+        if tuple(t.shape) != (batch, n_best):
+            raise ValueError(f"{name} must be [{batch}][{n_best}], got {tuple(t.shape)}")
+    f, i = torch.float32, torch.int32
+    _check(load().lq_beam_select(_dtype_id(logits.dtype), batch, beams, vocab, n_best, logits.data_ptr(), s1,
+                                 _ptr(scores, "scores", f), _ptr(out_scores, "out_scores", f),
+                                 _ptr(out_parent, "out_parent", i), _ptr(out_token, "out_token", i),
+                                 _ptr(workspace, "workspace"), workspace.nbytes, _stream(stream)))
+
+
+def _parents(parent):
+    import torch
+
+    if parent.dim() != 2:
+        raise ValueError(f"parent must be [groups][beams], got {tuple(parent.shape)}")
+    return _ptr(parent, "parent", torch.int32), parent.shape[0], parent.shape[1]
+
+
+def state_reorder(cfg: Config, state, n_states, parent, outer=1, inner=1, stream=None):
+    """Head-states follow the chosen hypotheses, in place: head-state ((x * groups + g) * beams + b) * inner + i
+    takes what beam parent[g][b] held (x < outer, i < inner); parent int32 [groups][beams]."""
+    p, groups, beams = _parents(parent)
+    _check(load().lq_state_reorder(ctypes.byref(cfg), _ptr(state, "state"), n_states, outer, groups, beams, inner, p,
+                                   _stream(stream)))
+
+
+def fp32_state_reorder(S, parent, outer=1, inner=1, stream=None):
+    """``state_reorder`` for fp32 states S [n_states][128][128] (any leading shape)."""
+    p, groups, beams = _parents(parent)
+    _check(load().lq_fp32_state_reorder(_ptr(S, "S", _f32()), S.numel() // (128 * 128), outer, groups, beams, inner, p,
+                                        _stream(stream)))
 
 
 def get_status(state, stream=None):
