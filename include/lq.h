@@ -348,8 +348,8 @@ void lq_la_config_default(lq_la_config* cfg, int32_t heads, int32_t key_heads, i
 /*
  * Bytes of workspace lq_la_prefill needs for n_seqs sequences with n_tokens tokens
  * in all, the longest of max_len (0: not known); 0 when it needs none or when an
- * argument is invalid. Host only. Up to 64 KB per head and segment of a sequence
- * that is split; the call never needs more for fewer tokens at the same max_len.
+ * argument is invalid. Host only. It needs some where sequences may be split: 64 KB
+ * per head and segment, and 64 KB per head and sequence.
  */
 size_t lq_la_workspace_bytes(const lq_la_config* cfg, int64_t n_seqs, int64_t n_tokens, int64_t max_len);
 

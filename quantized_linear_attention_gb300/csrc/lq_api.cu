@@ -367,8 +367,11 @@ lqi::LaParams la_params(const lq_la_config* c, const void* q, const void* k, con
   return p;
 }
 
-size_t la_workspace(const lq_la_config* c, int64_t slots) {
-  return align256((size_t)slots * c->heads * kD * kD * sizeof(float)) + align256((size_t)slots * c->heads * sizeof(float));
+// Split sequences: what each segment adds to the state, its decay, and the last states where they replace S0.
+size_t la_workspace(const lq_la_config* c, int64_t n_seqs, int64_t slots) {
+  return align256((size_t)slots * c->heads * kD * kD * sizeof(float)) +
+         align256((size_t)slots * c->heads * sizeof(double)) +
+         align256((size_t)n_seqs * c->heads * kD * kD * sizeof(float));
 }
 
 int check_beams(int64_t batch, int32_t beams, int64_t vocab, int32_t n_best) {
@@ -689,7 +692,7 @@ size_t lq_la_workspace_bytes(const lq_la_config* cfg, int64_t n_seqs, int64_t n_
   if (check_prompt_sizes(cfg, n_seqs, n_tokens, max_len) || n_seqs == 0) return 0;
   int64_t seg, slots;
   lqi::la_plan(cfg, n_seqs, n_tokens, max_len, &seg, &slots);
-  return slots ? la_workspace(cfg, slots) : 0;
+  return slots ? la_workspace(cfg, n_seqs, slots) : 0;
 }
 
 int lq_la_prefill(const lq_la_config* cfg, int64_t n_seqs, int64_t n_tokens, int64_t max_len,
@@ -720,7 +723,7 @@ int lq_la_prefill(const lq_la_config* cfg, int64_t n_seqs, int64_t n_tokens, int
   if (S0 && overlaps(S0, sb, o, no)) return fail(LQ_ERR_INVALID_ARG, "o overlaps S0");
   lqi::LaParams p = la_params(cfg, q, k, v, alpha, o);
   lqi::la_plan(cfg, n_seqs, n_tokens, max_len, &p.seg, &p.slots);
-  const size_t need = p.slots ? la_workspace(cfg, p.slots) : 0;
+  const size_t need = p.slots ? la_workspace(cfg, n_seqs, p.slots) : 0;
   if (need) {
     if ((rc = check_addr(workspace, "workspace", 256))) return rc;
     if (workspace_bytes < need)
@@ -743,9 +746,12 @@ int lq_la_prefill(const lq_la_config* cfg, int64_t n_seqs, int64_t n_tokens, int
   p.cu = cu_seqlens;
   p.S0 = S0;
   p.S = S_out;
-  p.ws_state = static_cast<float*>(workspace);
-  p.ws_decay = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                        align256((size_t)p.slots * cfg->heads * kD * kD * sizeof(float)));
+  char* ws = static_cast<char*>(workspace);
+  p.ws_state = reinterpret_cast<float*>(ws);
+  ws += align256((size_t)p.slots * cfg->heads * kD * kD * sizeof(float));
+  p.ws_decay = reinterpret_cast<double*>(ws);
+  ws += align256((size_t)p.slots * cfg->heads * sizeof(double));
+  p.ws_last = reinterpret_cast<float*>(ws);
   return launched(lqi::launch_la_prefill(p, (cudaStream_t)stream), "lq_la_prefill launch");
 }
 

@@ -129,7 +129,8 @@ struct LaParams {
   float* S;  // prefill: final states (may be NULL); decode step: states, in place
   void* o;
   float* ws_state;  // [slots][heads][128][128]: what a segment adds to the state
-  float* ws_decay;  // [slots][heads]: the product of a segment's decays
+  double* ws_decay; // [slots][heads]: the product of a segment's decays
+  float* ws_last;   // [n_seqs][heads][128][128]: last states on their way into S where that is S0
 };
 
 struct BeamParams {
@@ -150,6 +151,7 @@ struct ReorderParams {
 };
 
 // Tokens per segment (0: whole sequences) and the segments there can be, by size.
+// (Fewer tokens at the same max_len never need more.)
 void la_plan(const lq_la_config* c, int64_t n_seqs, int64_t n_tokens, int64_t max_len, int64_t* seg, int64_t* slots);
 size_t beam_workspace(int64_t batch, int beams, int64_t vocab, int n_best);
 int beam_splits(int dtype, int64_t vocab);

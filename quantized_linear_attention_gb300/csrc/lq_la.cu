@@ -7,57 +7,11 @@
 #include <stdint.h>
 
 #include "lq_internal.h"
+#include "lq_la.cuh"
 
 namespace lqi {
 
 namespace {
-
-template <typename T>
-__device__ __forceinline__ float to_f(T x);
-template <>
-__device__ __forceinline__ float to_f(float x) { return x; }
-template <>
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <>
-__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
-
-// One rounding, to nearest even, of an fp32 sum to the type of the tokens.
-template <typename T>
-__device__ __forceinline__ T from_f(float x);
-template <>
-__device__ __forceinline__ float from_f(float x) { return x; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f(float x) { return __float2bfloat16_rn(x); }
-template <>
-__device__ __forceinline__ __half from_f(float x) { return __float2half_rn(x); }
-
-// Four consecutive channels as floats.
-__device__ __forceinline__ void ld4(const float* p, float d[4]) {
-  const float4 x = *reinterpret_cast<const float4*>(p);
-  d[0] = x.x, d[1] = x.y, d[2] = x.z, d[3] = x.w;
-}
-template <typename T>
-__device__ __forceinline__ void ld4(const T* p, float d[4]) {
-  const uint2 x = *reinterpret_cast<const uint2*>(p);
-  T t[4];
-  static_assert(sizeof(T) == 2, "16-bit tokens");
-  memcpy(t, &x, 8);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) d[e] = to_f(t[e]);
-}
-
-// The bounds of sequence b; one whose bounds are not 0 <= begin <= end <= n_tokens,
-// or that is longer than a stated max_len, counts as empty.
-__device__ __forceinline__ void bounds(const LaParams& p, int64_t b, int64_t& begin, int64_t& len) {
-  begin = 0;
-  int64_t end = p.n_tokens;
-  if (p.cu) {
-    begin = p.cu[b];
-    end = p.cu[b + 1];
-  }
-  len = end - begin;
-  if (begin < 0 || end > p.n_tokens || len < 0 || (p.max_len > 0 && len > p.max_len)) begin = len = 0;
-}
 
 // --------------------------------------------------------------------------------------------
 // Prompts, token by token: one CTA of 128 threads per (sequence, head, 32 value
@@ -194,10 +148,21 @@ cudaError_t step(const LaParams& p, cudaStream_t st) {
 
 }  // namespace
 
-void la_plan(const lq_la_config*, int64_t, int64_t, int64_t, int64_t* seg, int64_t* slots) { *seg = *slots = 0; }
+void la_plan(const lq_la_config* c, int64_t n_seqs, int64_t n_tokens, int64_t max_len, int64_t* seg, int64_t* slots) {
+  *seg = *slots = 0;
+  if (c->dtype != LQ_BF16) return;
+  const int64_t longest = max_len > 0 && max_len < n_tokens ? max_len : n_tokens;
+  const int64_t share = n_tokens * c->heads / 152;  // head-tokens of an SM
+  // Splitting reads k and v twice (1.5 times the bytes), so it pays where the longest
+  // sequence alone takes longer than that: 1.6 shares.
+  if (5 * longest <= 8 * share || longest <= 1024) return;
+  *seg = (share / 4 + 127) / 128 * 128;
+  if (*seg < 512) *seg = 512;
+  *slots = n_tokens / *seg + n_seqs;
+}
 
 cudaError_t launch_la_prefill(const LaParams& p, cudaStream_t st) {
-  if (p.dtype == LQ_BF16) return prefill<__nv_bfloat16>(p, st);
+  if (p.dtype == LQ_BF16) return launch_la_chunk_bf16(p, st);
   if (p.dtype == LQ_F16) return prefill<__half>(p, st);
   return prefill<float>(p, st);
 }
