@@ -294,7 +294,7 @@ int check_la(const lq_la_config* c) {
   const char* names[4] = {"q", "k", "v", "o"};
   for (int i = 0; i < 4; ++i) {
     const int64_t least = (int64_t)(i < 2 ? c->key_heads : c->heads) * kD;
-    if (st[i] < least || st[i] % per16 != 0 || st[i] > ((int64_t)1 << 40))
+    if (st[i] < least || st[i] % per16 != 0 || st[i] > ((int64_t)1 << 38))
       return fail(LQ_ERR_INVALID_ARG, "%s_stride must be at least %lld and a multiple of 16 bytes (got %lld)", names[i],
                   (long long)least, (long long)st[i]);
   }

@@ -19,13 +19,15 @@
 // same direction chunk after chunk. Sums of logarithms are whole numbers of 2^-40.
 //
 // Warps: 0-7 weigh P, scale O and write o (A); 8-15 keep the state and make
-// the parts of wV (B); 16-17 copy tiles (even and odd chunks); 18 sums the
-// logarithms; 19 issues the products. They meet at mbarriers only. Every wait is
-// bounded; one that gives up ends the CTA's work, and the outputs become NaN.
+// the parts of wV (B); 16 copies tiles in and out (TMA); 17 and 18 sum the logarithms
+// (even and odd chunks); 19 issues the products. They meet at mbarriers only. Every wait is bounded; one that gives up
+// ends the CTA's work, and the outputs become NaN.
 //
-// A masked product cannot hold back 0 x inf: where a chunk's values are not all
-// finite, or a decay is not in [0, 1], the CTA takes its tokens again one by one
-// (redo), exactly as the recurrence is written.
+// A masked product cannot hold back 0 x inf: where the state comes out not finite
+// (any value or key that is not makes it so), or a decay is not in [0, 1], the CTA
+// takes its tokens again one by one (redo), exactly as the recurrence is written.
+#include <cuda.h>
+
 #include "lq_device.cuh"
 #include "lq_la.cuh"
 
@@ -47,10 +49,10 @@ constexpr uint32_t kU = 0, kP = 128, kO = 256, kV3 = 384;  // kV3: two buffers o
 
 struct Misc {
   float2 gamma[4];
-  uint64_t full[2], empty[2], sums[2], qk, qs, pv, pvok, ofree, sready, vfull[2], vfree[2], drain;
+  uint64_t land[2], full[2], empty[2], sums[2], oready[2], qk, qs, pv, pvok, ofree, sready, vfull[2], vfree[2], drain;
   uint32_t tmem;
   int abort, flag;
-  double prod;
+  double prod[2];
   int64_t piece[5];
 };
 static_assert(sizeof(Misc) <= 512, "misc");
@@ -134,6 +136,16 @@ __device__ __forceinline__ void arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Waits for phase `parity`; false once this or any other wait of the CTA has given up.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -154,8 +166,19 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* a
   return __all_sync(0xffffffffu, wait(bar, parity, abort));
 }
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+// 128 tokens x 64 channels into half a tile; tokens past the tensor's end are zeros. x is a multiple of 64.
+__device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, int x, int t, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
+          "r"(dst),
+      "l"(map), "r"(x), "r"(t), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int t, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x),
+               "r"(t), "r"(src)
+               : "memory");
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -163,13 +186,29 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ uint32_t lds_u16(uint32_t a) {
+  uint16_t x;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(a) : "memory");
+  return x;
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {  // to nearest
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 
+// A product of two numbers in two parts each (high + low), to about 2^-45.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  const float p = __fmul_rn(a.x, b.x);
+  const float e = __fmaf_rn(a.y, b.x, __fmaf_rn(a.x, b.y, __fmaf_rn(a.x, b.x, -p)));
+  const float h = __fadd_rn(p, e);
+  return make_float2(h, __fsub_rn(e, __fsub_rn(h, p)));
+}
+
 using bf16 = __nv_bfloat16;
+using PFN_encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 // The state before segment i, columns [c0, c0 + 16) of row `row`: S0 (or zero), then what segments 0..i-1 added.
 __device__ __forceinline__ void start_state(const LaParams& p, const Piece& pc, int64_t slot, int h, int row, int c0,
@@ -274,7 +313,9 @@ __device__ __noinline__ void redo(const LaParams& p, const Piece& pc, int64_t sl
 
 // OUT: outputs and last states. Otherwise the first pass over split sequences: what a segment adds to the state.
 template <bool OUT>
-__global__ void __launch_bounds__(kThreadsLa, 1) k_la_chunk(LaParams p) {
+__global__ void __launch_bounds__(kThreadsLa, 1)
+    k_la_chunk(LaParams p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+               const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo) {
   extern __shared__ __align__(1024) char la_smem[];
   Misc& ms = *reinterpret_cast<Misc*>(la_smem + kMisc);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -301,10 +342,12 @@ __global__ void __launch_bounds__(kThreadsLa, 1) k_la_chunk(LaParams p) {
   }
   if (tid == 32) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ms.full[i], 32);
+      mbar_init(&ms.land[i], 1);
+      mbar_init(&ms.full[i], 1);
       mbar_init(&ms.empty[i], 1);
       mbar_init(&ms.sums[i], 32);
-      mbar_init(&ms.vfull[i], 256);
+      mbar_init(&ms.oready[i], 256);
+      mbar_init(&ms.vfull[i], 128);
       mbar_init(&ms.vfree[i], 1);
     }
     mbar_init(&ms.qk, 1);
@@ -315,7 +358,7 @@ __global__ void __launch_bounds__(kThreadsLa, 1) k_la_chunk(LaParams p) {
     mbar_init(&ms.sready, 256);
     mbar_init(&ms.drain, 1);
     ms.abort = ms.flag = 0;
-    ms.prod = 1.0;
+    ms.prod[0] = ms.prod[1] = 1.0;
   }
   tc_before();
   __syncthreads();
@@ -393,11 +436,22 @@ __global__ void __launch_bounds__(kThreadsLa, 1) k_la_chunk(LaParams p) {
         }
         tc_before();
         arrive(&ms.ofree);
-        const int64_t t = (int64_t)c * kC + i;
-        if (t < pc.len) {
-          uint4* dst = reinterpret_cast<uint4*>(o + (pc.begin + t) * p.so);
+        // o goes out by way of Q's tile, which nothing reads any more: rows of 128 bytes, swizzled as Q's were
+        char* tile = la_smem + (c & 1) * kStage + half * 16384;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) dst[e] = make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+        for (int e = 0; e < 8; ++e)
+          *reinterpret_cast<uint4*>(tile + i * 128 + ((e ^ (i & 7)) << 4)) =
+              make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+        const int n = (int)min((int64_t)kC, pc.len - (int64_t)c * kC);
+        if (n == kC) {
+          fence_proxy_async();
+          arrive(&ms.oready[c & 1]);
+        } else {  // the rows past the end are not this sequence's: each warp writes those of its 32 that are
+          __syncwarp();
+          const int e = lane & 7;
+          for (int r = 32 * quad + (lane >> 3); r < min(n, 32 * quad + 32); r += 4)
+            *reinterpret_cast<uint4*>(o + (pc.begin + (int64_t)c * kC + r) * p.so + 8 * e) =
+                *reinterpret_cast<const uint4*>(tile + r * 128 + ((e ^ (r & 7)) << 4));
         }
       }
     }
@@ -412,13 +466,53 @@ __global__ void __launch_bounds__(kThreadsLa, 1) k_la_chunk(LaParams p) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) S[16 * blk + e] = 0.f;
     }
-    bool ok = true, odd = false;
+    // Tokens 32 qt .. 32 qt + 31 of chunk c, weighted and in three parts, as this row of the A operand. Warps 8-11
+    // take quarters 0 and 2, warps 12-15 quarters 1 and 3, each in a TMEM buffer of its own.
+    auto parts = [&](int c, int qt) -> bool {
+      // this row's channel of token j: + 128 j, the 16-byte chunk swizzled by j mod 8
+      const uint32_t V = sb + (c & 1) * kStage + 2 * kTile + (row >> 6) * 16384 + (row & 7) * 2 + qt * 4096;
+      const uint32_t swz = ((row & 63) >> 3) << 4;
+      const float* w = sw + (c & 1) * kC + 32 * qt;
+#pragma unroll
+      for (int b16 = 0; b16 < 2; ++b16) {
+        uint32_t p0[8], p1[8], p2[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t v0 = lds_u16(V + b16 * 2048 + 256 * e + (swz ^ (((2 * e) & 7) << 4)));
+          const uint32_t v1 = lds_u16(V + b16 * 2048 + 256 * e + 128 + (swz ^ (((2 * e + 1) & 7) << 4)));
+          // two tokens at once; the top 8 bits, the next 8, the last 8: each difference is exact
+          const f32x2 x = f2_mul(f2_bits(v0 << 16, v1 << 16), *reinterpret_cast<const f32x2*>(w + 16 * b16 + 2 * e));
+          const f32x2 a = x & 0xffff0000ffff0000ull, r = f2_sub(x, a);
+          const f32x2 b = r & 0xffff0000ffff0000ull, d = f2_sub(r, b);
+          p0[e] = __byte_perm((uint32_t)x, (uint32_t)(x >> 32), 0x7632);
+          p1[e] = __byte_perm((uint32_t)r, (uint32_t)(r >> 32), 0x7632);
+          p2[e] = __byte_perm((uint32_t)d, (uint32_t)(d >> 32), 0x7632);
+        }
+        if (b16 == 0) {
+          const int use = 2 * c + (qt >> 1);
+          if (use && !wait_warp(&ms.vfree[half], (use - 1) & 1, ab)) return false;
+          tc_after();
+        }
+        const uint32_t at = tl + kV3 + 48 * half + 8 * b16;
+        tm_st8(at, p0);
+        tm_st8(at + 16, p1);
+        tm_st8(at + 32, p2);
+      }
+      wait_st();
+      tc_before();
+      arrive(&ms.vfull[half]);
+      return true;
+    };
     for (int c = 0; c <= nc; ++c) {
-      if (!(ok = wait_warp(&ms.sums[c & 1], (c >> 1) & 1, ab))) break;
+      if (c < nc) {  // ahead of the state
+        if (!wait_warp(&ms.sums[c & 1], (c >> 1) & 1, ab)) break;
+        if (!wait_warp(&ms.full[c & 1], (c >> 1) & 1, ab)) break;
+        if (!parts(c, half)) break;
+      }
       if (c) {  // S <- gamma S + U
-        if (!(ok = wait_warp(&ms.empty[(c - 1) & 1], ((c - 1) >> 1) & 1, ab))) break;
+        const float2 g = ms.gamma[(c - 1) & 3];  // (came with the sums of chunk c - 1)
+        if (!wait_warp(&ms.empty[(c - 1) & 1], ((c - 1) >> 1) & 1, ab)) break;
         tc_after();
-        const float2 g = ms.gamma[(c - 1) & 3];
 #pragma unroll
         for (int blk = 0; blk < 4; ++blk) {
           uint32_t u[16];
@@ -430,7 +524,6 @@ __global__ void __launch_bounds__(kThreadsLa, 1) k_la_chunk(LaParams p) {
             s = __fmaf_rn(s, g.x, __fmaf_rn(s, g.y, __uint_as_float(u[e])));
           }
         }
-        tc_before();
       }
       if (c == nc) break;
       if (OUT) {
@@ -445,97 +538,93 @@ __global__ void __launch_bounds__(kThreadsLa, 1) k_la_chunk(LaParams p) {
           *reinterpret_cast<uint4*>(s16 + ((e ^ (row & 7)) << 4)) = x;
         }
         fence_proxy_async();
-        arrive(&ms.sready);
       }
-      if (!(ok = wait_warp(&ms.full[c & 1], (c >> 1) & 1, ab))) break;
-      const char* V = la_smem + (c & 1) * kStage + 2 * kTile + (row >> 6) * 16384 + (row & 7) * 2;
-      const int chunk16 = (row & 63) >> 3;
-      const float* w = sw + (c & 1) * kC;
-#pragma unroll 1
-      for (int qt = 0; qt < 4; ++qt) {  // 32 tokens; this warp's 16 of them
-        const int buf = qt & 1, use = 2 * c + (qt >> 1);
-        if (use && !(ok = wait_warp(&ms.vfree[buf], (use - 1) & 1, ab))) break;
-        tc_after();
-        uint32_t p0[8], p1[8], p2[8];
-        const int j0 = 32 * qt + 16 * half;
+      tc_before();
+      arrive(&ms.sready);
+      if (!parts(c, 2 + half)) break;
+    }
+    float sum = 0.f;  // NaN, whatever entry is infinite or NaN
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float r[2];
-          uint32_t a[2], b[2], d[2];
-#pragma unroll
-          for (int f = 0; f < 2; ++f) {
-            const int j = j0 + 2 * e + f;
-            const uint32_t bits = *reinterpret_cast<const uint16_t*>(V + j * 128 + ((chunk16 ^ (j & 7)) << 4));
-            odd |= (bits & 0x7f80u) == 0x7f80u;
-            const float x = __fmul_rn(__uint_as_float(bits << 16), w[j]);
-            // the top 8 bits, the next 8, the last 8: each difference is exact
-            a[f] = __float_as_uint(x) & 0xffff0000u;
-            r[f] = __fsub_rn(x, __uint_as_float(a[f]));
-            b[f] = __float_as_uint(r[f]) & 0xffff0000u;
-            d[f] = __float_as_uint(__fsub_rn(r[f], __uint_as_float(b[f])));
-          }
-          p0[e] = __byte_perm(a[0], a[1], 0x7632);
-          p1[e] = __byte_perm(b[0], b[1], 0x7632);
-          p2[e] = __byte_perm(d[0], d[1], 0x7632);
+    for (int e = 0; e < 64; ++e) sum = __fmaf_rn(S[e], 0.f, sum);
+    if (sum != 0.f) ms.flag = 1;
+  } else if (warp == 16) {
+    // Copies. The last chunk's rows past the end are other sequences': they are set to
+    // zero in K and V (a weight of zero does not stop an infinity; Q's only reach rows that are not written).
+    // Full chunks of o leave from Q's tile before the next Q comes in.
+    int issued = 0;
+    for (int c = 0; c < nc + 2; ++c) {
+      const int s = c & 1, n = (int)min((int64_t)kC, pc.len - (int64_t)c * kC);  // (n <= 0: nothing more comes in)
+      const uint32_t dst = sb + s * kStage;
+      const int t0 = (int)(pc.begin + (int64_t)c * kC);
+      uint64_t* bar = n == kC ? &ms.full[s] : &ms.land[s];
+      if (c >= 2 && c - 2 < nc && !wait_warp(&ms.empty[s], ((c - 2) >> 1) & 1, ab)) break;
+      if (n > 0 && lane == 0) {
+        mbar_expect_tx(bar, OUT ? kStage : 2 * kTile);
+        for (int x = 0; x < 2; ++x) tma_tile(dst + kTile + 16384 * x, &mk, kh * kD + 64 * x, t0, bar);
+        for (int x = 0; x < 2; ++x) tma_tile(dst + 2 * kTile + 16384 * x, &mv, h * kD + 64 * x, t0, bar);
+      }
+      if (n > 0) issued = c + 1;
+      if (OUT && c >= 2 && pc.len >= (int64_t)(c - 1) * kC) {  // chunk c - 2 is a full one
+        if (!wait_warp(&ms.oready[s], ((c - 2) >> 1) & 1, ab)) break;
+        if (lane == 0) {
+          for (int x = 0; x < 2; ++x) tma_store(&mo, h * kD + 64 * x, t0 - 2 * kC, dst + 16384 * x);
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         }
-        const uint32_t at = tl + kV3 + 48 * buf + 8 * half;
-        tm_st8(at, p0);
-        tm_st8(at + 16, p1);
-        tm_st8(at + 32, p2);
-        wait_st();
-        tc_before();
-        arrive(&ms.vfull[buf]);
       }
-      if (!ok) break;
-    }
-    if (odd) ms.flag = 1;
-  } else if (warp < 18) {
-    // Copies: tokens past the end are zeros.
-    const bf16* src[3] = {static_cast<const bf16*>(p.q) + kh * kD, static_cast<const bf16*>(p.k) + kh * kD,
-                          static_cast<const bf16*>(p.v) + h * kD};
-    const int64_t st[3] = {p.sq, p.sk, p.sv};
-    for (int c = warp - 16; c < nc; c += 2) {
-      if (c >= 2 && !wait_warp(&ms.empty[c & 1], ((c - 2) >> 1) & 1, ab)) break;
-      const int64_t t0 = pc.begin + (int64_t)c * kC;
-      const int n = (int)min((int64_t)kC, pc.len - (int64_t)c * kC);
-      const int ch = lane & 15;
-#pragma unroll
-      for (int x = OUT ? 0 : 1; x < 3; ++x) {
-        const uint32_t dst = sb + (c & 1) * kStage + x * kTile + (ch >> 3) * 16384;
-        const bf16* from = src[x] + t0 * st[x] + 8 * ch;
-#pragma unroll 8
-        for (int r = lane >> 4; r < kC; r += 2)
-          cp16(dst + r * 128 + (((ch & 7) ^ (r & 7)) << 4), r < n ? from + r * st[x] : from, r < n);
+      if (OUT && n > 0 && lane == 0)
+        for (int x = 0; x < 2; ++x) tma_tile(dst + 16384 * x, &mq, kh * kD + 64 * x, t0, bar);
+      __syncwarp();
+      if (n > 0 && n < kC) {
+        if (!wait_warp(&ms.land[s], 0, ab)) break;
+        uint4* tile = reinterpret_cast<uint4*>(la_smem + s * kStage + kTile);
+        for (int x = lane; x < (kC - n) * 32; x += 32)  // 8 chunks of 16 bytes x 4 half tiles a row
+          tile[((x >> 3) & 3) * 1024 + (n + (x >> 5)) * 8 + (x & 7)] = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) arrive(&ms.full[s]);
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      fence_proxy_async();
-      arrive(&ms.full[c & 1]);
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp == 18) {
+    if (OUT && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    // A wait gave up: what was asked for still has to land before the CTA ends. (In a chunk whose Q was not asked
+    // for, the barrier cannot complete: that wait runs into its limit.)
+    int ignored = 0;
+    if (*reinterpret_cast<volatile int*>(ab))
+      for (int c = max(0, issued - 2); c < issued; ++c) {
+        const bool whole = pc.len >= (int64_t)(c + 1) * kC;
+        wait(whole ? &ms.full[c & 1] : &ms.land[c & 1], whole ? (c >> 1) & 1 : 0, &ignored);
+      }
+  } else if (warp < 19) {
     // Sums of log2 alpha in whole numbers of 2^-40, four tokens to a lane. A decay of
     // zero counts 2^-200: any weight across it is below fp32's smallest number.
     double prod = 1.0;
     bool odd = false;
-    for (int c = 0; c <= nc; ++c) {
-      if (c >= 2 && !wait_warp(&ms.empty[c & 1], ((c - 2) >> 1) & 1, ab)) break;
-      if (c == nc) {
-        arrive(&ms.sums[c & 1]);
-        break;
-      }
-      long long g[4], run = 0;
+    float a[4];
+    auto load = [&](int c) {  // a chunk ahead of its use
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int64_t t = (int64_t)c * kC + 4 * lane + e;
-        float l = 0.f;
-        if (t < pc.len) {
-          const float a = p.alpha[(pc.begin + t) * p.sa + h];
-          if (!(a >= 0.f && a <= 1.f)) odd = true;
-          l = a > 0.f ? fmaxf(log2f(a), -200.f) : -200.f;
-        }
+        a[e] = t < pc.len ? p.alpha[(pc.begin + t) * p.sa + h] : 1.f;
+      }
+    };
+    load(warp - 17);
+    for (int c = warp - 17; c < nc; c += 2) {
+      // gamma, the product of the decays, in two parts; the same in every lane
+      float2 gm = mul2(mul2(make_float2(a[0], 0.f), make_float2(a[1], 0.f)),
+                       mul2(make_float2(a[2], 0.f), make_float2(a[3], 0.f)));
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1)
+        gm = mul2(gm, make_float2(__shfl_xor_sync(0xffffffffu, gm.x, o), __shfl_xor_sync(0xffffffffu, gm.y, o)));
+      prod *= (double)gm.x + (double)gm.y;
+      long long g[4], run = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (!(a[e] >= 0.f && a[e] <= 1.f)) odd = true;
+        const float l = a[e] > 0.f ? fmaxf(log2f(a[e]), -200.f) : -200.f;
         run += __float2ll_rn(__fmul_rn(l, 1099511627776.f));
         g[e] = run;
       }
+      load(c + 2);
       long long sum = run;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -550,33 +639,33 @@ __global__ void __launch_bounds__(kThreadsLa, 1) k_la_chunk(LaParams p) {
         G[e] = __fmul_rn(__ll2float_rn(g[e]), 9.094947017729282e-13f);
         w[e] = exp2f(__fmul_rn(__ll2float_rn(end - g[e]), 9.094947017729282e-13f));
       }
+      if (c >= 2 && !wait_warp(&ms.empty[c & 1], ((c - 2) >> 1) & 1, ab)) break;
       *reinterpret_cast<float4*>(sG + (c & 1) * kC + 4 * lane) = make_float4(G[0], G[1], G[2], G[3]);
       *reinterpret_cast<float4*>(sw + (c & 1) * kC + 4 * lane) = make_float4(w[0], w[1], w[2], w[3]);
+      if (lane == 0) ms.gamma[c & 3] = gm;
       arrive(&ms.sums[c & 1]);
-      // gamma is wanted one chunk later
-      const double gm = exp2((double)end * 9.094947017729282e-13);
-      prod *= gm;
-      if (lane == 0) {
-        const float hi = (float)gm;
-        ms.gamma[c & 3] = make_float2(hi, (float)(gm - (double)hi));
-      }
-      __syncwarp();
     }
     if (odd) ms.flag = 1;
-    if (lane == 0) ms.prod = prod;
+    if (lane == 0) ms.prod[warp - 17] = prod;
   } else if (lane == 0) {
     // The products.
+    auto scores = [&](int c) {  // P = Q K^T
+      tc_after();
+      const uint32_t Q = sb + (c & 1) * kStage, K = Q + kTile;
+      for (int s = 0; s < 8; ++s) {
+        const uint32_t off = (s >> 2) * 16384 + (s & 3) * 32;
+        mma_ss(tm + kP, desc_k(Q + off), desc_k(K + off), kIdesc, s > 0);
+      }
+      commit(&ms.qk);
+    };
+    bool early = false;  // the chunk's scores are on their way
     for (int c = 0; c < nc; ++c) {
       const uint32_t Q = sb + (c & 1) * kStage, K = Q + kTile, V = K + kTile, S16 = sb + kS16;
       if (!wait(&ms.full[c & 1], (c >> 1) & 1, ab)) break;
+      if (OUT && !early) scores(c);
+      if (!wait(&ms.sready, c & 1, ab)) break;  // U has been read, S is in place
       tc_after();
       if (OUT) {
-        for (int s = 0; s < 8; ++s) {
-          const uint32_t off = (s >> 2) * 16384 + (s & 3) * 32;
-          mma_ss(tm + kP, desc_k(Q + off), desc_k(K + off), kIdesc, s > 0);
-        }
-        commit(&ms.qk);
-        if (!wait(&ms.sready, c & 1, ab)) break;
         if (c && !wait(&ms.ofree, (c - 1) & 1, ab)) break;
         tc_after();
         for (int s = 0; s < 8; ++s) {
@@ -594,6 +683,9 @@ __global__ void __launch_bounds__(kThreadsLa, 1) k_la_chunk(LaParams p) {
           for (int s = 0; s < 8; ++s)
             mma_ts(tm + kO, tm + kP + 64 * (s >> 2) + 8 * (s & 3), desc_mn(V + s * 2048), kIdescMn, true);
           commit(&ms.pv);
+          // the next chunk's scores at once (they follow P's last use in order), if its tiles are there
+          early = c + 1 < nc && mbar_test(&ms.full[(c + 1) & 1], ((c + 1) >> 1) & 1);
+          if (early) scores(c + 1);
         }
         if (!(ok = wait(&ms.vfull[buf], use & 1, ab))) break;
         tc_after();
@@ -617,7 +709,7 @@ __global__ void __launch_bounds__(kThreadsLa, 1) k_la_chunk(LaParams p) {
   tc_after();
   if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
-  if (ms.abort) {  // a wait gave up: make that visible
+  if (ms.abort) {  // a wait gave up: make that visible (nothing of this CTA is in flight any more)
     const bf16 bad = __float2bfloat16_rn(__int_as_float(0x7fc00000));
     if (OUT)
       for (int64_t x = tid; x < pc.len * kD; x += kThreadsLa)
@@ -638,7 +730,7 @@ __global__ void __launch_bounds__(kThreadsLa, 1) k_la_chunk(LaParams p) {
     for (int e = 0; e < 16; ++e)
       *reinterpret_cast<float4*>(dst + 4 * e) = make_float4(S[4 * e], S[4 * e + 1], S[4 * e + 2], S[4 * e + 3]);
   }
-  if (!OUT && tid == 0) p.ws_decay[slot * p.heads + h] = ms.prod;
+  if (!OUT && tid == 0) p.ws_decay[slot * p.heads + h] = ms.prod[0] * ms.prod[1];
 }
 
 // The states of split sequences that were staged in the workspace (last states that replace S0 in place).
@@ -650,9 +742,35 @@ __global__ void k_copy_states(LaParams p, const float* from) {
 
 }  // namespace
 
+// A token array as a tensor of heads x 128 channels by tokens, read 64 channels by 128 tokens.
+static cudaError_t tile_map(CUtensorMap* m, const void* base, int heads, int64_t stride, int64_t tokens) {
+  static PFN_encode encode = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_encode>(f);
+  }();
+  if (!encode) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {(cuuint64_t)heads * kD, (cuuint64_t)tokens}, pitch[1] = {(cuuint64_t)stride * 2};
+  const cuuint32_t box[2] = {64, kC}, one[2] = {1, 1};
+  const CUresult r =
+      encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, pitch, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 cudaError_t launch_la_chunk_bf16(const LaParams& p0, cudaStream_t st) {
   LaParams p = p0;
   cudaError_t e;
+  CUtensorMap mq = {}, mk = {}, mv = {}, mo = {};
+  if (p.n_tokens && ((e = tile_map(&mq, p.q, p.key_heads, p.sq, p.n_tokens)) != cudaSuccess ||
+                     (e = tile_map(&mk, p.k, p.key_heads, p.sk, p.n_tokens)) != cudaSuccess ||
+                     (e = tile_map(&mv, p.v, p.heads, p.sv, p.n_tokens)) != cudaSuccess ||
+                     (e = tile_map(&mo, p.o, p.heads, p.so, p.n_tokens)) != cudaSuccess))
+    return e;
   if ((e = cudaFuncSetAttribute(k_la_chunk<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) != cudaSuccess)
     return e;
   const int64_t slots = p.seg ? p.slots : p.n_seqs;
@@ -661,11 +779,11 @@ cudaError_t launch_la_chunk_bf16(const LaParams& p0, cudaStream_t st) {
   if (p.seg) {
     e = cudaFuncSetAttribute(k_la_chunk<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    k_la_chunk<false><<<grid, kThreadsLa, kSmem, st>>>(p);
+    k_la_chunk<false><<<grid, kThreadsLa, kSmem, st>>>(p, mq, mk, mv, mo);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (staged) p.S = p.ws_last;
   }
-  k_la_chunk<true><<<grid, kThreadsLa, kSmem, st>>>(p);
+  k_la_chunk<true><<<grid, kThreadsLa, kSmem, st>>>(p, mq, mk, mv, mo);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (staged) {
     p.S = p0.S;
