@@ -57,29 +57,46 @@ struct Misc {
 };
 static_assert(sizeof(Misc) <= 512, "misc");
 
-__device__ __forceinline__ uint64_t desc_k(uint32_t a) {  // rows of the operand are rows of the tile
-  return (uint64_t)((a & 0x3ffff) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+// Shared-memory operands: 128-byte rows, swizzled; the low word has the address, the high word
+// the 1,024 bytes between groups of eight rows. Rows of the operand are rows of the tile (kByRow) or its
+// channels, 64 of them to a half tile (kByChannel).
+constexpr uint32_t kByRow = 1u << 16, kByChannel = 1024u << 16;
+__device__ __forceinline__ uint64_t desc(uint32_t lo) {
+  return (uint64_t)lo | ((uint64_t)(64u | (1u << 14) | (2u << 29)) << 32);
 }
-__device__ __forceinline__ uint64_t desc_mn(uint32_t a) {  // rows of the operand are channels of the tile
-  return (uint64_t)((a & 0x3ffff) >> 4) | (1024ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
-// fp32 accumulators, bf16 operands, M = N = 128; B by channels or by rows
+// fp32 accumulators, bf16 operands, M = N = 128; B by rows or by channels
 constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (16u << 17) | (8u << 24);
 constexpr uint32_t kIdescMn = kIdesc | (1u << 16);
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool acc) {
+// The products are issued by one thread of a converged warp, chosen by elect.sync with warp-uniform operands:
+// from a thread chosen by its lane number the same instructions took 220 cycles each to issue (64 to run).
+__device__ __forceinline__ bool elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0;
+}
+template <bool ACC>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"((uint32_t)acc)
+      "l"(desc(a)), "l"(desc(b)), "r"(id), "n"(ACC ? 1 : 0)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool acc) {
+template <bool ACC>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"((uint32_t)acc)
+      "r"(a), "l"(desc(b)), "r"(id), "n"(ACC ? 1 : 0)
       : "memory");
+}
+// d = a b^T, both 128 x 128 by rows: eight steps of 16 channels
+__device__ __forceinline__ void product(uint32_t d, uint32_t a, uint32_t b) {
+  mma_ss<false>(d, a, b, kIdesc);
+#pragma unroll
+  for (int s = 1; s < 8; ++s)
+    mma_ss<true>(d, a + (s >> 2) * 1024 + (s & 3) * 2, b + (s >> 2) * 1024 + (s & 3) * 2, kIdesc);
 }
 __device__ __forceinline__ void commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
@@ -647,61 +664,79 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
     }
     if (odd) ms.flag = 1;
     if (lane == 0) ms.prod[warp - 17] = prod;
-  } else if (lane == 0) {
+  } else {
     // The products.
-    auto scores = [&](int c) {  // P = Q K^T
-      tc_after();
-      const uint32_t Q = sb + (c & 1) * kStage, K = Q + kTile;
-      for (int s = 0; s < 8; ++s) {
-        const uint32_t off = (s >> 2) * 16384 + (s & 3) * 32;
-        mma_ss(tm + kP, desc_k(Q + off), desc_k(K + off), kIdesc, s > 0);
-      }
-      commit(&ms.qk);
-    };
+    const uint32_t tmu = __shfl_sync(0xffffffffu, tm, 0);
+    const uint32_t S16 = ((sb + kS16) >> 4) | kByRow;
     bool early = false;  // the chunk's scores are on their way
     for (int c = 0; c < nc; ++c) {
-      const uint32_t Q = sb + (c & 1) * kStage, K = Q + kTile, V = K + kTile, S16 = sb + kS16;
-      if (!wait(&ms.full[c & 1], (c >> 1) & 1, ab)) break;
-      if (OUT && !early) scores(c);
-      if (!wait(&ms.sready, c & 1, ab)) break;  // U has been read, S is in place
+      const uint32_t at = (sb + (c & 1) * kStage) >> 4, next = (sb + ((c + 1) & 1) * kStage) >> 4;
+      const uint32_t Q = at | kByRow, K = (at + kTile / 16) | kByRow;
+      const uint32_t Kc = (at + kTile / 16) | kByChannel, Vc = (at + 2 * kTile / 16) | kByChannel;
+      if (!wait_warp(&ms.full[c & 1], (c >> 1) & 1, ab)) break;
+      tc_after();
+      if (OUT && !early) {
+        if (elect()) {
+          product(tmu + kP, Q, K);
+          commit(&ms.qk);
+        }
+        __syncwarp();
+      }
+      if (!wait_warp(&ms.sready, c & 1, ab)) break;  // U has been read, S is in place
+      if (OUT && c && !wait_warp(&ms.ofree, (c - 1) & 1, ab)) break;
       tc_after();
       if (OUT) {
-        if (c && !wait(&ms.ofree, (c - 1) & 1, ab)) break;
-        tc_after();
-        for (int s = 0; s < 8; ++s) {
-          const uint32_t off = (s >> 2) * 16384 + (s & 3) * 32;
-          mma_ss(tm + kO, desc_k(Q + off), desc_k(S16 + off), kIdesc, s > 0);
+        if (elect()) {
+          product(tmu + kO, Q, S16);
+          commit(&ms.qs);
         }
-        commit(&ms.qs);
+        __syncwarp();
       }
       bool ok = true;
+#pragma unroll
       for (int qt = 0; qt < 4; ++qt) {
         const int buf = qt & 1, use = 2 * c + (qt >> 1);
         if (OUT && qt == 2) {
-          if (!(ok = wait(&ms.pvok, c & 1, ab))) break;
-          tc_after();
-          for (int s = 0; s < 8; ++s)
-            mma_ts(tm + kO, tm + kP + 64 * (s >> 2) + 8 * (s & 3), desc_mn(V + s * 2048), kIdescMn, true);
-          commit(&ms.pv);
+          if (!(ok = wait_warp(&ms.pvok, c & 1, ab))) break;
           // the next chunk's scores at once (they follow P's last use in order), if its tiles are there
-          early = c + 1 < nc && mbar_test(&ms.full[(c + 1) & 1], ((c + 1) >> 1) & 1);
-          if (early) scores(c + 1);
+          early = c + 1 < nc && __all_sync(0xffffffffu, mbar_test(&ms.full[(c + 1) & 1], ((c + 1) >> 1) & 1));
+          tc_after();
+          if (elect()) {
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+              mma_ts<true>(tmu + kO, tmu + kP + 64 * (s >> 2) + 8 * (s & 3), Vc + s * 128, kIdescMn);
+            commit(&ms.pv);
+            if (early) {
+              product(tmu + kP, next | kByRow, (next + kTile / 16) | kByRow);
+              commit(&ms.qk);
+            }
+          }
+          __syncwarp();
         }
-        if (!(ok = wait(&ms.vfull[buf], use & 1, ab))) break;
+        if (!(ok = wait_warp(&ms.vfull[buf], use & 1, ab))) break;
         tc_after();
-        for (int part = 2; part >= 0; --part)  // the small parts first
-          for (int s = 0; s < 2; ++s)
-            mma_ts(tm + kU, tm + kV3 + 48 * buf + 16 * part + 8 * s, desc_mn(K + (2 * qt + s) * 2048), kIdescMn,
-                   !(qt == 0 && part == 2 && s == 0));
-        commit(&ms.vfree[buf]);
+        if (elect()) {
+          const uint32_t a = tmu + kV3 + 48 * buf, b = Kc + 2 * qt * 128;
+          // the small parts first
+          if (qt == 0) mma_ts<false>(tmu + kU, a + 32, b, kIdescMn);
+          else mma_ts<true>(tmu + kU, a + 32, b, kIdescMn);
+          mma_ts<true>(tmu + kU, a + 40, b + 128, kIdescMn);
+#pragma unroll
+          for (int part = 1; part >= 0; --part)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) mma_ts<true>(tmu + kU, a + 16 * part + 8 * s, b + 128 * s, kIdescMn);
+          commit(&ms.vfree[buf]);
+          if (qt == 3) commit(&ms.empty[c & 1]);
+        }
+        __syncwarp();
       }
       if (!ok) break;
-      commit(&ms.empty[c & 1]);
     }
     // nothing may be in flight when TMEM is given back
-    commit(&ms.drain);
+    if (elect()) commit(&ms.drain);
+    __syncwarp();
     int ignored = 0;
-    wait(&ms.drain, 0, &ignored);
+    wait_warp(&ms.drain, 0, &ignored);
   }
   __syncwarp();
   tc_before();
