@@ -153,16 +153,6 @@ __device__ __forceinline__ void arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 // Waits for phase `parity`; false once this or any other wait of the CTA has given up.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -227,27 +217,10 @@ using PFN_encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, v
                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// The state before segment i, columns [c0, c0 + 16) of row `row`: S0 (or zero), then what segments 0..i-1 added.
-__device__ __forceinline__ void start_state(const LaParams& p, const Piece& pc, int64_t slot, int h, int row, int c0,
-                                            float s[16]) {
-  if (p.S0) {
-    const float* a = p.S0 + (((pc.b * p.heads + h) * kD) + row) * kD + c0;
-#pragma unroll
-    for (int e = 0; e < 16; e += 4) ld4(a + e, s + e);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 16; ++e) s[e] = 0.f;
-  }
-  for (int64_t r = slot - pc.i; r < slot; ++r) {
-    const double d = p.ws_decay[r * p.heads + h];
-    const float hi = (float)d, lo = (float)(d - (double)hi);
-    const float* a = p.ws_state + (((r * p.heads + h) * kD) + row) * kD + c0;
-    float u[16];
-#pragma unroll
-    for (int e = 0; e < 16; e += 4) ld4(a + e, u + e);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) s[e] = __fmaf_rn(s[e], hi, __fmaf_rn(s[e], lo, u[e]));
-  }
+// The state before a piece: S0 (NULL: zero), or where a sequence is split what k_la_scan left in the piece's slot.
+__device__ __forceinline__ const float* start_state(const LaParams& p, const Piece& pc, int64_t slot, int h) {
+  if (pc.n > 1) return p.ws_state + (slot * p.heads + h) * (kD * kD);
+  return p.S0 ? p.S0 + (pc.b * p.heads + h) * (kD * kD) : nullptr;
 }
 
 // Token by token: 512 threads, four lanes to a row, 32 columns each (as k_la_recurrent).
@@ -272,15 +245,8 @@ __device__ __noinline__ void redo(const LaParams& p, const Piece& pc, int64_t sl
       const int col = 4 * (4 * c + part);
       S[c][0] = S[c][1] = S[c][2] = S[c][3] = 0.f;
       if (!OUT) continue;
-      if (p.S0) ld4(p.S0 + (((pc.b * p.heads + h) * kD) + row) * kD + col, S[c]);
-      for (int64_t r = slot - pc.i; r < slot; ++r) {
-        const double d = p.ws_decay[r * p.heads + h];
-        const float hi = (float)d, lo = (float)(d - (double)hi);
-        float u[4];
-        ld4(p.ws_state + (((r * p.heads + h) * kD) + row) * kD + col, u);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) S[c][e] = __fmaf_rn(S[c][e], hi, __fmaf_rn(S[c][e], lo, u[e]));
-      }
+      const float* from = start_state(p, pc, slot, h);
+      if (from) ld4(from + row * kD + col, S[c]);
     }
   }
   for (int64_t t0 = 0; t0 < pc.len; t0 += 16) {
@@ -384,7 +350,7 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
   float* sG = reinterpret_cast<float*>(la_smem + kSums);
   float* sw = sG + 2 * kC;
   int* ab = &ms.abort;
-  float S[64];  // warps 8-15: row 32 (warp & 3) + lane, columns 64 (warp >= 12) ..
+  f32x2 S[32];  // warps 8-15: row 32 (warp & 3) + lane, columns 64 (warp >= 12) .., in pairs
 
   if (warp < 8) {
     if (OUT) {
@@ -399,19 +365,20 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
         const float ei = ex2(gi);
         if (!wait_warp(&ms.qk, c & 1, ab)) break;
         tc_after();
-#pragma unroll
-        for (int blk = 0; blk < 2; ++blk) {  // 32 columns j at a time
-          const int j0 = 64 * half + 32 * blk;
-          uint32_t w[16];
+        // Loops are kept rolled here and below: five roles run at once, and with everything unrolled the warps
+        // waited for instructions more than for data.
+#pragma unroll 1
+        for (int j0 = 64 * half; j0 < 64 * half + 64; j0 += 16) {
+          uint32_t w[8];
           if (j0 > 32 * quad + 31) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = 0u;
+            for (int e = 0; e < 8; ++e) w[e] = 0u;
           } else {
-            uint32_t x[32];
-            tm_ld32(tl + kP + j0, x);
+            uint32_t x[16];
+            tm_ld16(tl + kP + j0, x);
             wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
+            for (int e = 0; e < 16; e += 4) {
               const float4 g = *reinterpret_cast<const float4*>(G + j0 + e);
               const float gj[4] = {g.x, g.y, g.z, g.w};
               float y[4];
@@ -422,43 +389,40 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
               w[e / 2 + 1] = pack_bf16(y[2], y[3]);
             }
           }
-          // P's tokens 64 half .. sit in columns 64 half .. of its own accumulator: a warp overwrites what it has read
-          tm_st16(tl + kP + 64 * half + 16 * blk, w);
+          // P's tokens 64 half .. go to columns 64 half .. of its own accumulator: a warp overwrites what it has read
+          tm_st8(tl + kP + 64 * half + (j0 & 63) / 2, w);
         }
         if (!wait_warp(&ms.qs, c & 1, ab)) break;
         tc_after();
-#pragma unroll
-        for (int blk = 0; blk < 2; ++blk) {
-          uint32_t x[32];
-          tm_ld32(tl + kO + 64 * half + 32 * blk, x);
+#pragma unroll 1
+        for (uint32_t at = tl + kO + 64 * half; at < tl + kO + 64 * half + 64; at += 16) {
+          uint32_t x[16];
+          tm_ld16(at, x);
           wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__fmul_rn(ei, __uint_as_float(x[e])));
-          tm_st32(tl + kO + 64 * half + 32 * blk, x);
+          for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__fmul_rn(ei, __uint_as_float(x[e])));
+          tm_st16(at, x);
         }
         wait_st();
         tc_before();
         arrive(&ms.pvok);
         if (!wait_warp(&ms.pv, c & 1, ab)) break;
         tc_after();
-        uint32_t y[32];
-#pragma unroll
-        for (int blk = 0; blk < 2; ++blk) {
-          uint32_t x[32];
-          tm_ld32(tl + kO + 64 * half + 32 * blk, x);
+        // o goes out by way of Q's tile, which nothing reads any more: rows of 128 bytes, swizzled as Q's were
+        char* tile = la_smem + (c & 1) * kStage + half * 16384;
+#pragma unroll 1
+        for (int blk = 0; blk < 4; ++blk) {
+          uint32_t x[16];
+          tm_ld16(tl + kO + 64 * half + 16 * blk, x);
           wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            y[16 * blk + e] = pack_bf16(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+          for (int e = 0; e < 8; ++e) x[e] = pack_bf16(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+          *reinterpret_cast<uint4*>(tile + i * 128 + (((2 * blk) ^ (i & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+          *reinterpret_cast<uint4*>(tile + i * 128 + (((2 * blk + 1) ^ (i & 7)) << 4)) =
+              make_uint4(x[4], x[5], x[6], x[7]);
         }
         tc_before();
         arrive(&ms.ofree);
-        // o goes out by way of Q's tile, which nothing reads any more: rows of 128 bytes, swizzled as Q's were
-        char* tile = la_smem + (c & 1) * kStage + half * 16384;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          *reinterpret_cast<uint4*>(tile + i * 128 + ((e ^ (i & 7)) << 4)) =
-              make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
         const int n = (int)min((int64_t)kC, pc.len - (int64_t)c * kC);
         if (n == kC) {
           fence_proxy_async();
@@ -476,69 +440,75 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
     // B
     const int quad = warp & 3, half = (warp - 8) >> 2, row = 32 * quad + lane;
     const uint32_t tl = tm + ((uint32_t)(32 * quad) << 16);
+    {
+      const float* from = OUT ? start_state(p, pc, slot, h) : nullptr;
 #pragma unroll
-    for (int blk = 0; blk < 4; ++blk) {
-      if (OUT) start_state(p, pc, slot, h, row, 64 * half + 16 * blk, &S[16 * blk]);
-      else
-#pragma unroll
-        for (int e = 0; e < 16; ++e) S[16 * blk + e] = 0.f;
-    }
-    // Tokens 32 qt .. 32 qt + 31 of chunk c, weighted and in three parts, as this row of the A operand. Warps 8-11
-    // take quarters 0 and 2, warps 12-15 quarters 1 and 3, each in a TMEM buffer of its own.
-    auto parts = [&](int c, int qt) -> bool {
-      // this row's channel of token j: + 128 j, the 16-byte chunk swizzled by j mod 8
-      const uint32_t V = sb + (c & 1) * kStage + 2 * kTile + (row >> 6) * 16384 + (row & 7) * 2 + qt * 4096;
-      const uint32_t swz = ((row & 63) >> 3) << 4;
-      const float* w = sw + (c & 1) * kC + 32 * qt;
-#pragma unroll
-      for (int b16 = 0; b16 < 2; ++b16) {
-        uint32_t p0[8], p1[8], p2[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t v0 = lds_u16(V + b16 * 2048 + 256 * e + (swz ^ (((2 * e) & 7) << 4)));
-          const uint32_t v1 = lds_u16(V + b16 * 2048 + 256 * e + 128 + (swz ^ (((2 * e + 1) & 7) << 4)));
-          // two tokens at once; the top 8 bits, the next 8, the last 8: each difference is exact
-          const f32x2 x = f2_mul(f2_bits(v0 << 16, v1 << 16), *reinterpret_cast<const f32x2*>(w + 16 * b16 + 2 * e));
-          const f32x2 a = x & 0xffff0000ffff0000ull, r = f2_sub(x, a);
-          const f32x2 b = r & 0xffff0000ffff0000ull, d = f2_sub(r, b);
-          p0[e] = __byte_perm((uint32_t)x, (uint32_t)(x >> 32), 0x7632);
-          p1[e] = __byte_perm((uint32_t)r, (uint32_t)(r >> 32), 0x7632);
-          p2[e] = __byte_perm((uint32_t)d, (uint32_t)(d >> 32), 0x7632);
-        }
-        if (b16 == 0) {
-          const int use = 2 * c + (qt >> 1);
-          if (use && !wait_warp(&ms.vfree[half], (use - 1) & 1, ab)) return false;
-          tc_after();
-        }
-        const uint32_t at = tl + kV3 + 48 * half + 8 * b16;
-        tm_st8(at, p0);
-        tm_st8(at + 16, p1);
-        tm_st8(at + 32, p2);
+      for (int e = 0; e < 16; ++e) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (from) x = *reinterpret_cast<const float4*>(from + row * kD + 64 * half + 4 * e);
+        S[2 * e] = f2_pack(x.x, x.y);
+        S[2 * e + 1] = f2_pack(x.z, x.w);
       }
-      wait_st();
-      tc_before();
-      arrive(&ms.vfull[half]);
-      return true;
-    };
-    for (int c = 0; c <= nc; ++c) {
-      if (c < nc) {  // ahead of the state
+    }
+    // Two steps a chunk, each one quarter of its tokens (32) weighted and in three parts, as this row of the A
+    // operand: warps 8-11 take quarters 0 and 2, warps 12-15 quarters 1 and 3, each in a TMEM buffer of its own.
+    // The first step's parts are made ahead of the state, which waits for the chunk before.
+    const uint32_t Vrow = sb + 2 * kTile + (row >> 6) * 16384 + (row & 7) * 2;
+    const uint32_t swz = ((row & 63) >> 3) << 4;  // 16-byte chunk of the row's channel, swizzled by the token mod 8
+    const uint32_t to = tl + kV3 + 48 * half;
+    for (int u = 0; u <= 2 * nc; ++u) {
+      const int c = u >> 1, qt = 2 * (u & 1) + half;
+      if (!(u & 1) && c < nc) {
         if (!wait_warp(&ms.sums[c & 1], (c >> 1) & 1, ab)) break;
         if (!wait_warp(&ms.full[c & 1], (c >> 1) & 1, ab)) break;
-        if (!parts(c, half)) break;
       }
+      if (c < nc) {
+        const uint32_t V = Vrow + (c & 1) * kStage + qt * 4096;
+        const float* w = sw + (c & 1) * kC + 32 * qt;
+        bool ok = true;
+#pragma unroll 1
+        for (int b16 = 0; b16 < 2; ++b16) {
+          uint32_t p0[8], p1[8], p2[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t v0 = lds_u16(V + b16 * 2048 + 256 * e + (swz ^ (((2 * e) & 7) << 4)));
+            const uint32_t v1 = lds_u16(V + b16 * 2048 + 256 * e + 128 + (swz ^ (((2 * e + 1) & 7) << 4)));
+            // two tokens at once; the top 8 bits, the next 8, the last 8: each difference is exact
+            const f32x2 x = f2_mul(f2_bits(v0 << 16, v1 << 16), *reinterpret_cast<const f32x2*>(w + 16 * b16 + 2 * e));
+            const f32x2 r = f2_sub(x, x & 0xffff0000ffff0000ull);
+            const f32x2 d = f2_sub(r, r & 0xffff0000ffff0000ull);
+            p0[e] = __byte_perm((uint32_t)x, (uint32_t)(x >> 32), 0x7632);
+            p1[e] = __byte_perm((uint32_t)r, (uint32_t)(r >> 32), 0x7632);
+            p2[e] = __byte_perm((uint32_t)d, (uint32_t)(d >> 32), 0x7632);
+          }
+          if (b16 == 0 && u >= 1) {
+            if (!(ok = wait_warp(&ms.vfree[half], (u - 1) & 1, ab))) break;
+            tc_after();
+          }
+          tm_st8(to + 8 * b16, p0);
+          tm_st8(to + 8 * b16 + 16, p1);
+          tm_st8(to + 8 * b16 + 32, p2);
+        }
+        if (!ok) break;
+        wait_st();
+        tc_before();
+        arrive(&ms.vfull[half]);
+      }
+      if (u & 1) continue;
       if (c) {  // S <- gamma S + U
         const float2 g = ms.gamma[(c - 1) & 3];  // (came with the sums of chunk c - 1)
+        const f32x2 g0 = f2_dup(g.x), g1 = f2_dup(g.y);
         if (!wait_warp(&ms.empty[(c - 1) & 1], ((c - 1) >> 1) & 1, ab)) break;
         tc_after();
 #pragma unroll
         for (int blk = 0; blk < 4; ++blk) {
-          uint32_t u[16];
-          tm_ld16(tl + kU + 64 * half + 16 * blk, u);
+          uint32_t x[16];
+          tm_ld16(tl + kU + 64 * half + 16 * blk, x);
           wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float& s = S[16 * blk + e];
-            s = __fmaf_rn(s, g.x, __fmaf_rn(s, g.y, __uint_as_float(u[e])));
+          for (int e = 0; e < 8; ++e) {
+            f32x2& s = S[8 * blk + e];
+            s = f2_fma(s, g0, f2_fma(s, g1, f2_bits(x[2 * e], x[2 * e + 1])));
           }
         }
       }
@@ -547,23 +517,26 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
         char* s16 = la_smem + kS16 + half * 16384 + row * 128;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          uint4 x;
-          x.x = pack_bf16(S[8 * e], S[8 * e + 1]);
-          x.y = pack_bf16(S[8 * e + 2], S[8 * e + 3]);
-          x.z = pack_bf16(S[8 * e + 4], S[8 * e + 5]);
-          x.w = pack_bf16(S[8 * e + 6], S[8 * e + 7]);
-          *reinterpret_cast<uint4*>(s16 + ((e ^ (row & 7)) << 4)) = x;
+          uint32_t x[4];
+#pragma unroll
+          for (int f = 0; f < 4; ++f) {
+            float lo, hi;
+            f2_unpack(S[4 * e + f], lo, hi);
+            x[f] = pack_bf16(lo, hi);
+          }
+          *reinterpret_cast<uint4*>(s16 + ((e ^ (row & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
         }
         fence_proxy_async();
       }
       tc_before();
       arrive(&ms.sready);
-      if (!parts(c, 2 + half)) break;
     }
-    float sum = 0.f;  // NaN, whatever entry is infinite or NaN
+    f32x2 sum = 0ull;  // NaN where an entry is infinite or NaN
 #pragma unroll
-    for (int e = 0; e < 64; ++e) sum = __fmaf_rn(S[e], 0.f, sum);
-    if (sum != 0.f) ms.flag = 1;
+    for (int e = 0; e < 32; ++e) sum = f2_fma(S[e], 0ull, sum);
+    float s0, s1;
+    f2_unpack(sum, s0, s1);
+    if (s0 != 0.f || s1 != 0.f) ms.flag = 1;
   } else if (warp == 16) {
     // Copies. The last chunk's rows past the end are other sequences': they are set to
     // zero in K and V (a weight of zero does not stop an infinity; Q's only reach rows that are not written).
@@ -668,15 +641,14 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
     // The products.
     const uint32_t tmu = __shfl_sync(0xffffffffu, tm, 0);
     const uint32_t S16 = ((sb + kS16) >> 4) | kByRow;
-    bool early = false;  // the chunk's scores are on their way
     for (int c = 0; c < nc; ++c) {
       const uint32_t at = (sb + (c & 1) * kStage) >> 4, next = (sb + ((c + 1) & 1) * kStage) >> 4;
       const uint32_t Q = at | kByRow, K = (at + kTile / 16) | kByRow;
       const uint32_t Kc = (at + kTile / 16) | kByChannel, Vc = (at + 2 * kTile / 16) | kByChannel;
-      if (!wait_warp(&ms.full[c & 1], (c >> 1) & 1, ab)) break;
-      tc_after();
-      if (OUT && !early) {
-        if (elect()) {
+      if (c == 0 || !OUT) {
+        if (!wait_warp(&ms.full[c & 1], (c >> 1) & 1, ab)) break;
+        tc_after();
+        if (OUT && elect()) {
           product(tmu + kP, Q, K);
           commit(&ms.qk);
         }
@@ -693,25 +665,27 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
         __syncwarp();
       }
       bool ok = true;
-#pragma unroll
+#pragma unroll 1
       for (int qt = 0; qt < 4; ++qt) {
         const int buf = qt & 1, use = 2 * c + (qt >> 1);
         if (OUT && qt == 2) {
           if (!(ok = wait_warp(&ms.pvok, c & 1, ab))) break;
-          // the next chunk's scores at once (they follow P's last use in order), if its tiles are there
-          early = c + 1 < nc && __all_sync(0xffffffffu, mbar_test(&ms.full[(c + 1) & 1], ((c + 1) >> 1) & 1));
           tc_after();
           if (elect()) {
 #pragma unroll
             for (int s = 0; s < 8; ++s)
               mma_ts<true>(tmu + kO, tmu + kP + 64 * (s >> 2) + 8 * (s & 3), Vc + s * 128, kIdescMn);
             commit(&ms.pv);
-            if (early) {
+          }
+          __syncwarp();
+          if (c + 1 < nc) {  // the next chunk's scores at once: they follow P's last use in order
+            if (!(ok = wait_warp(&ms.full[(c + 1) & 1], ((c + 1) >> 1) & 1, ab))) break;
+            if (elect()) {
               product(tmu + kP, next | kByRow, (next + kTile / 16) | kByRow);
               commit(&ms.qk);
             }
+            __syncwarp();
           }
-          __syncwarp();
         }
         if (!(ok = wait_warp(&ms.vfull[buf], use & 1, ab))) break;
         tc_after();
@@ -762,10 +736,62 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
   if (warp >= 8 && warp < 16 && S_out) {
     float* dst = S_out + (32 * (warp & 3) + lane) * kD + 64 * ((warp - 8) >> 2);
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-      *reinterpret_cast<float4*>(dst + 4 * e) = make_float4(S[4 * e], S[4 * e + 1], S[4 * e + 2], S[4 * e + 3]);
+    for (int e = 0; e < 32; e += 2) {
+      float4 x;
+      f2_unpack(S[e], x.x, x.y);
+      f2_unpack(S[e + 1], x.z, x.w);
+      *reinterpret_cast<float4*>(dst + 2 * e) = x;
+    }
   }
   if (!OUT && tid == 0) p.ws_decay[slot * p.heads + h] = ms.prod[0] * ms.prod[1];
+}
+
+// Between the passes: each segment's growth becomes the state before it, S_{i+1} = decay_i S_i + growth_i from S0 on.
+// One thread per four entries; the segments of a sequence are read a few ahead.
+__global__ void __launch_bounds__(256) k_la_scan(LaParams p) {
+  __shared__ int64_t sfirst, sn;
+  const int h = blockIdx.y;
+  const int64_t b = blockIdx.z;
+  if (threadIdx.x < 32) {
+    int64_t first = 0, n = 1, begin, len;
+    for (int64_t x = threadIdx.x; x < b; x += 32) {
+      bounds(p, x, begin, len);
+      first += len > p.seg ? (len + p.seg - 1) / p.seg : 1;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) first += __shfl_xor_sync(0xffffffffu, first, o);
+    bounds(p, b, begin, len);
+    if (len > p.seg) n = (len + p.seg - 1) / p.seg;
+    if (threadIdx.x == 0) sfirst = first, sn = n;
+  }
+  __syncthreads();
+  const int64_t first = sfirst, n = sn;
+  if (n == 1 || first + n > p.slots) return;
+  const int at = 4 * (blockIdx.x * 256 + threadIdx.x);
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  if (p.S0) ld4(p.S0 + (b * p.heads + h) * (kD * kD) + at, s);
+  float* w = p.ws_state + (first * p.heads + h) * (kD * kD) + at;
+  const int64_t pitch = (int64_t)p.heads * (kD * kD);
+  constexpr int kAhead = 4;
+  for (int64_t i = 0; i < n; i += kAhead) {
+    float u[kAhead][4];
+    double d[kAhead];
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x)
+      if (i + x < n - 1) {
+        ld4(w + (i + x) * pitch, u[x]);
+        d[x] = p.ws_decay[(first + i + x) * p.heads + h];
+      }
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) {
+      if (i + x < n) *reinterpret_cast<float4*>(w + (i + x) * pitch) = make_float4(s[0], s[1], s[2], s[3]);
+      if (i + x < n - 1) {
+        const float hi = (float)d[x], lo = (float)(d[x] - (double)hi);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] = __fmaf_rn(s[e], hi, __fmaf_rn(s[e], lo, u[x][e]));
+      }
+    }
+  }
 }
 
 // The states of split sequences that were staged in the workspace (last states that replace S0 in place).
@@ -815,6 +841,8 @@ cudaError_t launch_la_chunk_bf16(const LaParams& p0, cudaStream_t st) {
     e = cudaFuncSetAttribute(k_la_chunk<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     k_la_chunk<false><<<grid, kThreadsLa, kSmem, st>>>(p, mq, mk, mv, mo);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    k_la_scan<<<dim3(kD * kD / 1024, (unsigned)p.heads, (unsigned)p.n_seqs), 256, 0, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (staged) p.S = p.ws_last;
   }
