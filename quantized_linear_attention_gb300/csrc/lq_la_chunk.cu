@@ -36,7 +36,11 @@ namespace lqi {
 namespace {
 
 constexpr int kC = 128;  // tokens per chunk
-constexpr int kThreadsLa = 640;
+constexpr int kThreadsLa = 896;
+// Registers of a thread: 72 at launch (64,512 in all), then 64, 96, 64 and 48 for A, B, C and the rest (63,488).
+// An increase waits until the registers are there, and nothing bounds that wait: all but B give theirs up first
+// thing and take them back only after B has (roles_done), so each increase finds what it needs.
+constexpr int kRegs = 72, kRegsA = 64, kRegsB = 96, kRegsC = 64, kRegsRest = 48;
 constexpr uint32_t kTile = 32768;             // 128 x 128 bf16: two halves of 64 channels, 128-byte rows, swizzled
 constexpr uint32_t kStage = 3 * kTile;        // Q, K, V
 constexpr uint32_t kS16 = 2 * kStage;         // the state in bf16
@@ -49,7 +53,7 @@ constexpr uint32_t kU = 0, kP = 128, kO = 256, kV3 = 384;  // kV3: two buffers o
 
 struct Misc {
   float2 gamma[4];
-  uint64_t land[2], full[2], empty[2], sums[2], oready[2], qk, qs, pv, pvok, ofree, sready, vfull[2], vfree[2], drain;
+  uint64_t land[2], full[2], empty[2], sums[2], oready[2], qk, qs, pv, pvok, ofree, sready, grown, vfull[2], vfree[2], drain;
   uint32_t tmem;
   int abort, flag;
   double prod[2];
@@ -147,6 +151,21 @@ __device__ __forceinline__ void tm_st8(uint32_t a, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(a), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// All warps, each at the end of its role.
+__device__ __forceinline__ void roles_done() {
+  __syncwarp();
+  asm volatile("bar.sync 2, %0;" ::"n"(kThreadsLa) : "memory");
 }
 
 __device__ __forceinline__ void arrive(uint64_t* bar) {
@@ -335,6 +354,7 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
     }
     mbar_init(&ms.qk, 1);
     mbar_init(&ms.qs, 1);
+    mbar_init(&ms.grown, 1);
     mbar_init(&ms.pv, 1);
     mbar_init(&ms.pvok, 256);
     mbar_init(&ms.ofree, 256);
@@ -350,9 +370,9 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
   float* sG = reinterpret_cast<float*>(la_smem + kSums);
   float* sw = sG + 2 * kC;
   int* ab = &ms.abort;
-  f32x2 S[32];  // warps 8-15: row 32 (warp & 3) + lane, columns 64 (warp >= 12) .., in pairs
 
   if (warp < 8) {
+    regs_down<kRegsA>();
     if (OUT) {
       // A: row i = 32 (warp & 3) + lane of the chunk, columns 64 half .. 64 half + 63
       const int quad = warp & 3, half = warp >> 2, i = 32 * quad + lane;
@@ -436,10 +456,14 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
         }
       }
     }
+    roles_done();
+    regs_up<kRegs>();
   } else if (warp < 16) {
     // B
+    regs_up<kRegsB>();
     const int quad = warp & 3, half = (warp - 8) >> 2, row = 32 * quad + lane;
     const uint32_t tl = tm + ((uint32_t)(32 * quad) << 16);
+    f32x2 S[32];  // row `row` of the state, columns 64 half .., in pairs
     {
       const float* from = OUT ? start_state(p, pc, slot, h) : nullptr;
 #pragma unroll
@@ -450,55 +474,11 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
         S[2 * e + 1] = f2_pack(x.z, x.w);
       }
     }
-    // Two steps a chunk, each one quarter of its tokens (32) weighted and in three parts, as this row of the A
-    // operand: warps 8-11 take quarters 0 and 2, warps 12-15 quarters 1 and 3, each in a TMEM buffer of its own.
-    // The first step's parts are made ahead of the state, which waits for the chunk before.
-    const uint32_t Vrow = sb + 2 * kTile + (row >> 6) * 16384 + (row & 7) * 2;
-    const uint32_t swz = ((row & 63) >> 3) << 4;  // 16-byte chunk of the row's channel, swizzled by the token mod 8
-    const uint32_t to = tl + kV3 + 48 * half;
-    for (int u = 0; u <= 2 * nc; ++u) {
-      const int c = u >> 1, qt = 2 * (u & 1) + half;
-      if (!(u & 1) && c < nc) {
-        if (!wait_warp(&ms.sums[c & 1], (c >> 1) & 1, ab)) break;
-        if (!wait_warp(&ms.full[c & 1], (c >> 1) & 1, ab)) break;
-      }
-      if (c < nc) {
-        const uint32_t V = Vrow + (c & 1) * kStage + qt * 4096;
-        const float* w = sw + (c & 1) * kC + 32 * qt;
-        bool ok = true;
-#pragma unroll 1
-        for (int b16 = 0; b16 < 2; ++b16) {
-          uint32_t p0[8], p1[8], p2[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint32_t v0 = lds_u16(V + b16 * 2048 + 256 * e + (swz ^ (((2 * e) & 7) << 4)));
-            const uint32_t v1 = lds_u16(V + b16 * 2048 + 256 * e + 128 + (swz ^ (((2 * e + 1) & 7) << 4)));
-            // two tokens at once; the top 8 bits, the next 8, the last 8: each difference is exact
-            const f32x2 x = f2_mul(f2_bits(v0 << 16, v1 << 16), *reinterpret_cast<const f32x2*>(w + 16 * b16 + 2 * e));
-            const f32x2 r = f2_sub(x, x & 0xffff0000ffff0000ull);
-            const f32x2 d = f2_sub(r, r & 0xffff0000ffff0000ull);
-            p0[e] = __byte_perm((uint32_t)x, (uint32_t)(x >> 32), 0x7632);
-            p1[e] = __byte_perm((uint32_t)r, (uint32_t)(r >> 32), 0x7632);
-            p2[e] = __byte_perm((uint32_t)d, (uint32_t)(d >> 32), 0x7632);
-          }
-          if (b16 == 0 && u >= 1) {
-            if (!(ok = wait_warp(&ms.vfree[half], (u - 1) & 1, ab))) break;
-            tc_after();
-          }
-          tm_st8(to + 8 * b16, p0);
-          tm_st8(to + 8 * b16 + 16, p1);
-          tm_st8(to + 8 * b16 + 32, p2);
-        }
-        if (!ok) break;
-        wait_st();
-        tc_before();
-        arrive(&ms.vfull[half]);
-      }
-      if (u & 1) continue;
+    for (int c = 0; c <= nc; ++c) {
       if (c) {  // S <- gamma S + U
-        const float2 g = ms.gamma[(c - 1) & 3];  // (came with the sums of chunk c - 1)
+        const float2 g = ms.gamma[(c - 1) & 3];
         const f32x2 g0 = f2_dup(g.x), g1 = f2_dup(g.y);
-        if (!wait_warp(&ms.empty[(c - 1) & 1], ((c - 1) >> 1) & 1, ab)) break;
+        if (!wait_warp(&ms.grown, (c - 1) & 1, ab)) break;  // (S's bf16 copy has been read by then, too)
         tc_after();
 #pragma unroll
         for (int blk = 0; blk < 4; ++blk) {
@@ -513,6 +493,9 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
         }
       }
       if (c == nc) break;
+      // gamma of this chunk, for the next round (a barrier's phase has to be waited for before this warp lets the
+      // chunk go on: two chunks later it would be taken for the one before)
+      if (!wait_warp(&ms.sums[c & 1], (c >> 1) & 1, ab)) break;
       if (OUT) {
         char* s16 = la_smem + kS16 + half * 16384 + row * 128;
 #pragma unroll
@@ -537,7 +520,63 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
     float s0, s1;
     f2_unpack(sum, s0, s1);
     if (s0 != 0.f || s1 != 0.f) ms.flag = 1;
-  } else if (warp == 16) {
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    // (odd decays were flagged before their sums were handed over)
+    if (S_out && !*reinterpret_cast<volatile int*>(&ms.flag) && !*reinterpret_cast<volatile int*>(ab)) {
+      float* dst = S_out + row * kD + 64 * half;
+#pragma unroll
+      for (int e = 0; e < 32; e += 2) {
+        float4 x;
+        f2_unpack(S[e], x.x, x.y);
+        f2_unpack(S[e + 1], x.z, x.w);
+        *reinterpret_cast<float4*>(dst + 2 * e) = x;
+      }
+    }
+    regs_down<kRegs>();
+    roles_done();
+  } else if (warp < 24) {
+    // C: quarters (32 tokens) of a chunk, weighted and in three parts, as rows of the A operand: row 32 (warp & 3) +
+    // lane. Warps 16-19 take quarters 0 and 2, warps 20-23 quarters 1 and 3, each in a TMEM buffer of its own.
+    regs_down<kRegsC>();
+    const int quad = warp & 3, set = (warp - 16) >> 2, row = 32 * quad + lane;
+    const uint32_t Vrow = sb + 2 * kTile + (row >> 6) * 16384 + (row & 7) * 2;
+    const uint32_t swz = ((row & 63) >> 3) << 4;  // 16-byte chunk of the row's channel, swizzled by the token mod 8
+    const uint32_t to = tm + ((uint32_t)(32 * quad) << 16) + kV3 + 48 * set;
+    for (int u = 0; u < 2 * nc; ++u) {
+      const int c = u >> 1, qt = 2 * (u & 1) + set;
+      if (!(u & 1)) {
+        if (!wait_warp(&ms.sums[c & 1], (c >> 1) & 1, ab)) break;
+        if (!wait_warp(&ms.full[c & 1], (c >> 1) & 1, ab)) break;
+      }
+      const uint32_t V = Vrow + (c & 1) * kStage + qt * 4096;
+      const float* w = sw + (c & 1) * kC + 32 * qt;
+      uint32_t p0[16], p1[16], p2[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const uint32_t v0 = lds_u16(V + 256 * e + (swz ^ (((2 * e) & 7) << 4)));
+        const uint32_t v1 = lds_u16(V + 256 * e + 128 + (swz ^ (((2 * e + 1) & 7) << 4)));
+        // two tokens at once; the top 8 bits, the next 8, the last 8: each difference is exact
+        const f32x2 x = f2_mul(f2_bits(v0 << 16, v1 << 16), *reinterpret_cast<const f32x2*>(w + 2 * e));
+        const f32x2 r = f2_sub(x, x & 0xffff0000ffff0000ull);
+        const f32x2 d = f2_sub(r, r & 0xffff0000ffff0000ull);
+        p0[e] = __byte_perm((uint32_t)x, (uint32_t)(x >> 32), 0x7632);
+        p1[e] = __byte_perm((uint32_t)r, (uint32_t)(r >> 32), 0x7632);
+        p2[e] = __byte_perm((uint32_t)d, (uint32_t)(d >> 32), 0x7632);
+      }
+      if (u && !wait_warp(&ms.vfree[set], (u - 1) & 1, ab)) break;
+      tc_after();
+      tm_st16(to, p0);
+      tm_st16(to + 16, p1);
+      tm_st16(to + 32, p2);
+      wait_st();
+      tc_before();
+      arrive(&ms.vfull[set]);
+    }
+    roles_done();
+    regs_up<kRegs>();
+  } else {
+  regs_down<kRegsRest>();
+  if (warp == 24) {
     // Copies. The last chunk's rows past the end are other sequences': they are set to
     // zero in K and V (a weight of zero does not stop an infinity; Q's only reach rows that are not written).
     // Full chunks of o leave from Q's tile before the next Q comes in.
@@ -584,7 +623,7 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
         const bool whole = pc.len >= (int64_t)(c + 1) * kC;
         wait(whole ? &ms.full[c & 1] : &ms.land[c & 1], whole ? (c >> 1) & 1 : 0, &ignored);
       }
-  } else if (warp < 19) {
+  } else if (warp < 27) {
     // Sums of log2 alpha in whole numbers of 2^-40, four tokens to a lane. A decay of
     // zero counts 2^-200: any weight across it is below fp32's smallest number.
     double prod = 1.0;
@@ -597,8 +636,8 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
         a[e] = t < pc.len ? p.alpha[(pc.begin + t) * p.sa + h] : 1.f;
       }
     };
-    load(warp - 17);
-    for (int c = warp - 17; c < nc; c += 2) {
+    load(warp - 25);
+    for (int c = warp - 25; c < nc; c += 2) {
       // gamma, the product of the decays, in two parts; the same in every lane
       float2 gm = mul2(mul2(make_float2(a[0], 0.f), make_float2(a[1], 0.f)),
                        mul2(make_float2(a[2], 0.f), make_float2(a[3], 0.f)));
@@ -633,10 +672,10 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
       *reinterpret_cast<float4*>(sG + (c & 1) * kC + 4 * lane) = make_float4(G[0], G[1], G[2], G[3]);
       *reinterpret_cast<float4*>(sw + (c & 1) * kC + 4 * lane) = make_float4(w[0], w[1], w[2], w[3]);
       if (lane == 0) ms.gamma[c & 3] = gm;
+      if (odd) ms.flag = 1;
       arrive(&ms.sums[c & 1]);
     }
-    if (odd) ms.flag = 1;
-    if (lane == 0) ms.prod[warp - 17] = prod;
+    if (lane == 0) ms.prod[warp - 25] = prod;
   } else {
     // The products.
     const uint32_t tmu = __shfl_sync(0xffffffffu, tm, 0);
@@ -655,37 +694,19 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
         __syncwarp();
       }
       if (!wait_warp(&ms.sready, c & 1, ab)) break;  // U has been read, S is in place
-      if (OUT && c && !wait_warp(&ms.ofree, (c - 1) & 1, ab)) break;
       tc_after();
-      if (OUT) {
-        if (elect()) {
-          product(tmu + kO, Q, S16);
-          commit(&ms.qs);
-        }
-        __syncwarp();
-      }
       bool ok = true;
 #pragma unroll 1
       for (int qt = 0; qt < 4; ++qt) {
         const int buf = qt & 1, use = 2 * c + (qt >> 1);
-        if (OUT && qt == 2) {
-          if (!(ok = wait_warp(&ms.pvok, c & 1, ab))) break;
+        if (OUT && qt == 2) {  // while quarter 2 is in the making
+          if (c && !(ok = wait_warp(&ms.ofree, (c - 1) & 1, ab))) break;
           tc_after();
           if (elect()) {
-#pragma unroll
-            for (int s = 0; s < 8; ++s)
-              mma_ts<true>(tmu + kO, tmu + kP + 64 * (s >> 2) + 8 * (s & 3), Vc + s * 128, kIdescMn);
-            commit(&ms.pv);
+            product(tmu + kO, Q, S16);
+            commit(&ms.qs);
           }
           __syncwarp();
-          if (c + 1 < nc) {  // the next chunk's scores at once: they follow P's last use in order
-            if (!(ok = wait_warp(&ms.full[(c + 1) & 1], ((c + 1) >> 1) & 1, ab))) break;
-            if (elect()) {
-              product(tmu + kP, next | kByRow, (next + kTile / 16) | kByRow);
-              commit(&ms.qk);
-            }
-            __syncwarp();
-          }
         }
         if (!(ok = wait_warp(&ms.vfull[buf], use & 1, ab))) break;
         tc_after();
@@ -700,17 +721,42 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
 #pragma unroll
             for (int s = 0; s < 2; ++s) mma_ts<true>(tmu + kU, a + 16 * part + 8 * s, b + 128 * s, kIdescMn);
           commit(&ms.vfree[buf]);
-          if (qt == 3) commit(&ms.empty[c & 1]);
+          if (qt == 3) commit(&ms.grown);
+          if (qt == 3 && !OUT) commit(&ms.empty[c & 1]);
         }
         __syncwarp();
       }
       if (!ok) break;
+      if (OUT) {  // while the state is brought up to date
+        if (!wait_warp(&ms.pvok, c & 1, ab)) break;
+        tc_after();
+        if (elect()) {
+#pragma unroll
+          for (int s = 0; s < 8; ++s)
+            mma_ts<true>(tmu + kO, tmu + kP + 64 * (s >> 2) + 8 * (s & 3), Vc + s * 128, kIdescMn);
+          commit(&ms.pv);
+          commit(&ms.empty[c & 1]);
+        }
+        __syncwarp();
+        if (c + 1 < nc) {  // the next chunk's scores: they follow P's last use in order
+          if (!wait_warp(&ms.full[(c + 1) & 1], ((c + 1) >> 1) & 1, ab)) break;
+          if (elect()) {
+            product(tmu + kP, next | kByRow, (next + kTile / 16) | kByRow);
+            commit(&ms.qk);
+          }
+          __syncwarp();
+        }
+      }
     }
     // nothing may be in flight when TMEM is given back
     if (elect()) commit(&ms.drain);
     __syncwarp();
     int ignored = 0;
     wait_warp(&ms.drain, 0, &ignored);
+  }
+  __syncwarp();
+  roles_done();
+  regs_up<kRegs>();
   }
   __syncwarp();
   tc_before();
@@ -732,16 +778,6 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
     redo<OUT>(p, pc, slot, h, reinterpret_cast<float*>(la_smem), S_out,
               OUT ? nullptr : p.ws_decay + slot * p.heads + h);
     return;
-  }
-  if (warp >= 8 && warp < 16 && S_out) {
-    float* dst = S_out + (32 * (warp & 3) + lane) * kD + 64 * ((warp - 8) >> 2);
-#pragma unroll
-    for (int e = 0; e < 32; e += 2) {
-      float4 x;
-      f2_unpack(S[e], x.x, x.y);
-      f2_unpack(S[e + 1], x.z, x.w);
-      *reinterpret_cast<float4*>(dst + 2 * e) = x;
-    }
   }
   if (!OUT && tid == 0) p.ws_decay[slot * p.heads + h] = ms.prod[0] * ms.prod[1];
 }
