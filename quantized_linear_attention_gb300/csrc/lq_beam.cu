@@ -11,8 +11,8 @@
 //
 // The sum of a slice: with m = ceil(max * log2 e), a whole number, each term is
 // 2^(x log2 e - m), its exponent formed by two fmas from a two-part log2 e (one
-// rounding, relative to the exponent itself), and the slices' sums join by exact
-// powers of two. Rows with equal contents sum in the same order whatever their
+// rounding, relative to the exponent itself). Threads' sums join as whole numbers of
+// 2^-40 and slices by shifts: exact, and 64-bit floating point is slow here. Rows with equal contents sum in the same order whatever their
 // place in memory, so equal hypotheses tie exactly.
 //
 // The n_best of a slice without a sort: 64 groups of four threads give their
@@ -27,6 +27,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "lq_device.cuh"
 #include "lq_internal.h"
 
 namespace lqi {
@@ -35,6 +36,7 @@ namespace {
 
 constexpr int kNT = 256;
 constexpr double kLn2 = 0.693147180559945309417;
+constexpr float kL2Ehi = 1.44269502162933349609375f, kL2Elo = 1.92596299e-8f;  // log2 e in two parts
 constexpr int kList = 512;   // candidates a slice collects before ranking
 constexpr int kPick = 2048;  // candidates a request collects before ranking
 
@@ -43,13 +45,14 @@ struct Cand {
   int32_t t;
 };
 
-// Workspace, per (row, slice): the sum (64 bits), what it is relative to, the number of candidates, the candidates.
+// Workspace, per (row, slice): the sum of its exponentials in whole numbers of 2^-40 (kNotFinite where it is not
+// finite), what it is relative to, and n_best candidates (x = -inf: none).
 constexpr int32_t kByTop = INT32_MAX;
+constexpr uint64_t kNotFinite = ~0ull;
 struct Ws {
-  double* sum;
+  uint64_t* sum;
   int32_t* exp2;  // the sum stands for sum * 2^exp2, or where this is kByTop
   float* top;     // for sum * e^top
-  int32_t* n;
   Cand* cand;
 };
 
@@ -58,13 +61,11 @@ __host__ __device__ inline size_t up256(size_t x) { return (x + 255) & ~(size_t)
 __host__ __device__ inline Ws carve(void* ws, int64_t lists) {
   char* c = static_cast<char*>(ws);
   Ws w;
-  w.sum = reinterpret_cast<double*>(c);
+  w.sum = reinterpret_cast<uint64_t*>(c);
   c += up256(8 * lists);
   w.exp2 = reinterpret_cast<int32_t*>(c);
   c += up256(4 * lists);
   w.top = reinterpret_cast<float*>(c);
-  c += up256(4 * lists);
-  w.n = reinterpret_cast<int32_t*>(c);
   c += up256(4 * lists);
   w.cand = reinterpret_cast<Cand*>(c);
   return w;
@@ -77,6 +78,10 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 }
 __device__ __forceinline__ float unordered(uint32_t u) {
   return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xffffffffu));
+}
+// An element's place in its row's order: larger logits first, then lower indices.
+__device__ __forceinline__ uint64_t key_of(float x, int64_t t) {
+  return ((uint64_t)ordered(x) << 32) | (0xffffffffu - (uint32_t)t);
 }
 __device__ __forceinline__ uint64_t ordered(double x) {
   const uint64_t u = (uint64_t)__double_as_longlong(x + 0.0);
@@ -115,57 +120,85 @@ struct Elem<__half> {
   }
 };
 
-// W words (of 32 bits) of a row held by a thread, VE elements to a load. Element i
-// of the thread is element ((i / VE) * 256 + tid) * VE + i % VE of the slice.
+// The larger of two words' elements, each by itself; a NaN gives way to a number (the sum meets it).
+template <typename T>
+__device__ __forceinline__ uint32_t max_words(uint32_t a, uint32_t b);
+template <>
+__device__ __forceinline__ uint32_t max_words<float>(uint32_t a, uint32_t b) {
+  return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+}
+template <>
+__device__ __forceinline__ uint32_t max_words<__nv_bfloat16>(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <>
+__device__ __forceinline__ uint32_t max_words<__half>(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// A slice of a row: W words (of 32 bits) to a thread, VE elements to a load. Element i of
+// thread t is element ((i / VE) * 256 + t) * VE + i % VE of the slice.
 template <typename T, int VE, int W>
-__global__ void __launch_bounds__(kNT, 4) k_beam_scan(BeamParams p) {
+__global__ void __launch_bounds__(kNT, W == 32 ? 4 : 8) k_beam_scan(BeamParams p) {
   constexpr int EPW = 4 / (int)sizeof(T), E = W * EPW;  // elements per word, per thread
   __shared__ float gmax[64];
-  __shared__ double wsum[8];
+  __shared__ uint64_t wsum[8];
+  __shared__ int bad;
   __shared__ uint64_t list[kList];
+  __shared__ uint16_t fours[kNT * (W / 4)];
   __shared__ float sT;
-  __shared__ int cnt;
+  __shared__ int cnt, nfour;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t row = blockIdx.x / p.splits;
-  const int64_t base = (int64_t)(blockIdx.x % p.splits) * (kNT * E);
+  const int64_t row = blockIdx.x / (unsigned)p.splits;
+  const int64_t base = (int64_t)(blockIdx.x % (unsigned)p.splits) * (kNT * E);
   const T* x = static_cast<const T*>(p.logits) + row * p.row_stride + base;
-  const int64_t left = p.vocab - base;  // elements from the slice's first on
-  if (tid == 0) cnt = 0;
+  const int left = (int)min(p.vocab - base, (int64_t)(kNT * E));  // elements of the slice
+  if (tid == 0) cnt = nfour = bad = 0;
+  cudaTriggerProgrammaticLaunchCompletion();  // k_beam_pick may be set up; it waits for this grid's end
 
   uint32_t w[W];
-  auto word_of = [&](int i) -> uint32_t {  // one element's bits, -inf past the end
-    const int64_t e = ((int64_t)(i / VE) * kNT + tid) * VE + i % VE;
+  auto at = [&](int i) { return ((i / VE) * kNT + tid) * VE + i % VE; };
+  auto bits_of = [&](int i) -> uint32_t {  // one element's bits, -inf past the end
+    const int e = at(i);
     if (e >= left) return Elem<T>::kNegInf;
     if (sizeof(T) == 4) return reinterpret_cast<const uint32_t*>(x)[e];
     return reinterpret_cast<const uint16_t*>(x)[e];
   };
   constexpr int WPV = VE / EPW;  // words per load (0: less than a word)
+  if (WPV > 0) {
 #pragma unroll
-  for (int j = 0; j < (WPV ? W / (WPV ? WPV : 1) : 0); ++j) {
-    const int64_t e0 = ((int64_t)j * kNT + tid) * VE;
-    if (e0 + VE <= left) {
-      if (WPV == 4) {
-        const uint4 v = __ldcs(reinterpret_cast<const uint4*>(x + e0));
-        w[j * 4] = v.x, w[j * 4 + 1] = v.y, w[j * 4 + 2] = v.z, w[j * 4 + 3] = v.w;
+    for (int j = 0; j < W / (WPV ? WPV : 1); ++j) {
+      const int e0 = (j * kNT + tid) * VE;
+      if (e0 + VE <= left) {
+        if (WPV == 4) {
+          const uint4 v = __ldcs(reinterpret_cast<const uint4*>(x + e0));
+          w[j * 4] = v.x, w[j * 4 + 1] = v.y, w[j * 4 + 2] = v.z, w[j * 4 + 3] = v.w;
+        } else {
+          w[j] = __ldcs(reinterpret_cast<const uint32_t*>(x + e0));
+        }
       } else {
-        w[j] = __ldcs(reinterpret_cast<const uint32_t*>(x + e0));
-      }
-    } else {
 #pragma unroll
-      for (int c = 0; c < WPV; ++c) {
-        const int i = (j * WPV + c) * EPW;
-        w[j * WPV + c] = EPW == 1 ? word_of(i) : (word_of(i) | (word_of(i + 1) << 16));
+        for (int c = 0; c < WPV; ++c) {
+          const int i = (j * WPV + c) * EPW;
+          w[j * WPV + c] = EPW == 1 ? bits_of(i) : (bits_of(i) | (bits_of(i + 1) << 16));
+        }
       }
     }
-  }
-  if (WPV == 0) {
+  } else {
 #pragma unroll
-    for (int c = 0; c < W; ++c) w[c] = word_of(2 * c) | (word_of(2 * c + 1) << 16);
+    for (int c = 0; c < W; ++c) w[c] = bits_of(2 * c) | (bits_of(2 * c + 1) << 16);
   }
 
-  float mx = -INFINITY;  // (fmaxf passes NaN over: the sum meets it)
+  uint32_t mw = w[0];
 #pragma unroll
-  for (int i = 0; i < E; ++i) mx = fmaxf(mx, Elem<T>::get(w, i));
+  for (int c = 1; c < W; ++c) mw = max_words<T>(mw, w[c]);
+  float mx = Elem<T>::get(&mw, 0);
+  if (EPW == 2) mx = fmaxf(mx, Elem<T>::get(&mw, EPW - 1));
+  if (!(mx >= -INFINITY)) mx = -INFINITY;  // (all NaN)
   mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
   mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
   if ((tid & 3) == 0) gmax[tid >> 2] = mx;
@@ -187,30 +220,59 @@ __global__ void __launch_bounds__(kNT, 4) k_beam_scan(BeamParams p) {
     rank += __shfl_xor_sync(0xffffffffu, rank, 2);
     if ((tid & 3) == 0 && rank == p.n_best - 1) sT = mine;
   }
-  __syncthreads();
-  const float T0 = sT;
   // A whole exponent of two not below the largest term's; nothing finite in the slice: any will do.
-  constexpr float kL2Ehi = 1.44269502162933349609375f, kL2Elo = 1.92596299e-8f;  // log2 e in two parts
   // Past 2^20 the exponents' own rounding would show: then relative to the largest logit itself.
   const bool byTop = top < INFINITY && top > -INFINITY && fabsf(top) > 1048576.0f;
   const float m = (!byTop && fabsf(top) < INFINITY) ? ceilf(__fmul_rn(top, kL2Ehi)) : 0.0f;
-  const float less = byTop ? top : 0.0f;
   float sum = 0.0f;
+  if (!byTop) {
+    f32x2 s2[2] = {0ull, 0ull};
+    const f32x2 hi2 = f2_dup(kL2Ehi), lo2 = f2_dup(kL2Elo), m2 = f2_dup(-m);
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const float v = Elem<T>::get(w, i);
-    const float d = __fsub_rn(v, less);  // (v itself, exactly, in the usual case; -inf stays -inf)
-    sum = __fadd_rn(sum, ex2(__fmaf_rn(d, kL2Elo, __fmaf_rn(d, kL2Ehi, -m))));
-    if (v >= T0 && v > -INFINITY) {
-      const int at = atomicAdd(&cnt, 1);
-      const int64_t e = ((int64_t)(i / VE) * kNT + tid) * VE + i % VE;
-      if (at < kList) list[at] = ((uint64_t)ordered(v) << 32) | (0xffffffffu - (uint32_t)(base + e));
+    for (int i = 0; i < E; i += 2) {
+      const f32x2 v = f2_pack(Elem<T>::get(w, i), Elem<T>::get(w, i + 1));
+      // (-inf: the first fma is -inf and the second keeps it)
+      float t0, t1;
+      f2_unpack(f2_fma(v, lo2, f2_fma(v, hi2, m2)), t0, t1);
+      s2[(i >> 1) & 1] = f2_add(s2[(i >> 1) & 1], f2_pack(ex2(t0), ex2(t1)));
+    }
+    float t0, t1;
+    f2_unpack(f2_add(s2[0], s2[1]), t0, t1);
+    sum = __fadd_rn(t0, t1);
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < E; ++i) {
+      if (at(i) >= left) continue;
+      const float d = __fsub_rn((float)x[at(i)], top);
+      sum = __fadd_rn(sum, ex2(__fmaf_rn(d, kL2Elo, __fmul_rn(d, kL2Ehi))));
     }
   }
-  double s = (double)sum;
+  __syncthreads();
+  // The few elements at or above the threshold, read again (they are in cache).
+  const float T0 = sT;
+  // Four words at a time; those with a hit are listed, and looked through by all threads together.
+  constexpr int G = 4 * EPW;
+#pragma unroll
+  for (int j = 0; j < W / 4; ++j) {
+    const uint32_t g = max_words<T>(max_words<T>(w[4 * j], w[4 * j + 1]), max_words<T>(w[4 * j + 2], w[4 * j + 3]));
+    const float v = fmaxf(Elem<T>::get(&g, 0), Elem<T>::get(&g, EPW - 1));
+    if (v >= T0 && v > -INFINITY) fours[atomicAdd(&nfour, 1)] = (uint16_t)(j * kNT + tid);
+  }
+  uint64_t s = __float2ull_rn(__fmul_rn(sum, 1099511627776.f));  // (a thread has at most 64 terms of at most 1)
 #pragma unroll
   for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if (lane == 0) wsum[warp] = s;
+  if (!(sum < 1e30f)) bad = 1;
+  __syncthreads();
+  for (int h = tid; h < nfour * G; h += kNT) {
+    const int f = fours[h / G], i = f / kNT * G + h % G;  // element i of thread f % kNT
+    const int e = ((i / VE) * kNT + f % kNT) * VE + i % VE;
+    const float v = e < left ? (float)x[e] : -INFINITY;
+    if (v >= T0 && v > -INFINITY) {
+      const int at1 = atomicAdd(&cnt, 1);
+      if (at1 < kList) list[at1] = key_of(v, base + e);
+    }
+  }
   __syncthreads();
   int n = cnt;
   if (n > kList) {
@@ -220,12 +282,10 @@ __global__ void __launch_bounds__(kNT, 4) k_beam_scan(BeamParams p) {
     for (int bit = 63; bit >= 0; --bit) {
       const uint64_t want = key | (1ull << bit);
       int c = 0;
-#pragma unroll
       for (int i = 0; i < E; ++i) {
-        const float v = Elem<T>::get(w, i);
-        const int64_t e = ((int64_t)(i / VE) * kNT + tid) * VE + i % VE;
-        const uint64_t u = ((uint64_t)ordered(v) << 32) | (0xffffffffu - (uint32_t)(base + e));
-        c += (v > -INFINITY && u >= want) ? 1 : 0;
+        const int e = at(i);
+        const float v = e < left ? (float)x[e] : -INFINITY;
+        c += (v > -INFINITY && key_of(v, base + e) >= want) ? 1 : 0;
       }
       c = __reduce_add_sync(0xffffffffu, c);
       if (tid == 0) above = 0;
@@ -237,14 +297,12 @@ __global__ void __launch_bounds__(kNT, 4) k_beam_scan(BeamParams p) {
     }
     if (tid == 0) cnt = 0;
     __syncthreads();
-#pragma unroll
     for (int i = 0; i < E; ++i) {
-      const float v = Elem<T>::get(w, i);
-      const int64_t e = ((int64_t)(i / VE) * kNT + tid) * VE + i % VE;
-      const uint64_t u = ((uint64_t)ordered(v) << 32) | (0xffffffffu - (uint32_t)(base + e));
-      if (v > -INFINITY && u >= key) {
-        const int at = atomicAdd(&cnt, 1);
-        if (at < kList) list[at] = u;
+      const int e = at(i);
+      const float v = e < left ? (float)x[e] : -INFINITY;
+      if (v > -INFINITY && key_of(v, base + e) >= key) {
+        const int at1 = atomicAdd(&cnt, 1);
+        if (at1 < kList) list[at1] = key_of(v, base + e);
       }
     }
     __syncthreads();
@@ -252,21 +310,21 @@ __global__ void __launch_bounds__(kNT, 4) k_beam_scan(BeamParams p) {
   }
   const Ws ws = carve(p.ws, p.batch * p.beams * p.splits);
   const int64_t l = blockIdx.x;
+  Cand* out = ws.cand + l * p.n_best;
   for (int c = tid; c < n; c += kNT) {
     const uint64_t mine = list[c];
     int rank = 0;
     for (int j = 0; j < n; ++j) rank += list[j] > mine ? 1 : 0;
-    if (rank < p.n_best)
-      ws.cand[l * p.n_best + rank] = Cand{unordered((uint32_t)(mine >> 32)), (int32_t)(0xffffffffu - (uint32_t)mine)};
+    if (rank < p.n_best) out[rank] = Cand{unordered((uint32_t)(mine >> 32)), (int32_t)(0xffffffffu - (uint32_t)mine)};
   }
+  for (int c = n + tid; c < p.n_best; c += kNT) out[c] = Cand{-INFINITY, 0};
   if (tid == 0) {
-    double t = wsum[0];
+    uint64_t t = 0;
 #pragma unroll
-    for (int j = 1; j < 8; ++j) t += wsum[j];
-    ws.sum[l] = t;
+    for (int j = 0; j < 8; ++j) t += wsum[j];
+    ws.sum[l] = bad ? kNotFinite : t;
     ws.exp2[l] = byTop ? kByTop : (int32_t)m;
     ws.top[l] = top;
-    ws.n[l] = min(n, p.n_best);
   }
 }
 
@@ -275,97 +333,185 @@ __device__ __forceinline__ bool before(uint64_t s1, uint32_t f1, uint64_t s2, ui
   return s1 > s2 || (s1 == s2 && f1 < f2);
 }
 
+// log of a positive finite s to about 1e-13 with few 64-bit steps (64-bit arithmetic is slow here, and the sums are
+// good to 1e-8): s = 2^k m, m in [0.703, 1.406); with r near 1/m from a table of 32, log m = log(1 + u) - log r,
+// u = r m - 1, |u| < 0.017, by its series (table-driven, after P. Tang, "Table-driven implementation of the logarithm
+// function", 1990).
+__constant__ double kLog[32][2] = {
+    {1.4003, -0.33668649937959438},
+    {1.3585, -0.3063811498842654},
+    {1.3192, -0.27702549226325202},
+    {1.2820, -0.24842135849847832},
+    {1.2469, -0.22066047102040334},
+    {1.2136, -0.19359114905218544},
+    {1.1821, -0.16729251777419415},
+    {1.1522, -0.1416731583161456},
+    {1.1237, -0.11662681193171956},
+    {1.0967, -0.092305670784026142},
+    {1.0708, -0.068406032664060368},
+    {1.0462, -0.045164551954373661},
+    {1.0227, -0.022446188829829995},
+    {1.0002, -0.00019998000266624471},
+    {0.9787, 0.021530118550363214},
+    {0.9581, 0.042803122325309445},
+    {0.9384, 0.063578981642871332},
+    {0.9194, 0.084033995610009446},
+    {0.9012, 0.10402807042404769},
+    {0.8837, 0.12363764045817827},
+    {0.8669, 0.14283164910754234},
+    {0.8507, 0.16169573900029838},
+    {0.8351, 0.18020380082295337},
+    {0.8200, 0.19845093872383832},
+    {0.8055, 0.216292076365108},
+    {0.7915, 0.23382539966107024},
+    {0.7780, 0.25102875480374542},
+    {0.7649, 0.26801017265431665},
+    {0.7522, 0.28475303294590104},
+    {0.7400, 0.30110509278392161},
+    {0.7282, 0.31717954324080405},
+    {0.7167, 0.3330979359822635}};
+__device__ __forceinline__ double log_of(double s) {
+  if (!(s > 0.0 && s < INFINITY)) return log(s);
+  int hi = __double2hiint(s), k = (hi >> 20) - 1023;
+  double m = __hiloint2double((hi & 0xfffff) | (1023 << 20), __double2loint(s));  // [1, 2)
+  if (m >= 1.40625) m *= 0.5, ++k;
+  const int i = min(31, (int)(((float)m - 0.703125f) * (32.0f / 0.703125f)));
+  const double u = fma(m, kLog[i][0], -1.0);
+  double t = fma(u, -1.0 / 6.0, 1.0 / 5.0);
+  t = fma(u, t, -1.0 / 4.0);
+  t = fma(u, t, 1.0 / 3.0);
+  t = fma(u, t, -0.5);
+  return fma((double)k, kLn2, kLog[i][1] + fma(u * u, t, u));
+}
+
 template <typename T>
 __device__ __forceinline__ bool is_masked(const BeamParams& p, int64_t row, int64_t t) {
   const T x = static_cast<const T*>(p.logits)[row * p.row_stride + t];
   return (float)x == -INFINITY;
 }
 
-// One CTA per request.
+// One CTA per request. It runs once through little data, so it is bound by latencies, those of its own
+// instructions' fetches among them: loops stay rolled.
 template <typename T>
 __global__ void __launch_bounds__(kNT) k_beam_pick(BeamParams p) {
   extern __shared__ __align__(16) unsigned char dyn[];
   uint64_t* ks = reinterpret_cast<uint64_t*>(dyn);
   uint32_t* kf = reinterpret_cast<uint32_t*>(dyn + 8 * kPick);
-  __shared__ double sum[kMaxBeams], sco[kMaxBeams];  // log-sum-exps (NaN: a dead hypothesis) and scores
+  Cand* sc = reinterpret_cast<Cand*>(dyn + 12 * kPick);  // the first kPick candidates
+  __shared__ double lse[kMaxBeams], sco[kMaxBeams], ref[kMaxBeams];  // log-sum-exps, scores
+  __shared__ uint64_t rsum[kMaxBeams];
+  __shared__ bool alive[kMaxBeams];
+  __shared__ float cut[kMaxBeams];
   __shared__ uint64_t hs[kNT], sT;
   __shared__ uint32_t hf[kNT];
-  __shared__ int cnt, total;
-  const int tid = threadIdx.x, M = p.n_best;
+  __shared__ int cnt;
+  const int tid = threadIdx.x, lane = tid & 31, M = p.n_best;
   const int64_t r = blockIdx.x;
+  const int NL = p.beams * p.splits, NC = NL * M;  // (below 2^27: a slice has 2,048 tokens at least)
+  const float mine = tid < p.beams ? p.scores[r * p.beams + tid] : 0.f;
+  if (tid == 0) cnt = 0, sT = 0;
+  cudaGridDependencySynchronize();
   const Ws ws = carve(p.ws, p.batch * p.beams * p.splits);
-  const int64_t l0 = r * p.beams * p.splits;  // the request's first list
-  const int64_t NL = (int64_t)p.beams * p.splits;
-  if (tid == 0) cnt = total = 0, sT = 0;
-  if (tid < p.beams) {
-    const int64_t l = l0 + (int64_t)tid * p.splits;
+  const int64_t l0 = r * NL;  // the request's first list
+  const Cand* gc = ws.cand + l0 * M;
+#pragma unroll 2
+  for (int e = tid; e < min(NC, kPick); e += kNT) sc[e] = gc[e];
+  // A warp joins a hypothesis' slices by shifts; the logarithms are then taken side by side in one warp.
+  for (int b = tid >> 5; b < p.beams; b += kNT / 32) {
+    const int64_t l = l0 + b * p.splits;
     int e = INT32_MIN;
-    for (int j = 0; j < p.splits; ++j)
-      if (ws.sum[l + j] != 0.0) e = max(e, ws.exp2[l + j]);
-    double s = 0.0, lse;
-    if (e != kByTop) {
-      for (int j = 0; j < p.splits; ++j)
-        if (ws.sum[l + j] != 0.0) s += ldexp(ws.sum[l + j], max(ws.exp2[l + j] - e, -4000));
-      lse = log(s) + (double)e * kLn2;
-    } else {
-      auto ref = [&](int64_t i) { return ws.exp2[i] == kByTop ? (double)ws.top[i] : ws.exp2[i] * kLn2; };
-      double most = -INFINITY;
-      for (int j = 0; j < p.splits; ++j)
-        if (ws.sum[l + j] != 0.0) most = fmax(most, ref(l + j));
-      for (int j = 0; j < p.splits; ++j)
-        if (ws.sum[l + j] != 0.0) s += ws.sum[l + j] * exp(ref(l + j) - most);
-      lse = log(s) + most;
+    bool nf = false;
+    for (int j = lane; j < p.splits; j += 32) {
+      const uint64_t x = ws.sum[l + j];
+      if (x) e = max(e, ws.exp2[l + j]);
+      nf |= x == kNotFinite;
     }
-    const double sc = (double)p.scores[r * p.beams + tid];
-    sum[tid] = (isfinite(lse) && isfinite(sc)) ? lse : (double)NAN;
-    sco[tid] = sc;
+    e = __reduce_max_sync(0xffffffffu, e);
+    uint64_t s = 0;
+    double base = 0.0;
+    if (e != kByTop) {
+      for (int j = lane; j < p.splits; j += 32) {
+        const uint64_t x = ws.sum[l + j];
+        if (x && e - ws.exp2[l + j] < 64) s += x >> (e - ws.exp2[l + j]);
+      }
+    } else {  // logits past 2^20
+      auto at = [&](int64_t i) { return ws.exp2[i] == kByTop ? (double)ws.top[i] : ws.exp2[i] * kLn2; };
+      base = -INFINITY;
+      for (int j = 0; j < p.splits; ++j)
+        if (ws.sum[l + j]) base = fmax(base, at(l + j));
+      for (int j = lane; j < p.splits; j += 32)
+        if (ws.sum[l + j]) s += (uint64_t)((double)ws.sum[l + j] * exp(at(l + j) - base));
+    }
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    nf = __any_sync(0xffffffffu, nf);
+    if (lane == 0) {
+      rsum[b] = nf ? 0 : s;
+      ref[b] = e == kByTop ? base : (double)e;
+      alive[b] = e == kByTop;  // for the next step
+    }
   }
   __syncthreads();
-  auto entry = [&](int64_t l, int j, uint64_t& s, uint32_t& f) -> bool {  // candidate j of list l
-    if (j >= ws.n[l0 + l]) return false;
-    const int b = (int)(l / p.splits);
-    if (isnan(sum[b])) return false;
-    const Cand c = ws.cand[(l0 + l) * M + j];
-    s = ordered(sco[b] + ((double)c.x - sum[b]));
+  if (tid < p.beams) {
+    const bool byTop = alive[tid];
+    const double x = log_of((double)rsum[tid] * 0x1p-40);  // (of zero: -inf)
+    lse[tid] = x + (byTop ? ref[tid] : ref[tid] * kLn2);
+    sco[tid] = (double)mine;
+    alive[tid] = isfinite(mine) && rsum[tid] != 0;
+  }
+  __syncthreads();
+  auto look = [&](int e, uint64_t& s, uint32_t& f) -> bool {  // candidate e % M of list e / M
+    const Cand c = e < kPick ? sc[e] : gc[e];
+    const int b = e / (M * p.splits);
+    if (!(c.x > -INFINITY) || !alive[b] || c.x < cut[b]) return false;
+    s = ordered(sco[b] + ((double)c.x - lse[b]));
     f = (uint32_t)((int64_t)b * p.vocab + c.t);
     return true;
   };
+  if (tid < p.beams) cut[tid] = -INFINITY;
+  __syncthreads();
   // A threshold with at least M candidates not below it: the M-th largest of the
   // threads' best among the lists' first candidates (first few, where there are
   // fewer lists than M).
-  const int first = (int)((M + NL - 1) / NL);
+  const int first = (M + NL - 1) / NL;
   uint64_t s, bs = 0;
   uint32_t f, bf = 0xffffffffu;
-  int live = 0;
-  for (int64_t e = tid; e < NL * first; e += kNT)
-    if (entry(e / first, (int)(e % first), s, f) && before(s, f, bs, bf)) bs = s, bf = f;
-  for (int64_t l = tid; l < NL; l += kNT)
-    if (!isnan(sum[l / p.splits])) live += min(ws.n[l0 + l], M);
+#pragma unroll 1
+  for (int h = tid; h < NL * first; h += kNT)
+    if (look(h / first * M + h % first, s, f) && before(s, f, bs, bf)) bs = s, bf = f;
   hs[tid] = bs;
   hf[tid] = bf;
-  atomicAdd(&total, min(live, 1 << 20));
   __syncthreads();
   if (bs) {
+    const int n = min(kNT, NL * first);
     int rank = 0;
-    for (int j = 0; j < kNT; ++j) rank += before(hs[j], hf[j], bs, bf) ? 1 : 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) rank += before(hs[j], hf[j], bs, bf) ? 1 : 0;
     if (rank == M - 1) sT = bs;
   }
   __syncthreads();
-  const int take = min(total, M);
   const uint64_t T0 = sT;  // 0: fewer than M threads have a candidate, so all are taken
-  for (int64_t e = tid; e < NL * M; e += kNT)
-    if (entry(e / M, (int)(e % M), s, f) && s >= T0) {
+  // Per hypothesis the logit that the threshold stands for, rounded down past every rounding of a score: most
+  // candidates are told by it without 64-bit arithmetic.
+  if (tid < p.beams && T0 && alive[tid]) {
+    const double t = unordered(T0), slack = 4e-15 * (fabs(t) + fabs(sco[tid]) + fabs(lse[tid]));
+    cut[tid] = __double2float_rd((t - sco[tid]) + lse[tid] - slack);
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int e = tid; e < NC; e += kNT)
+    if (look(e, s, f) && s >= T0) {
       const int at = atomicAdd(&cnt, 1);
       if (at < kPick) ks[at] = s, kf[at] = f;
     }
   __syncthreads();
+  const int take = min(cnt, M);
   float* os = p.out_scores + r * M;
   int32_t* op = p.out_parent + r * M;
   int32_t* ot = p.out_token + r * M;
   auto put = [&](int at, double score, uint32_t flat) {
     os[at] = (float)score;
-    op[at] = (int32_t)(flat / (uint64_t)p.vocab);
-    ot[at] = (int32_t)(flat % (uint64_t)p.vocab);
+    op[at] = (int32_t)(flat / (uint32_t)p.vocab);  // (beams x vocab < 2^31)
+    ot[at] = (int32_t)(flat % (uint32_t)p.vocab);
   };
   if (cnt <= kPick) {
     const int n = cnt;
@@ -373,6 +519,7 @@ __global__ void __launch_bounds__(kNT) k_beam_pick(BeamParams p) {
       const uint64_t ms = ks[c];
       const uint32_t mf = kf[c];
       int rank = 0;
+#pragma unroll 4
       for (int j = 0; j < n; ++j) rank += before(ks[j], kf[j], ms, mf) ? 1 : 0;
       if (rank < M) put(rank, unordered(ms), mf);
     }
@@ -383,8 +530,8 @@ __global__ void __launch_bounds__(kNT) k_beam_pick(BeamParams p) {
     bool any = false;
     for (int i = 0; i < take; ++i) {
       bs = 0, bf = 0xffffffffu;
-      for (int64_t e = tid; e < NL * M; e += kNT)
-        if (entry(e / M, (int)(e % M), s, f) && (!any || before(ls, lf, s, f)) && before(s, f, bs, bf)) bs = s, bf = f;
+      for (int e = tid; e < NC; e += kNT)
+        if (look(e, s, f) && (!any || before(ls, lf, s, f)) && before(s, f, bs, bf)) bs = s, bf = f;
       __syncthreads();
       hs[tid] = bs;
       hf[tid] = bf;
@@ -400,7 +547,7 @@ __global__ void __launch_bounds__(kNT) k_beam_pick(BeamParams p) {
   if (take < M && tid < 32) {
     int at = take;
     for (int b = 0; b < p.beams && at < M; ++b) {
-      const bool dead = isnan(sum[b]);
+      const bool dead = !alive[b];
       for (int64_t t0 = 0; t0 < p.vocab && at < M; t0 += 32) {
         const int64_t t = t0 + tid;
         const bool yes = t < p.vocab && (dead || is_masked<T>(p, r * p.beams + b, t));
@@ -416,7 +563,8 @@ __global__ void __launch_bounds__(kNT) k_beam_pick(BeamParams p) {
 template <typename T, int VE>
 cudaError_t scan(const BeamParams& p, cudaStream_t st) {
   const unsigned grid = (unsigned)(p.batch * p.beams * p.splits);
-  k_beam_scan<T, VE, 32><<<grid, kNT, 0, st>>>(p);
+  if (p.words == 32) k_beam_scan<T, VE, 32><<<grid, kNT, 0, st>>>(p);
+  else k_beam_scan<T, VE, 8><<<grid, kNT, 0, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -428,23 +576,45 @@ cudaError_t select(const BeamParams& p, cudaStream_t st) {
   if (a % 16 == 0) e = scan<T, 16 / (int)sizeof(T)>(p, st);
   else e = scan<T, 1>(p, st);
   if (e != cudaSuccess) return e;
-  constexpr int smem = 12 * kPick;
-  k_beam_pick<T><<<(unsigned)p.batch, kNT, smem, st>>>(p);
-  return cudaGetLastError();
+  // k_beam_pick is set up while the scan runs and waits for its end itself.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.batch);
+  cfg.blockDim = dim3(kNT);
+  cfg.dynamicSmemBytes = 20 * kPick;
+  cfg.stream = st;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_beam_pick<T>, p);
+}
+
+int64_t slices(int dtype, int64_t vocab, int words) {
+  const int64_t n = (int64_t)kNT * words * (dtype == LQ_F32 ? 1 : 2);
+  return (vocab + n - 1) / n;
 }
 
 }  // namespace
 
-// Elements of a slice: 32 words of 256 threads.
-int beam_splits(int dtype, int64_t vocab) {
-  const int64_t n = (int64_t)kNT * 32 * (dtype == LQ_F32 ? 1 : 2);
-  return (int)((vocab + n - 1) / n);
+// Words of a thread: 32 fill the registers and leave least to join; 8 where the rows are too few to give every SM
+// a CTA that way.
+void beam_plan(int dtype, int64_t rows, int64_t vocab, int* words, int64_t* splits) {
+  *words = rows * slices(dtype, vocab, 32) >= 152 ? 32 : 8;
+  *splits = slices(dtype, vocab, *words);
 }
 
-// Enough for any type: as many slices as fp32 logits take.
+// Enough for any type.
 size_t beam_workspace(int64_t batch, int beams, int64_t vocab, int n_best) {
-  const int64_t lists = batch * beams * beam_splits(LQ_F32, vocab);
-  return up256(8 * lists) + 3 * up256(4 * lists) + up256(sizeof(Cand) * lists * n_best);
+  int64_t most = 0;
+  for (int dtype : {LQ_F32, LQ_BF16}) {
+    int words;
+    int64_t n;
+    beam_plan(dtype, batch * beams, vocab, &words, &n);
+    if (n > most) most = n;
+  }
+  const int64_t lists = batch * beams * most;
+  return up256(8 * lists) + 2 * up256(4 * lists) + up256(sizeof(Cand) * lists * n_best);
 }
 
 cudaError_t launch_beam_select(const BeamParams& p, cudaStream_t st) {

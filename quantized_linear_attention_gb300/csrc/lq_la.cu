@@ -156,7 +156,10 @@ void la_plan(const lq_la_config* c, int64_t n_seqs, int64_t n_tokens, int64_t ma
   // Splitting reads k and v twice (1.5 times the bytes), so it pays where the longest
   // sequence alone takes longer than that: 1.6 shares.
   if (5 * longest <= 8 * share || longest <= 1024) return;
-  *seg = (share / 4 + 127) / 128 * 128;
+  // Two rounds of CTAs, less the last piece of each head, which is shorter: a piece costs about as much again as
+  // six chunks (32,768 tokens x 32 heads: four rounds 437 us, three 417, two 381).
+  const int64_t pieces = c->heads < 152 ? 304 - c->heads : 152;
+  *seg = (n_tokens * c->heads / pieces + 127) / 128 * 128;
   if (*seg < 512) *seg = 512;
   *slots = n_tokens / *seg + n_seqs;
 }

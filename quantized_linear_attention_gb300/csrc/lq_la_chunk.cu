@@ -808,7 +808,7 @@ __global__ void __launch_bounds__(256) k_la_scan(LaParams p) {
   if (p.S0) ld4(p.S0 + (b * p.heads + h) * (kD * kD) + at, s);
   float* w = p.ws_state + (first * p.heads + h) * (kD * kD) + at;
   const int64_t pitch = (int64_t)p.heads * (kD * kD);
-  constexpr int kAhead = 4;
+  constexpr int kAhead = 8;
   for (int64_t i = 0; i < n; i += kAhead) {
     float u[kAhead][4];
     double d[kAhead];
