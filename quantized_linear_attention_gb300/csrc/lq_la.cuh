@@ -109,6 +109,27 @@ __device__ __forceinline__ Piece find_piece(const LaParams& p, int64_t slot) {
   return r;
 }
 
+// A product of two numbers in two parts each (high + low), to about 2^-45.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  const float p = __fmul_rn(a.x, b.x);
+  const float e = __fmaf_rn(a.y, b.x, __fmaf_rn(a.x, b.y, __fmaf_rn(a.x, b.x, -p)));
+  const float h = __fadd_rn(p, e);
+  return make_float2(h, __fsub_rn(e, __fsub_rn(h, p)));
+}
+
+// The state before a piece: S0 (NULL: zero), or where a sequence is split what k_la_scan left in the piece's slot.
+__device__ __forceinline__ const float* start_state(const LaParams& p, const Piece& pc, int64_t slot, int h) {
+  if (pc.n > 1) return p.ws_state + (slot * p.heads + h) * (kD * kD);
+  return p.S0 ? p.S0 + (pc.b * p.heads + h) * (kD * kD) : nullptr;
+}
+
 cudaError_t launch_la_chunk_bf16(const LaParams& p, cudaStream_t st);
+
+// Split sequences: the states before the segments, from what the first pass left in the workspace.
+cudaError_t launch_la_scan(const LaParams& p, cudaStream_t st);
+// Split sequences whose last states replace S0: other segments may not have read it yet, so the second pass leaves
+// them in the workspace and launch_la_unstage copies them.
+inline bool la_staged(const LaParams& p) { return p.seg && p.S && p.S == p.S0; }
+cudaError_t launch_la_unstage(const LaParams& p, cudaStream_t st);
 
 }  // namespace lqi

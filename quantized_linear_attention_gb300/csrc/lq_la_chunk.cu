@@ -223,24 +223,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {  // to neare
   return r;
 }
 
-// A product of two numbers in two parts each (high + low), to about 2^-45.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  const float p = __fmul_rn(a.x, b.x);
-  const float e = __fmaf_rn(a.y, b.x, __fmaf_rn(a.x, b.y, __fmaf_rn(a.x, b.x, -p)));
-  const float h = __fadd_rn(p, e);
-  return make_float2(h, __fsub_rn(e, __fsub_rn(h, p)));
-}
-
 using bf16 = __nv_bfloat16;
 using PFN_encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// The state before a piece: S0 (NULL: zero), or where a sequence is split what k_la_scan left in the piece's slot.
-__device__ __forceinline__ const float* start_state(const LaParams& p, const Piece& pc, int64_t slot, int h) {
-  if (pc.n > 1) return p.ws_state + (slot * p.heads + h) * (kD * kD);
-  return p.S0 ? p.S0 + (pc.b * p.heads + h) * (kD * kD) : nullptr;
-}
 
 // Token by token: 512 threads, four lanes to a row, 32 columns each (as k_la_recurrent).
 // OUT: from the segment's start, with outputs; else from zero, the segment's own sum.
@@ -782,61 +768,6 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
   if (!OUT && tid == 0) p.ws_decay[slot * p.heads + h] = ms.prod[0] * ms.prod[1];
 }
 
-// Between the passes: each segment's growth becomes the state before it, S_{i+1} = decay_i S_i + growth_i from S0 on.
-// One thread per four entries; the segments of a sequence are read a few ahead.
-__global__ void __launch_bounds__(256) k_la_scan(LaParams p) {
-  __shared__ int64_t sfirst, sn;
-  const int h = blockIdx.y;
-  const int64_t b = blockIdx.z;
-  if (threadIdx.x < 32) {
-    int64_t first = 0, n = 1, begin, len;
-    for (int64_t x = threadIdx.x; x < b; x += 32) {
-      bounds(p, x, begin, len);
-      first += len > p.seg ? (len + p.seg - 1) / p.seg : 1;
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) first += __shfl_xor_sync(0xffffffffu, first, o);
-    bounds(p, b, begin, len);
-    if (len > p.seg) n = (len + p.seg - 1) / p.seg;
-    if (threadIdx.x == 0) sfirst = first, sn = n;
-  }
-  __syncthreads();
-  const int64_t first = sfirst, n = sn;
-  if (n == 1 || first + n > p.slots) return;
-  const int at = 4 * (blockIdx.x * 256 + threadIdx.x);
-  float s[4] = {0.f, 0.f, 0.f, 0.f};
-  if (p.S0) ld4(p.S0 + (b * p.heads + h) * (kD * kD) + at, s);
-  float* w = p.ws_state + (first * p.heads + h) * (kD * kD) + at;
-  const int64_t pitch = (int64_t)p.heads * (kD * kD);
-  constexpr int kAhead = 8;
-  for (int64_t i = 0; i < n; i += kAhead) {
-    float u[kAhead][4];
-    double d[kAhead];
-#pragma unroll
-    for (int x = 0; x < kAhead; ++x)
-      if (i + x < n - 1) {
-        ld4(w + (i + x) * pitch, u[x]);
-        d[x] = p.ws_decay[(first + i + x) * p.heads + h];
-      }
-#pragma unroll
-    for (int x = 0; x < kAhead; ++x) {
-      if (i + x < n) *reinterpret_cast<float4*>(w + (i + x) * pitch) = make_float4(s[0], s[1], s[2], s[3]);
-      if (i + x < n - 1) {
-        const float hi = (float)d[x], lo = (float)(d[x] - (double)hi);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] = __fmaf_rn(s[e], hi, __fmaf_rn(s[e], lo, u[x][e]));
-      }
-    }
-  }
-}
-
-// The states of split sequences that were staged in the workspace (last states that replace S0 in place).
-__global__ void k_copy_states(LaParams p, const float* from) {
-  const int64_t n = p.n_seqs * p.heads * (int64_t)(kD * kD / 4);
-  for (int64_t x = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; x < n; x += (int64_t)gridDim.x * blockDim.x)
-    reinterpret_cast<float4*>(p.S)[x] = reinterpret_cast<const float4*>(from)[x];
-}
-
 }  // namespace
 
 // A token array as a tensor of heads x 128 channels by tokens, read 64 channels by 128 tokens.
@@ -872,24 +803,16 @@ cudaError_t launch_la_chunk_bf16(const LaParams& p0, cudaStream_t st) {
     return e;
   const int64_t slots = p.seg ? p.slots : p.n_seqs;
   const unsigned grid = (unsigned)(slots * p.heads);
-  const bool staged = p.seg && p.S && p.S == p.S0;
   if (p.seg) {
     e = cudaFuncSetAttribute(k_la_chunk<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     k_la_chunk<false><<<grid, kThreadsLa, kSmem, st>>>(p, mq, mk, mv, mo);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    k_la_scan<<<dim3(kD * kD / 1024, (unsigned)p.heads, (unsigned)p.n_seqs), 256, 0, st>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if (staged) p.S = p.ws_last;
+    if ((e = cudaGetLastError()) != cudaSuccess || (e = launch_la_scan(p, st)) != cudaSuccess) return e;
   }
+  if (la_staged(p)) p.S = p.ws_last;
   k_la_chunk<true><<<grid, kThreadsLa, kSmem, st>>>(p, mq, mk, mv, mo);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (staged) {
-    p.S = p0.S;
-    k_copy_states<<<608, 256, 0, st>>>(p, p.ws_last);
-    e = cudaGetLastError();
-  }
-  return e;
+  return la_staged(p0) ? launch_la_unstage(p0, st) : cudaSuccess;
 }
 
 }  // namespace lqi
