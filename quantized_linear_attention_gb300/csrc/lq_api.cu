@@ -370,7 +370,7 @@ lqi::LaParams la_params(const lq_la_config* c, const void* q, const void* k, con
 // Split sequences: what each segment adds to the state, its decay, and the last states where they replace S0.
 size_t la_workspace(const lq_la_config* c, int64_t n_seqs, int64_t slots) {
   return align256((size_t)slots * c->heads * kD * kD * sizeof(float)) +
-         align256((size_t)slots * c->heads * sizeof(double)) +
+         align256((size_t)slots * c->heads * sizeof(float2)) +
          align256((size_t)n_seqs * c->heads * kD * kD * sizeof(float));
 }
 
@@ -750,8 +750,8 @@ int lq_la_prefill(const lq_la_config* cfg, int64_t n_seqs, int64_t n_tokens, int
   char* ws = static_cast<char*>(workspace);
   p.ws_state = reinterpret_cast<float*>(ws);
   ws += align256((size_t)p.slots * cfg->heads * kD * kD * sizeof(float));
-  p.ws_decay = reinterpret_cast<double*>(ws);
-  ws += align256((size_t)p.slots * cfg->heads * sizeof(double));
+  p.ws_decay = reinterpret_cast<float2*>(ws);
+  ws += align256((size_t)p.slots * cfg->heads * sizeof(float2));
   p.ws_last = reinterpret_cast<float*>(ws);
   return launched(lqi::launch_la_prefill(p, (cudaStream_t)stream), "lq_la_prefill launch");
 }

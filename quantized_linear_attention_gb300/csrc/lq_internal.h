@@ -129,7 +129,7 @@ struct LaParams {
   float* S;  // prefill: final states (may be NULL); decode step: states, in place
   void* o;
   float* ws_state;  // [slots][heads][128][128]: what a segment adds to the state
-  double* ws_decay; // [slots][heads]: the product of a segment's decays
+  float2* ws_decay; // [slots][heads]: the product of a segment's decays, in two parts
   float* ws_last;   // [n_seqs][heads][128][128]: last states on their way into S where that is S0
 };
 

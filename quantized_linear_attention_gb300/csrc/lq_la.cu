@@ -16,15 +16,15 @@ namespace {
 
 // --------------------------------------------------------------------------------------------
 // Prompts of fp32 and fp16 tokens, token by token in fp32: bound by the FMA units, 32,768
-// FMAs a token and head (256 cycles of an SM). One CTA of 256 threads per piece of a sequence and head; four
-// lanes hold two rows of the state, 32 columns each (float4 groups part, part + 4, ..: the four lanes read 64
-// consecutive bytes of a staged key), in packed pairs.
+// FMAs a token and head (256 cycles of an SM). One CTA of 256 threads per piece of a sequence and head; a thread
+// holds 8 x 8 entries of the state in packed pairs: 24 cycles of shared memory a warp and token (two rows of 32 took
+// 73, more than the FMAs).
 //
 // The decay would take a third multiplication per entry. It is kept apart instead: S = A s with one number A
-// for the whole state, s += (v / A) k^T, o = A (s q). Every 16 tokens A goes back into s, in two parts (rounded
+// for the whole state, s += (v / A) k^T, o = A (s q). Every 8 tokens A goes back into s, in two parts (rounded
 // to one it would be off in the same direction again and again), and so it does before a token at which it
 // would leave 2^-12 .. 2^12 (a decay of zero among them) or is not a number.
-constexpr int kRecTok = 16;  // tokens staged at a time
+constexpr int kRecTok = 8;  // tokens staged at a time
 
 struct RecTok {
   float hi, lo;  // what s is multiplied by before this token's update, where `now` is set
@@ -34,10 +34,12 @@ struct RecTok {
 
 template <typename T, bool OUT>
 __global__ void __launch_bounds__(256, 2) k_la_recurrent(LaParams p) {
-  __shared__ __align__(16) float sk[kRecTok][kD], sq[OUT ? kRecTok : 1][kD], sv[kRecTok][kD];
-  __shared__ RecTok tok[kRecTok + 1];
+  __shared__ __align__(16) float sk[2][kRecTok][kD], sq[2][OUT ? kRecTok : 1][kD], sv[2][kRecTok][kD];
+  __shared__ RecTok tok[2][kRecTok + 1];
+  __shared__ bool even[2];  // no token of the block needs A put back before it
+  __shared__ double sprod[8];
   __shared__ Piece spc;
-  const int tid = threadIdx.x, part = tid & 3, row = tid >> 2;  // and row + 64
+  const int tid = threadIdx.x, tx = tid & 15, row = 8 * (tid >> 4), warp = tid >> 5, lane = tid & 31;
   const int h = (int)(blockIdx.x % (unsigned)p.heads), kh = h / p.group;
   const int64_t slot = blockIdx.x / (unsigned)p.heads;
   if (tid < 32) {
@@ -54,140 +56,163 @@ __global__ void __launch_bounds__(256, 2) k_la_recurrent(LaParams p) {
   const T* v = static_cast<const T*>(p.v) + h * kD;
   T* o = static_cast<T*>(p.o) + h * kD;
 
-  f32x2 S[2][8][2];  // row + 64 x, columns 16 c + 4 part .. + 3
+  f32x2 S[8][4];  // row + x, columns 4 tx .. + 3 (pairs 0, 1) and 64 + 4 tx .. + 3 (pairs 2, 3)
   const float* from = OUT ? start_state(p, pc, slot, h) : nullptr;
 #pragma unroll
-  for (int x = 0; x < 2; ++x)
+  for (int x = 0; x < 8; ++x)
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
+    for (int c = 0; c < 2; ++c) {
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (from) y = *reinterpret_cast<const float4*>(from + (row + 64 * x) * kD + 16 * c + 4 * part);
-      S[x][c][0] = f2_pack(y.x, y.y);
-      S[x][c][1] = f2_pack(y.z, y.w);
+      if (from) y = *reinterpret_cast<const float4*>(from + (row + x) * kD + 64 * c + 4 * tx);
+      S[x][2 * c] = f2_pack(y.x, y.y);
+      S[x][2 * c + 1] = f2_pack(y.z, y.w);
     }
 
-  // Tokens of a block: thread tid takes channels 4 (tid & 31) .. of tokens tid / 32 and tid / 32 + 8.
-  float ld[2][3][4], la = 1.f;
+  // Tokens of a block: warp w takes token w of each, a lane four channels.
+  float ld[3][4];
   const int nb = (int)((pc.len + kRecTok - 1) / kRecTok);
   auto fetch = [&](int b) {
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int64_t t = (int64_t)b * kRecTok + (tid >> 5) + 8 * x;
-      if (t < pc.len) {
-        const int64_t at = pc.begin + t;
-        const int c = 4 * (tid & 31);
-        if (OUT) ld4(q + at * p.sq + c, ld[x][0]);
-        ld4(k + at * p.sk + c, ld[x][1]);
-        ld4(v + at * p.sv + c, ld[x][2]);
-      }
+    const int64_t t = (int64_t)b * kRecTok + warp, at = pc.begin + t;
+    if (t < pc.len) {
+      if (OUT) ld4(q + at * p.sq + 4 * lane, ld[0]);
+      ld4(k + at * p.sk + 4 * lane, ld[1]);
+      ld4(v + at * p.sv + 4 * lane, ld[2]);
     }
-    const int64_t t = (int64_t)b * kRecTok + tid;
-    if (tid < kRecTok) la = t < pc.len ? p.alpha[(pc.begin + t) * p.sa + h] : 1.f;
   };
+  auto stage = [&](int s) {
+    if (OUT) *reinterpret_cast<float4*>(&sq[s][OUT ? warp : 0][4 * lane]) = make_float4(ld[0][0], ld[0][1], ld[0][2], ld[0][3]);
+    *reinterpret_cast<float4*>(&sk[s][warp][4 * lane]) = make_float4(ld[1][0], ld[1][1], ld[1][2], ld[1][3]);
+    *reinterpret_cast<float4*>(&sv[s][warp][4 * lane]) = make_float4(ld[2][0], ld[2][1], ld[2][2], ld[2][3]);
+  };
+  // A from token to token of block b, in two parts: warp b mod 8, which has had the block's decays since its last turn.
   double prod = 1.0;
-  auto stage = [&]() {
+  auto decays = [&](int b) {
+    const int64_t t = (int64_t)b * kRecTok + lane;
+    return lane < kRecTok && t < pc.len ? p.alpha[(pc.begin + t) * p.sa + h] : 1.f;
+  };
+  float la = decays(warp);
+  auto prepare = [&](int b) {
+    const int s = b & 1;
+    const float one = la;
+    la = decays(b + 8);
+    float2 a = make_float2(one, 0.f);
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int t = (tid >> 5) + 8 * x, c = 4 * (tid & 31);
-      if (OUT) *reinterpret_cast<float4*>(&sq[OUT ? t : 0][c]) = make_float4(ld[x][0][0], ld[x][0][1], ld[x][0][2], ld[x][0][3]);
-      *reinterpret_cast<float4*>(&sk[t][c]) = make_float4(ld[x][1][0], ld[x][1][1], ld[x][1][2], ld[x][1][3]);
-      *reinterpret_cast<float4*>(&sv[t][c]) = make_float4(ld[x][2][0], ld[x][2][1], ld[x][2][2], ld[x][2][3]);
+    for (int d = 1; d < kRecTok; d <<= 1) {
+      const float2 y = make_float2(__shfl_up_sync(0xffffffffu, a.x, d), __shfl_up_sync(0xffffffffu, a.y, d));
+      if (lane >= d) a = mul2(a, y);
     }
-    if (tid < 32) {  // A from token to token, in two parts
-      const float one = tid < kRecTok ? la : 1.f;
-      float2 a = make_float2(one, 0.f);
-#pragma unroll
-      for (int d = 1; d < kRecTok; d <<= 1) {
-        const float2 y = make_float2(__shfl_up_sync(0xffffffffu, a.x, d), __shfl_up_sync(0xffffffffu, a.y, d));
-        if (tid >= d && tid < kRecTok) a = mul2(a, y);
+    const float g = fabsf(a.x);
+    if (__all_sync(0xffffffffu, lane >= kRecTok || (g > 2.44140625e-4f && g < 4096.f))) {
+      if (lane < kRecTok) tok[s][lane] = RecTok{1.f, 0.f, __fdiv_rn(1.f, a.x), a.x, 0};
+      if (lane == kRecTok - 1) tok[s][kRecTok] = RecTok{a.x, a.y, 1.f, 1.f, 1};
+      if (lane == 0) even[s] = true;
+    } else {
+      float2 A = make_float2(1.f, 0.f);
+      for (int t = 0; t < kRecTok; ++t) {
+        const float x = __shfl_sync(0xffffffffu, one, t);
+        const float2 f = fabsf(x) < INFINITY ? mul2(A, make_float2(x, 0.f)) : make_float2(x, 0.f);
+        const float m = fabsf(f.x);
+        const bool now = !(m > 2.44140625e-4f && m < 4096.f);
+        A = now ? make_float2(1.f, 0.f) : f;
+        if (lane == 0) tok[s][t] = RecTok{f.x, f.y, __fdiv_rn(1.f, A.x), A.x, now};
       }
-      const float g = fabsf(a.x);
-      if (__all_sync(0xffffffffu, tid >= kRecTok || (g > 2.44140625e-4f && g < 4096.f))) {
-        if (tid < kRecTok) tok[tid] = RecTok{1.f, 0.f, __fdiv_rn(1.f, a.x), a.x, 0};
-        if (tid == kRecTok - 1) tok[kRecTok] = RecTok{a.x, a.y, 1.f, 1.f, 1};
-      } else {
-        float2 A = make_float2(1.f, 0.f);
-        for (int t = 0; t < kRecTok; ++t) {
-          const float x = __shfl_sync(0xffffffffu, one, t);
-          float2 f = x == x && fabsf(x) < INFINITY ? mul2(A, make_float2(x, 0.f)) : make_float2(x, 0.f);
-          const float m = fabsf(f.x);
-          const bool now = !(m > 2.44140625e-4f && m < 4096.f);
-          A = now ? make_float2(1.f, 0.f) : f;
-          if (tid == 0) tok[t] = RecTok{f.x, f.y, __fdiv_rn(1.f, A.x), A.x, now};
-        }
-        if (tid == 0) tok[kRecTok] = RecTok{A.x, A.y, 1.f, 1.f, 1};
-      }
-      if (!OUT) {
-        for (int t = 0; t < kRecTok; ++t) prod *= (double)__shfl_sync(0xffffffffu, one, t);
-      }
+      if (lane == 0) tok[s][kRecTok] = RecTok{A.x, A.y, 1.f, 1.f, 1}, even[s] = false;
     }
+    if (!OUT)
+      for (int t = 0; t < kRecTok; ++t) prod *= (double)__shfl_sync(0xffffffffu, one, t);
   };
   auto scale = [&](float hi, float lo) {
     const f32x2 h2 = f2_dup(hi), l2 = f2_dup(lo);
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+    for (int x = 0; x < 8; ++x)
 #pragma unroll
-      for (int c = 0; c < 8; ++c)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) S[x][c][e] = f2_fma(S[x][c][e], h2, f2_mul(S[x][c][e], l2));
+      for (int c = 0; c < 4; ++c) S[x][c] = f2_fma(S[x][c], h2, f2_mul(S[x][c], l2));
   };
-  if (nb) fetch(0);
-  for (int b = 0; b < nb; ++b) {
-    const int n = (int)min((int64_t)kRecTok, pc.len - (int64_t)b * kRecTok);
-    stage();
-    __syncthreads();
-    if (b + 1 < nb) fetch(b + 1);
-#pragma unroll 1
-    for (int t = 0; t < n; ++t) {
-      const RecTok k0 = tok[t];
-      if (k0.now) scale(k0.hi, k0.lo);
-      const f32x2 v0 = f2_dup(__fmul_rn(sv[t][row], k0.inv)), v1 = f2_dup(__fmul_rn(sv[t][row + 64], k0.inv));
-      f32x2 a0 = 0ull, a1 = 0ull, b0 = 0ull, b1 = 0ull;
+  auto token = [&](int b, int s, int t) {
+    const float inv = tok[s][t].inv;
+    const ulonglong2 k0 = *reinterpret_cast<const ulonglong2*>(&sk[s][t][4 * tx]);
+    const ulonglong2 k1 = *reinterpret_cast<const ulonglong2*>(&sk[s][t][64 + 4 * tx]);
+    float v[8];
+    ld4(&sv[s][t][row], v);
+    ld4(&sv[s][t][row + 4], v + 4);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const ulonglong2 kk = *reinterpret_cast<const ulonglong2*>(&sk[t][16 * c + 4 * part]);
-        S[0][c][0] = f2_fma(v0, kk.x, S[0][c][0]);
-        S[0][c][1] = f2_fma(v0, kk.y, S[0][c][1]);
-        S[1][c][0] = f2_fma(v1, kk.x, S[1][c][0]);
-        S[1][c][1] = f2_fma(v1, kk.y, S[1][c][1]);
-        if (OUT) {
-          const ulonglong2 qq = *reinterpret_cast<const ulonglong2*>(&sq[OUT ? t : 0][16 * c + 4 * part]);
-          a0 = f2_fma(S[0][c][0], qq.x, a0);
-          a1 = f2_fma(S[0][c][1], qq.y, a1);
-          b0 = f2_fma(S[1][c][0], qq.x, b0);
-          b1 = f2_fma(S[1][c][1], qq.y, b1);
+    for (int x = 0; x < 8; ++x) {
+      const f32x2 w = f2_dup(__fmul_rn(v[x], inv));
+      S[x][0] = f2_fma(w, k0.x, S[x][0]);
+      S[x][1] = f2_fma(w, k0.y, S[x][1]);
+      S[x][2] = f2_fma(w, k1.x, S[x][2]);
+      S[x][3] = f2_fma(w, k1.y, S[x][3]);
+    }
+    if (OUT) {
+      const ulonglong2 q0 = *reinterpret_cast<const ulonglong2*>(&sq[s][OUT ? t : 0][4 * tx]);
+      const ulonglong2 q1 = *reinterpret_cast<const ulonglong2*>(&sq[s][OUT ? t : 0][64 + 4 * tx]);
+      float r[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const f32x2 a = f2_fma(S[x][2], q1.x, f2_mul(S[x][0], q0.x)), c = f2_fma(S[x][3], q1.y, f2_mul(S[x][1], q0.y));
+        float lo, hi;
+        f2_unpack(f2_add(a, c), lo, hi);
+        r[x] = __fadd_rn(lo, hi);
+      }
+      // sums over the 16 lanes of a row group, half of the rows changing hands at each step: lane tx ends with
+      // row tx / 2
+#pragma unroll
+      for (int w = 4; w; w >>= 1) {
+        const bool up = tx & (2 * w);
+#pragma unroll
+        for (int x = 0; x < w; ++x) {
+          const float keep = up ? r[w + x] : r[x], send = up ? r[x] : r[w + x];
+          r[x] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, send, 2 * w));
         }
       }
-      if (OUT) {
-        float x0, x1, y0, y1;
-        f2_unpack(f2_add(a0, a1), x0, x1);
-        f2_unpack(f2_add(b0, b1), y0, y1);
-        // lanes 0, 1 of the four end with row's sum, lanes 2, 3 with row + 64's
-        const bool up = part & 2;
-        const float mine = up ? __fadd_rn(y0, y1) : __fadd_rn(x0, x1);
-        const float other = up ? __fadd_rn(x0, x1) : __fadd_rn(y0, y1);
-        float r = __fadd_rn(mine, __shfl_xor_sync(0xffffffffu, other, 2));
-        r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, 1));
-        if (!(part & 1))
-          o[(pc.begin + (int64_t)b * kRecTok + t) * p.so + row + 64 * (part >> 1)] = from_f<T>(__fmul_rn(r, k0.a));
+      r[0] = __fadd_rn(r[0], __shfl_xor_sync(0xffffffffu, r[0], 1));
+      if (!(tx & 1))
+        o[(pc.begin + (int64_t)b * kRecTok + t) * p.so + row + (tx >> 1)] = from_f<T>(__fmul_rn(r[0], tok[s][t].a));
+    }
+  };
+  if (nb) {
+    fetch(0);
+    if (warp == 0) prepare(0);
+  }
+  for (int b = 0; b < nb; ++b) {
+    const int s = b & 1, n = (int)min((int64_t)kRecTok, pc.len - (int64_t)b * kRecTok);
+    stage(s);
+    __syncthreads();  // (whoever is here is through with block b - 1, so its buffer may be written after this)
+    if (b + 1 < nb) {
+      fetch(b + 1);
+      if (warp == ((b + 1) & 7)) prepare(b + 1);
+    }
+    if (n == kRecTok && even[s]) {
+#pragma unroll 2
+      for (int t = 0; t < kRecTok; ++t) token(b, s, t);
+    } else {
+#pragma unroll 1
+      for (int t = 0; t < n; ++t) {
+        if (tok[s][t].now) scale(tok[s][t].hi, tok[s][t].lo);
+        token(b, s, t);
       }
     }
-    const RecTok k0 = tok[kRecTok];
-    scale(k0.hi, k0.lo);
-    __syncthreads();
+    scale(tok[s][kRecTok].hi, tok[s][kRecTok].lo);
   }
   if (S_out) {
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+    for (int x = 0; x < 8; ++x)
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
+      for (int c = 0; c < 2; ++c) {
         float4 y;
-        f2_unpack(S[x][c][0], y.x, y.y);
-        f2_unpack(S[x][c][1], y.z, y.w);
-        *reinterpret_cast<float4*>(S_out + (row + 64 * x) * kD + 16 * c + 4 * part) = y;
+        f2_unpack(S[x][2 * c], y.x, y.y);
+        f2_unpack(S[x][2 * c + 1], y.z, y.w);
+        *reinterpret_cast<float4*>(S_out + (row + x) * kD + 64 * c + 4 * tx) = y;
       }
   }
-  if (!OUT && tid == 0) p.ws_decay[slot * p.heads + h] = prod;
+  if (!OUT) {
+    if (lane == 0) sprod[warp] = prod;
+    __syncthreads();
+    if (tid == 0) {
+      for (int w = 1; w < 8; ++w) prod *= sprod[w];
+      p.ws_decay[slot * p.heads + h] = in_two(prod);
+    }
+  }
 }
 
 // Between the passes: each segment's growth becomes the state before it, S_{i+1} = decay_i S_i + growth_i from S0 on.
@@ -219,7 +244,7 @@ __global__ void __launch_bounds__(256) k_la_scan(LaParams p) {
   constexpr int kAhead = 8;
   for (int64_t i = 0; i < n; i += kAhead) {
     float u[kAhead][4];
-    double d[kAhead];
+    float2 d[kAhead];
 #pragma unroll
     for (int x = 0; x < kAhead; ++x)
       if (i + x < n - 1) {
@@ -230,9 +255,8 @@ __global__ void __launch_bounds__(256) k_la_scan(LaParams p) {
     for (int x = 0; x < kAhead; ++x) {
       if (i + x < n) *reinterpret_cast<float4*>(w + (i + x) * pitch) = make_float4(s[0], s[1], s[2], s[3]);
       if (i + x < n - 1) {
-        const float hi = (float)d[x], lo = (float)(d[x] - (double)hi);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] = __fmaf_rn(s[e], hi, __fmaf_rn(s[e], lo, u[x][e]));
+        for (int e = 0; e < 4; ++e) s[e] = __fmaf_rn(s[e], d[x].x, __fmaf_rn(s[e], d[x].y, u[x][e]));
       }
     }
   }

@@ -117,6 +117,11 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return make_float2(h, __fsub_rn(e, __fsub_rn(h, p)));
 }
 
+__device__ __forceinline__ float2 in_two(double x) {
+  const float hi = (float)x;
+  return make_float2(hi, (float)(x - (double)hi));
+}
+
 // The state before a piece: S0 (NULL: zero), or where a sequence is split what k_la_scan left in the piece's slot.
 __device__ __forceinline__ const float* start_state(const LaParams& p, const Piece& pc, int64_t slot, int h) {
   if (pc.n > 1) return p.ws_state + (slot * p.heads + h) * (kD * kD);

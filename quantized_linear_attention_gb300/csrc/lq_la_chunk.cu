@@ -232,7 +232,7 @@ using PFN_encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, v
 // OUT: from the segment's start, with outputs; else from zero, the segment's own sum.
 template <bool OUT>
 __device__ __noinline__ void redo(const LaParams& p, const Piece& pc, int64_t slot, int h, float* sm, float* S_out,
-                                  double* decay) {
+                                  float2* decay) {
   const int tid = threadIdx.x, part = tid & 3, row = tid >> 2, kh = h / p.group;
   float(*sk)[kD] = reinterpret_cast<float(*)[kD]>(sm);
   float(*sq)[kD] = sk + 16;
@@ -296,7 +296,7 @@ __device__ __noinline__ void redo(const LaParams& p, const Piece& pc, int64_t sl
       *reinterpret_cast<float4*>(S_out + row * kD + 4 * (4 * c + part)) =
           make_float4(S[c][0], S[c][1], S[c][2], S[c][3]);
   }
-  if (decay && tid == 0) *decay = prod;
+  if (decay && tid == 0) *decay = in_two(prod);
 }
 
 // OUT: outputs and last states. Otherwise the first pass over split sequences: what a segment adds to the state.
@@ -757,7 +757,7 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
         static_cast<bf16*>(p.o)[(pc.begin + x / kD) * p.so + h * kD + x % kD] = bad;
     if (S_out)
       for (int x = tid; x < kD * kD; x += kThreadsLa) S_out[x] = __int_as_float(0x7fc00000);
-    if (!OUT && tid == 0) p.ws_decay[slot * p.heads + h] = 1.0;
+    if (!OUT && tid == 0) p.ws_decay[slot * p.heads + h] = make_float2(1.f, 0.f);
     return;
   }
   if (ms.flag) {
@@ -765,7 +765,7 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
               OUT ? nullptr : p.ws_decay + slot * p.heads + h);
     return;
   }
-  if (!OUT && tid == 0) p.ws_decay[slot * p.heads + h] = ms.prod[0] * ms.prod[1];
+  if (!OUT && tid == 0) p.ws_decay[slot * p.heads + h] = in_two(ms.prod[0] * ms.prod[1]);
 }
 
 }  // namespace
