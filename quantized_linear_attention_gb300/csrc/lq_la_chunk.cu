@@ -53,7 +53,7 @@ constexpr uint32_t kU = 0, kP = 128, kO = 256, kV3 = 384;  // kV3: two buffers o
 
 struct Misc {
   float2 gamma[4];
-  uint64_t land[2], full[2], empty[2], sums[2], oready[2], qk, qs, pv, pvok, ofree, sready, grown, vfull[2], vfree[2], drain;
+  uint64_t land[2], full[2], empty[2], sums[2], oready[2], qk, qs, pv, pvok, ofree, uread, sready, grown, vfull[2], vfree[2], drain;
   uint32_t tmem;
   int abort, flag;
   double prod[2];
@@ -344,6 +344,7 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
     mbar_init(&ms.pv, 1);
     mbar_init(&ms.pvok, 256);
     mbar_init(&ms.ofree, 256);
+    mbar_init(&ms.uread, 256);
     mbar_init(&ms.sready, 256);
     mbar_init(&ms.drain, 1);
     ms.abort = ms.flag = 0;
@@ -461,6 +462,9 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
       }
     }
     for (int c = 0; c <= nc; ++c) {
+      // With the sums comes gamma of this chunk, for the next round. (A barrier's phase has to be waited for before
+      // this warp lets the chunk go on: two chunks later it would be taken for the one before.)
+      if (c < nc && !wait_warp(&ms.sums[c & 1], (c >> 1) & 1, ab)) break;
       if (c) {  // S <- gamma S + U
         const float2 g = ms.gamma[(c - 1) & 3];
         const f32x2 g0 = f2_dup(g.x), g1 = f2_dup(g.y);
@@ -477,11 +481,10 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
             s = f2_fma(s, g0, f2_fma(s, g1, f2_bits(x[2 * e], x[2 * e + 1])));
           }
         }
+        tc_before();
       }
       if (c == nc) break;
-      // gamma of this chunk, for the next round (a barrier's phase has to be waited for before this warp lets the
-      // chunk go on: two chunks later it would be taken for the one before)
-      if (!wait_warp(&ms.sums[c & 1], (c >> 1) & 1, ab)) break;
+      arrive(&ms.uread);
       if (OUT) {
         char* s16 = la_smem + kS16 + half * 16384 + row * 128;
 #pragma unroll
@@ -496,9 +499,8 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
           *reinterpret_cast<uint4*>(s16 + ((e ^ (row & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
         }
         fence_proxy_async();
+        arrive(&ms.sready);
       }
-      tc_before();
-      arrive(&ms.sready);
     }
     f32x2 sum = 0ull;  // NaN where an entry is infinite or NaN
 #pragma unroll
@@ -666,72 +668,68 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
     // The products.
     const uint32_t tmu = __shfl_sync(0xffffffffu, tm, 0);
     const uint32_t S16 = ((sb + kS16) >> 4) | kByRow;
-    for (int c = 0; c < nc; ++c) {
-      const uint32_t at = (sb + (c & 1) * kStage) >> 4, next = (sb + ((c + 1) & 1) * kStage) >> 4;
-      const uint32_t Q = at | kByRow, K = (at + kTile / 16) | kByRow;
-      const uint32_t Kc = (at + kTile / 16) | kByChannel, Vc = (at + 2 * kTile / 16) | kByChannel;
-      if (c == 0 || !OUT) {
-        if (!wait_warp(&ms.full[c & 1], (c >> 1) & 1, ab)) break;
+    for (int c = -1; c < nc; ++c) {
+      const uint32_t at = (sb + (c & 1) * kStage) >> 4;
+      if (c >= 0) {
+        const uint32_t Q = at | kByRow, Kc = (at + kTile / 16) | kByChannel, Vc = (at + 2 * kTile / 16) | kByChannel;
+        if (!OUT && !wait_warp(&ms.full[c & 1], (c >> 1) & 1, ab)) break;
+        if (!wait_warp(&ms.uread, c & 1, ab)) break;
         tc_after();
-        if (OUT && elect()) {
-          product(tmu + kP, Q, K);
+        bool ok = true;
+#pragma unroll 1
+        for (int qt = 0; qt < 4; ++qt) {
+          const int buf = qt & 1, use = 2 * c + (qt >> 1);
+          if (OUT && qt == 2) {  // while quarter 2 is in the making
+            if (!(ok = wait_warp(&ms.sready, c & 1, ab))) break;
+            if (c && !(ok = wait_warp(&ms.ofree, (c - 1) & 1, ab))) break;
+            tc_after();
+            if (elect()) {
+              product(tmu + kO, Q, S16);
+              commit(&ms.qs);
+            }
+            __syncwarp();
+          }
+          if (!(ok = wait_warp(&ms.vfull[buf], use & 1, ab))) break;
+          tc_after();
+          if (elect()) {
+            const uint32_t a = tmu + kV3 + 48 * buf, b = Kc + 2 * qt * 128;
+            // the small parts first
+            if (qt == 0) mma_ts<false>(tmu + kU, a + 32, b, kIdescMn);
+            else mma_ts<true>(tmu + kU, a + 32, b, kIdescMn);
+            mma_ts<true>(tmu + kU, a + 40, b + 128, kIdescMn);
+#pragma unroll
+            for (int part = 1; part >= 0; --part)
+#pragma unroll
+              for (int s = 0; s < 2; ++s) mma_ts<true>(tmu + kU, a + 16 * part + 8 * s, b + 128 * s, kIdescMn);
+            commit(&ms.vfree[buf]);
+            if (qt == 3) commit(&ms.grown);
+            if (qt == 3 && !OUT) commit(&ms.empty[c & 1]);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (OUT) {  // while the state is brought up to date
+          if (!wait_warp(&ms.pvok, c & 1, ab)) break;
+          tc_after();
+          if (elect()) {
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+              mma_ts<true>(tmu + kO, tmu + kP + 64 * (s >> 2) + 8 * (s & 3), Vc + s * 128, kIdescMn);
+            commit(&ms.pv);
+            commit(&ms.empty[c & 1]);
+          }
+          __syncwarp();
+        }
+      }
+      if (OUT && c + 1 < nc) {  // the next chunk's scores: they follow P's last use in order
+        if (!wait_warp(&ms.full[(c + 1) & 1], ((c + 1) >> 1) & 1, ab)) break;
+        tc_after();
+        const uint32_t next = (sb + ((c + 1) & 1) * kStage) >> 4;
+        if (elect()) {
+          product(tmu + kP, next | kByRow, (next + kTile / 16) | kByRow);
           commit(&ms.qk);
         }
         __syncwarp();
-      }
-      if (!wait_warp(&ms.sready, c & 1, ab)) break;  // U has been read, S is in place
-      tc_after();
-      bool ok = true;
-#pragma unroll 1
-      for (int qt = 0; qt < 4; ++qt) {
-        const int buf = qt & 1, use = 2 * c + (qt >> 1);
-        if (OUT && qt == 2) {  // while quarter 2 is in the making
-          if (c && !(ok = wait_warp(&ms.ofree, (c - 1) & 1, ab))) break;
-          tc_after();
-          if (elect()) {
-            product(tmu + kO, Q, S16);
-            commit(&ms.qs);
-          }
-          __syncwarp();
-        }
-        if (!(ok = wait_warp(&ms.vfull[buf], use & 1, ab))) break;
-        tc_after();
-        if (elect()) {
-          const uint32_t a = tmu + kV3 + 48 * buf, b = Kc + 2 * qt * 128;
-          // the small parts first
-          if (qt == 0) mma_ts<false>(tmu + kU, a + 32, b, kIdescMn);
-          else mma_ts<true>(tmu + kU, a + 32, b, kIdescMn);
-          mma_ts<true>(tmu + kU, a + 40, b + 128, kIdescMn);
-#pragma unroll
-          for (int part = 1; part >= 0; --part)
-#pragma unroll
-            for (int s = 0; s < 2; ++s) mma_ts<true>(tmu + kU, a + 16 * part + 8 * s, b + 128 * s, kIdescMn);
-          commit(&ms.vfree[buf]);
-          if (qt == 3) commit(&ms.grown);
-          if (qt == 3 && !OUT) commit(&ms.empty[c & 1]);
-        }
-        __syncwarp();
-      }
-      if (!ok) break;
-      if (OUT) {  // while the state is brought up to date
-        if (!wait_warp(&ms.pvok, c & 1, ab)) break;
-        tc_after();
-        if (elect()) {
-#pragma unroll
-          for (int s = 0; s < 8; ++s)
-            mma_ts<true>(tmu + kO, tmu + kP + 64 * (s >> 2) + 8 * (s & 3), Vc + s * 128, kIdescMn);
-          commit(&ms.pv);
-          commit(&ms.empty[c & 1]);
-        }
-        __syncwarp();
-        if (c + 1 < nc) {  // the next chunk's scores: they follow P's last use in order
-          if (!wait_warp(&ms.full[(c + 1) & 1], ((c + 1) >> 1) & 1, ab)) break;
-          if (elect()) {
-            product(tmu + kP, next | kByRow, (next + kTile / 16) | kByRow);
-            commit(&ms.qk);
-          }
-          __syncwarp();
-        }
       }
     }
     // nothing may be in flight when TMEM is given back

@@ -36,19 +36,27 @@ __device__ __forceinline__ int read_parents(const int32_t* parent, int64_t g, in
   return sbad ? -1 : smove;
 }
 
-// Moves vectors [0, n) of a plane; beam b's part starts at base + b * pitch (in
-// vectors). lim (if not NULL): the vectors of beam b that move, by its source.
-template <int KM>
-__device__ __forceinline__ void move_plane(uint4* base, int64_t pitch, int n, const int* lim, int per, int K,
-                                           const int* sp) {
+// Where vector x of a head-state lies: beam 0's address, the distance from beam to beam in vectors, and how many
+// records a source must hold for the vector to be live (0: always).
+struct Place {
+  uint4* at;
+  int64_t pitch;
+  int live;
+};
+
+// Moves vectors [0, n) as `place` gives them: all loads of a thread come before its first store. One vector of
+// each beam at a time; two (for up to four beams) were slower, 126 us for 16,384 states against 107, by their registers.
+template <int KM, typename F>
+__device__ __forceinline__ void move_all(int n, F place, const int* sn, int K, const int* sp) {
   for (int x = threadIdx.x; x < n; x += blockDim.x) {
+    const Place pl = place(x);
     uint4 r[KM];
 #pragma unroll
     for (int b = 0; b < KM; ++b)
-      if (b < K && sp[b] != b && (!lim || x < lim[sp[b]] * per)) r[b] = base[sp[b] * pitch + x];
+      if (b < K && sp[b] != b && sn[sp[b]] >= pl.live) r[b] = pl.at[sp[b] * pl.pitch];
 #pragma unroll
     for (int b = 0; b < KM; ++b)
-      if (b < K && sp[b] != b && (!lim || x < lim[sp[b]] * per)) base[b * pitch + x] = r[b];
+      if (b < K && sp[b] != b && sn[sp[b]] >= pl.live) __stcs(pl.at + b * pl.pitch, r[b]);
   }
 }
 
@@ -81,21 +89,30 @@ __global__ void __launch_bounds__(256) k_reorder(Params p, ReorderParams r) {
   for (int b = 0; b < K; ++b)
     if (sp[b] != b) nmax = max(nmax, sn[sp[b]]);
 
-  auto plane = [&](void* base, int64_t vecs, int n, const int* lim, int per) {
-    move_plane<KM>(static_cast<uint4*>(base) + s0 * vecs, r.inner * vecs, n, lim, per, K, sp);
-  };
   const int cv = kD * kD * p.bits / 128;  // 16-byte vectors of a head-state's codes
   const int lv = p.C * kD / 4 * (p.comp_fit > 0 ? 2 : 1);
-  plane(p.codes, cv, cv, nullptr, 0);
-  plane(p.rec_k, p.W * (kD / 4), nmax * (kD / 4), sn, kD / 4);
-  plane(p.rec_u, p.W * (kD / 4), nmax * (kD / 4), sn, kD / 4);
-  if (lv) plane(p.comp_line, lv, lv, nullptr, 0);
-  plane(p.sigma, kD / 4, kD / 4, nullptr, 0);
-  plane(p.lambda, kD / 4, kD / 4, nullptr, 0);
-  plane(p.comp_id, p.comp_id_stride / 4, (int)(p.comp_id_stride / 4), nullptr, 0);
-  if (p.kda) {
-    plane(p.rec_alpha, p.W * (kD / 4), nmax * (kD / 4), sn, kD / 4);
-  } else if ((int)threadIdx.x < nmax) {  // one decay per record
+  const int iv = (int)(p.comp_id_stride / 4), rv = nmax * (kD / 4);
+  // codes, record keys and corrections (and decays per key), compensators, steps, scales, compensator ids
+  const int e0 = cv, e1 = e0 + rv, e2 = e1 + rv, e3 = e2 + (p.kda ? rv : 0), e4 = e3 + lv, e5 = e4 + kD / 4,
+            e6 = e5 + kD / 4, n = e6 + iv;
+  const int wv = p.W * (kD / 4);
+  auto in = [&](void* base, int vecs, int x, bool record) {
+    return Place{static_cast<uint4*>(base) + s0 * vecs + x, r.inner * vecs, record ? x / (kD / 4) + 1 : 0};
+  };
+  move_all<KM>(
+      n,
+      [&](int x) {
+        if (x < e0) return in(p.codes, cv, x, false);
+        if (x < e1) return in(p.rec_k, wv, x - e0, true);
+        if (x < e2) return in(p.rec_u, wv, x - e1, true);
+        if (x < e3) return in(p.rec_alpha, wv, x - e2, true);
+        if (x < e4) return in(p.comp_line, lv, x - e3, false);
+        if (x < e5) return in(p.sigma, kD / 4, x - e4, false);
+        if (x < e6) return in(p.lambda, kD / 4, x - e5, false);
+        return in(p.comp_id, iv, x - e6, false);
+      },
+      sn, K, sp);
+  if (!p.kda && (int)threadIdx.x < nmax) {  // one decay per record
     float a[KM];
     float* base = p.rec_alpha + s0 * p.alpha_stride + threadIdx.x;
     const int64_t pitch = r.inner * p.alpha_stride;
@@ -112,12 +129,15 @@ __global__ void __launch_bounds__(256) k_reorder(Params p, ReorderParams r) {
 
 template <int KM>
 __global__ void __launch_bounds__(256) k_fp32_reorder(float* S, ReorderParams r) {
-  __shared__ int sp[kMaxBeams];
+  __shared__ int sp[kMaxBeams], sn[kMaxBeams];
   const int K = r.beams;
   const int64_t i = blockIdx.x % r.inner, xg = blockIdx.x / r.inner, g = xg % r.groups;
+  if (threadIdx.x < kMaxBeams) sn[threadIdx.x] = 0;
   if (read_parents(r.parent, g, K, sp) <= 0) return;
   constexpr int nv = kD * kD / 4;
-  move_plane<KM>(reinterpret_cast<uint4*>(S) + (xg * K * r.inner + i) * nv, r.inner * nv, nv, nullptr, 0, K, sp);
+  uint4* base = reinterpret_cast<uint4*>(S) + (xg * K * r.inner + i) * nv;
+  const int64_t pitch = r.inner * nv;
+  move_all<KM>(nv, [&](int x) { return Place{base + x, pitch, 0}; }, sn, K, sp);
 }
 
 }  // namespace
