@@ -207,6 +207,13 @@ __device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int t, 
                : "memory");
 }
 
+__device__ __forceinline__ void ld_32bytes(const float* p, f32x2& a, f32x2& b, f32x2& c, f32x2& d) {
+  asm volatile("ld.global.v4.b64 {%0, %1, %2, %3}, [%4];" : "=l"(a), "=l"(b), "=l"(c), "=l"(d) : "l"(p) : "memory");
+}
+__device__ __forceinline__ void st_32bytes(float* p, f32x2 a, f32x2 b, f32x2 c, f32x2 d) {
+  asm volatile("st.global.v4.b64 [%0], {%1, %2, %3, %4};" ::"l"(p), "l"(a), "l"(b), "l"(c), "l"(d) : "memory");
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -312,23 +319,11 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
   if (warp == 0) {
     const Piece f = find_piece(p, slot);
     if (lane == 0) ms.piece[0] = f.b, ms.piece[1] = f.begin, ms.piece[2] = f.len, ms.piece[3] = f.i, ms.piece[4] = f.n;
-  }
-  __syncthreads();
-  Piece pc;
-  pc.b = ms.piece[0], pc.begin = ms.piece[1], pc.len = ms.piece[2], pc.i = ms.piece[3], pc.n = ms.piece[4];
-  if (pc.b < 0 || (!OUT && pc.i == pc.n - 1)) return;
-  const bool last = pc.i == pc.n - 1;
-  // Where the state after the piece goes.
-  float* S_out = OUT ? (last && p.S ? p.S + (pc.b * p.heads + h) * (kD * kD) : nullptr)
-                     : p.ws_state + (slot * p.heads + h) * (kD * kD);
-  const int nc = (int)((pc.len + kC - 1) / kC);
-
-  if (warp == 0) {
+  } else if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&ms.tmem))
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
-  if (tid == 32) {
+  } else if (tid == 64) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ms.land[i], 1);
       mbar_init(&ms.full[i], 1);
@@ -353,6 +348,18 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
   tc_before();
   __syncthreads();
   tc_after();
+  Piece pc;
+  pc.b = ms.piece[0], pc.begin = ms.piece[1], pc.len = ms.piece[2], pc.i = ms.piece[3], pc.n = ms.piece[4];
+  const bool last = pc.i == pc.n - 1;
+  if (pc.b < 0 || (!OUT && last)) {
+    if (warp == 1)
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(ms.tmem) : "memory");
+    return;
+  }
+  // Where the state after the piece goes.
+  float* S_out = OUT ? (last && p.S ? p.S + (pc.b * p.heads + h) * (kD * kD) : nullptr)
+                     : p.ws_state + (slot * p.heads + h) * (kD * kD);
+  const int nc = (int)((pc.len + kC - 1) / kC);
   const uint32_t tm = ms.tmem, sb = smem_u32(la_smem);
   float* sG = reinterpret_cast<float*>(la_smem + kSums);
   float* sw = sG + 2 * kC;
@@ -454,11 +461,19 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
     {
       const float* from = OUT ? start_state(p, pc, slot, h) : nullptr;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (from) x = *reinterpret_cast<const float4*>(from + row * kD + 64 * half + 4 * e);
-        S[2 * e] = f2_pack(x.x, x.y);
-        S[2 * e + 1] = f2_pack(x.z, x.w);
+      for (int e = 0; e < 32; ++e) S[e] = 0ull;
+      if (from) {  // a lane has a row: 32 bytes at a time where the address allows
+        from += row * kD + 64 * half;
+        if ((uintptr_t)from % 32 == 0) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) ld_32bytes(from + 2 * e, S[e], S[e + 1], S[e + 2], S[e + 3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(from + 2 * e);
+            S[e] = x.x, S[e + 1] = x.y;
+          }
+        }
       }
     }
     for (int c = 0; c <= nc; ++c) {
@@ -512,12 +527,12 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
     // (odd decays were flagged before their sums were handed over)
     if (S_out && !*reinterpret_cast<volatile int*>(&ms.flag) && !*reinterpret_cast<volatile int*>(ab)) {
       float* dst = S_out + row * kD + 64 * half;
+      if ((uintptr_t)dst % 32 == 0) {
 #pragma unroll
-      for (int e = 0; e < 32; e += 2) {
-        float4 x;
-        f2_unpack(S[e], x.x, x.y);
-        f2_unpack(S[e + 1], x.z, x.w);
-        *reinterpret_cast<float4*>(dst + 2 * e) = x;
+        for (int e = 0; e < 32; e += 4) st_32bytes(dst + 2 * e, S[e], S[e + 1], S[e + 2], S[e + 3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) *reinterpret_cast<ulonglong2*>(dst + 2 * e) = make_ulonglong2(S[e], S[e + 1]);
       }
     }
     regs_down<kRegs>();
@@ -746,7 +761,7 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
   tc_before();
   __syncthreads();
   tc_after();
-  if (warp == 0)
+  if (warp == 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
   if (ms.abort) {  // a wait gave up: make that visible (nothing of this CTA is in flight any more)
     const bf16 bad = __float2bfloat16_rn(__int_as_float(0x7fc00000));
