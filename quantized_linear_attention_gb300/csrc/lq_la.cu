@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "lq_device.cuh"
 #include "lq_internal.h"
 #include "lq_la.cuh"
@@ -17,8 +19,10 @@ namespace {
 // --------------------------------------------------------------------------------------------
 // Prompts of fp32 and fp16 tokens, token by token in fp32: bound by the FMA units, 32,768
 // FMAs a token and head (256 cycles of an SM). One CTA of 256 threads per piece of a sequence and head; a thread
-// holds 8 x 8 entries of the state in packed pairs: 24 cycles of shared memory a warp and token (two rows of 32 took
-// 73, more than the FMAs).
+// holds 8 x 8 entries of the state in packed pairs: 32 cycles of shared memory a warp and token (two rows of 32 took
+// 73, more than the FMAs). Values are staged divided by A, and with
+// outputs twice over, so that they load as pairs: copying each into a pair took the FMA pipe. (Without outputs that
+// would be more shared memory than the FMAs cover.)
 //
 // The decay would take a third multiplication per entry. It is kept apart instead: S = A s with one number A
 // for the whole state, s += (v / A) k^T, o = A (s q). Every 8 tokens A goes back into s, in two parts (rounded
@@ -34,10 +38,12 @@ struct RecTok {
 
 template <typename T, bool OUT>
 __global__ void __launch_bounds__(256, 2) k_la_recurrent(LaParams p) {
-  __shared__ __align__(16) float sk[2][kRecTok][kD], sq[2][OUT ? kRecTok : 1][kD], sv[2][kRecTok][kD];
-  __shared__ RecTok tok[2][kRecTok + 1];
-  __shared__ bool even[2];  // no token of the block needs A put back before it
-  __shared__ double sprod[8];
+  __shared__ __align__(16) float sk[2][kRecTok][kD], sq[2][OUT ? kRecTok : 1][kD];
+  using Val = typename std::conditional<OUT, f32x2, float>::type;
+  __shared__ __align__(16) Val sv[2][kRecTok][kD];
+  __shared__ RecTok tok[4][kRecTok + 1];
+  __shared__ bool even[4];  // no token of the block needs A put back before it
+  __shared__ float2 sprod[8];
   __shared__ Piece spc;
   const int tid = threadIdx.x, tx = tid & 15, row = 8 * (tid >> 4), warp = tid >> 5, lane = tid & 31;
   const int h = (int)(blockIdx.x % (unsigned)p.heads), kh = h / p.group;
@@ -79,20 +85,30 @@ __global__ void __launch_bounds__(256, 2) k_la_recurrent(LaParams p) {
       ld4(v + at * p.sv + 4 * lane, ld[2]);
     }
   };
-  auto stage = [&](int s) {
+  auto stage = [&](int b) {
+    const int s = b & 1;
+    const float inv = tok[b & 3][warp].inv;
     if (OUT) *reinterpret_cast<float4*>(&sq[s][OUT ? warp : 0][4 * lane]) = make_float4(ld[0][0], ld[0][1], ld[0][2], ld[0][3]);
     *reinterpret_cast<float4*>(&sk[s][warp][4 * lane]) = make_float4(ld[1][0], ld[1][1], ld[1][2], ld[1][3]);
-    *reinterpret_cast<float4*>(&sv[s][warp][4 * lane]) = make_float4(ld[2][0], ld[2][1], ld[2][2], ld[2][3]);
+    float x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = __fmul_rn(ld[2][e], inv);
+    if (OUT) {
+      *reinterpret_cast<float4*>(&sv[s][warp][4 * lane]) = make_float4(x[0], x[0], x[1], x[1]);
+      *reinterpret_cast<float4*>(&sv[s][warp][4 * lane + 2]) = make_float4(x[2], x[2], x[3], x[3]);
+    } else {
+      *reinterpret_cast<float4*>(&sv[s][warp][4 * lane]) = make_float4(x[0], x[1], x[2], x[3]);
+    }
   };
   // A from token to token of block b, in two parts: warp b mod 8, which has had the block's decays since its last turn.
-  double prod = 1.0;
+  float2 prod = make_float2(1.f, 0.f);
   auto decays = [&](int b) {
     const int64_t t = (int64_t)b * kRecTok + lane;
     return lane < kRecTok && t < pc.len ? p.alpha[(pc.begin + t) * p.sa + h] : 1.f;
   };
   float la = decays(warp);
   auto prepare = [&](int b) {
-    const int s = b & 1;
+    const int s = b & 3;
     const float one = la;
     la = decays(b + 8);
     float2 a = make_float2(one, 0.f);
@@ -119,7 +135,7 @@ __global__ void __launch_bounds__(256, 2) k_la_recurrent(LaParams p) {
       if (lane == 0) tok[s][kRecTok] = RecTok{A.x, A.y, 1.f, 1.f, 1}, even[s] = false;
     }
     if (!OUT)
-      for (int t = 0; t < kRecTok; ++t) prod *= (double)__shfl_sync(0xffffffffu, one, t);
+      prod = mul2(prod, make_float2(__shfl_sync(0xffffffffu, a.x, kRecTok - 1), __shfl_sync(0xffffffffu, a.y, kRecTok - 1)));
   };
   auto scale = [&](float hi, float lo) {
     const f32x2 h2 = f2_dup(hi), l2 = f2_dup(lo);
@@ -128,20 +144,27 @@ __global__ void __launch_bounds__(256, 2) k_la_recurrent(LaParams p) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) S[x][c] = f2_fma(S[x][c], h2, f2_mul(S[x][c], l2));
   };
-  auto token = [&](int b, int s, int t) {
-    const float inv = tok[s][t].inv;
+  T* out = o + pc.begin * p.so + row + (tx >> 1);
+  auto token = [&](int s, int t, float A) {
     const ulonglong2 k0 = *reinterpret_cast<const ulonglong2*>(&sk[s][t][4 * tx]);
     const ulonglong2 k1 = *reinterpret_cast<const ulonglong2*>(&sk[s][t][64 + 4 * tx]);
-    float v[8];
-    ld4(&sv[s][t][row], v);
-    ld4(&sv[s][t][row + 4], v + 4);
 #pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      const f32x2 w = f2_dup(__fmul_rn(v[x], inv));
-      S[x][0] = f2_fma(w, k0.x, S[x][0]);
-      S[x][1] = f2_fma(w, k0.y, S[x][1]);
-      S[x][2] = f2_fma(w, k1.x, S[x][2]);
-      S[x][3] = f2_fma(w, k1.y, S[x][3]);
+    for (int x = 0; x < 8; x += 2) {
+      ulonglong2 v;
+      if (OUT) {
+        v = *reinterpret_cast<const ulonglong2*>(&sv[s][t][row + x]);
+      } else {
+        const float2 y = *reinterpret_cast<const float2*>(&sv[s][t][row + x]);
+        v = make_ulonglong2(f2_dup(y.x), f2_dup(y.y));
+      }
+      S[x][0] = f2_fma(v.x, k0.x, S[x][0]);
+      S[x][1] = f2_fma(v.x, k0.y, S[x][1]);
+      S[x][2] = f2_fma(v.x, k1.x, S[x][2]);
+      S[x][3] = f2_fma(v.x, k1.y, S[x][3]);
+      S[x + 1][0] = f2_fma(v.y, k0.x, S[x + 1][0]);
+      S[x + 1][1] = f2_fma(v.y, k0.y, S[x + 1][1]);
+      S[x + 1][2] = f2_fma(v.y, k1.x, S[x + 1][2]);
+      S[x + 1][3] = f2_fma(v.y, k1.y, S[x + 1][3]);
     }
     if (OUT) {
       const ulonglong2 q0 = *reinterpret_cast<const ulonglong2*>(&sq[s][OUT ? t : 0][4 * tx]);
@@ -149,9 +172,8 @@ __global__ void __launch_bounds__(256, 2) k_la_recurrent(LaParams p) {
       float r[8];
 #pragma unroll
       for (int x = 0; x < 8; ++x) {
-        const f32x2 a = f2_fma(S[x][2], q1.x, f2_mul(S[x][0], q0.x)), c = f2_fma(S[x][3], q1.y, f2_mul(S[x][1], q0.y));
         float lo, hi;
-        f2_unpack(f2_add(a, c), lo, hi);
+        f2_unpack(f2_fma(S[x][3], q1.y, f2_fma(S[x][2], q1.x, f2_fma(S[x][1], q0.y, f2_mul(S[x][0], q0.x)))), lo, hi);
         r[x] = __fadd_rn(lo, hi);
       }
       // sums over the 16 lanes of a row group, half of the rows changing hands at each step: lane tx ends with
@@ -166,33 +188,33 @@ __global__ void __launch_bounds__(256, 2) k_la_recurrent(LaParams p) {
         }
       }
       r[0] = __fadd_rn(r[0], __shfl_xor_sync(0xffffffffu, r[0], 1));
-      if (!(tx & 1))
-        o[(pc.begin + (int64_t)b * kRecTok + t) * p.so + row + (tx >> 1)] = from_f<T>(__fmul_rn(r[0], tok[s][t].a));
+      if (!(tx & 1)) *out = from_f<T>(__fmul_rn(r[0], A));
+      out += p.so;
     }
   };
   if (nb) {
     fetch(0);
-    if (warp == 0) prepare(0);
+    if (warp < min(2, nb)) prepare(warp);
   }
+  __syncthreads();
   for (int b = 0; b < nb; ++b) {
     const int s = b & 1, n = (int)min((int64_t)kRecTok, pc.len - (int64_t)b * kRecTok);
-    stage(s);
-    __syncthreads();  // (whoever is here is through with block b - 1, so its buffer may be written after this)
-    if (b + 1 < nb) {
-      fetch(b + 1);
-      if (warp == ((b + 1) & 7)) prepare(b + 1);
-    }
-    if (n == kRecTok && even[s]) {
+    const RecTok* tk = tok[b & 3];
+    stage(b);
+    __syncthreads();  // (whoever is here is through with block b - 1, so its buffers may be written after this)
+    if (b + 1 < nb) fetch(b + 1);
+    if (b + 2 < nb && warp == ((b + 2) & 7)) prepare(b + 2);
+    if (n == kRecTok && even[b & 3]) {
 #pragma unroll 2
-      for (int t = 0; t < kRecTok; ++t) token(b, s, t);
+      for (int t = 0; t < kRecTok; ++t) token(s, t, tk[t].a);
     } else {
 #pragma unroll 1
       for (int t = 0; t < n; ++t) {
-        if (tok[s][t].now) scale(tok[s][t].hi, tok[s][t].lo);
-        token(b, s, t);
+        if (tk[t].now) scale(tk[t].hi, tk[t].lo);
+        token(s, t, tk[t].a);
       }
     }
-    scale(tok[s][kRecTok].hi, tok[s][kRecTok].lo);
+    scale(tk[kRecTok].hi, tk[kRecTok].lo);
   }
   if (S_out) {
 #pragma unroll
@@ -209,8 +231,8 @@ __global__ void __launch_bounds__(256, 2) k_la_recurrent(LaParams p) {
     if (lane == 0) sprod[warp] = prod;
     __syncthreads();
     if (tid == 0) {
-      for (int w = 1; w < 8; ++w) prod *= sprod[w];
-      p.ws_decay[slot * p.heads + h] = in_two(prod);
+      for (int w = 1; w < 8; ++w) prod = mul2(prod, sprod[w]);
+      p.ws_decay[slot * p.heads + h] = prod;
     }
   }
 }
