@@ -48,12 +48,15 @@ constexpr uint32_t kSums = kS16 + kTile;      // G[2][128], w[2][128]
 constexpr uint32_t kMisc = kSums + 2048;      // gammas, barriers
 constexpr uint32_t kSmem = kMisc + 512;
 static_assert(kSmem <= 232448, "shared memory of a CTA");
-// TMEM columns
-constexpr uint32_t kU = 0, kP = 128, kO = 256, kV3 = 384;  // kV3: two buffers of 3 parts x 16 columns (32 tokens)
+// TMEM columns. With outputs: U, P, O and two buffers for a quarter of wV (3 parts x 16 columns). Without: U twice, so
+// that its products run ahead of the state, and a buffer for each quarter.
+constexpr uint32_t kU = 0, kP = 128, kO = 256;
+template <bool OUT>
+constexpr uint32_t kV3 = OUT ? 384 : 256;
 
 struct Misc {
   float2 gamma[4];
-  uint64_t land[2], full[2], empty[2], sums[2], oready[2], qk, qs, pv, pvok, ofree, uread, sready, grown, vfull[2], vfree[2], drain;
+  uint64_t land[2], full[2], empty[2], sums[2], oready[2], qk, qs, pv, pvok, ofree, uread[2], sready, grown[2], vfull[4], vfree[4], drain;
   uint32_t tmem;
   int abort, flag;
   double prod[2];
@@ -330,16 +333,18 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
       mbar_init(&ms.empty[i], 1);
       mbar_init(&ms.sums[i], 32);
       mbar_init(&ms.oready[i], 256);
+      mbar_init(&ms.grown[i], 1);
+      mbar_init(&ms.uread[i], 256);
+    }
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&ms.vfull[i], 128);
       mbar_init(&ms.vfree[i], 1);
     }
     mbar_init(&ms.qk, 1);
     mbar_init(&ms.qs, 1);
-    mbar_init(&ms.grown, 1);
     mbar_init(&ms.pv, 1);
     mbar_init(&ms.pvok, 256);
     mbar_init(&ms.ofree, 256);
-    mbar_init(&ms.uread, 256);
     mbar_init(&ms.sready, 256);
     mbar_init(&ms.drain, 1);
     ms.abort = ms.flag = 0;
@@ -477,18 +482,19 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
       }
     }
     for (int c = 0; c <= nc; ++c) {
-      // With the sums comes gamma of this chunk, for the next round. (A barrier's phase has to be waited for before
-      // this warp lets the chunk go on: two chunks later it would be taken for the one before.)
-      if (c < nc && !wait_warp(&ms.sums[c & 1], (c >> 1) & 1, ab)) break;
+      // With the sums comes gamma of this chunk, for the next round.
+      if (c < nc && (OUT || c == 0) && !wait_warp(&ms.sums[c & 1], (c >> 1) & 1, ab)) break;
       if (c) {  // S <- gamma S + U
         const float2 g = ms.gamma[(c - 1) & 3];
         const f32x2 g0 = f2_dup(g.x), g1 = f2_dup(g.y);
-        if (!wait_warp(&ms.grown, (c - 1) & 1, ab)) break;  // (S's bf16 copy has been read by then, too)
+        // (S's bf16 copy has been read by then, too)
+        if (!wait_warp(&ms.grown[(c - 1) & 1], ((c - 1) >> 1) & 1, ab)) break;
+        const uint32_t U = tl + kU + 64 * half + (OUT ? 0 : 128 * ((c - 1) & 1));
         tc_after();
 #pragma unroll
         for (int blk = 0; blk < 4; ++blk) {
           uint32_t x[16];
-          tm_ld16(tl + kU + 64 * half + 16 * blk, x);
+          tm_ld16(U + 16 * blk, x);
           wait_ld();
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -499,7 +505,9 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
         tc_before();
       }
       if (c == nc) break;
-      arrive(&ms.uread);
+      // (without outputs the next chunk's products need no more than this arrival)
+      if (!OUT && c + 1 < nc && !wait_warp(&ms.sums[(c + 1) & 1], ((c + 1) >> 1) & 1, ab)) break;
+      arrive(&ms.uread[c & 1]);
       if (OUT) {
         char* s16 = la_smem + kS16 + half * 16384 + row * 128;
 #pragma unroll
@@ -539,12 +547,12 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
     roles_done();
   } else if (warp < 24) {
     // C: quarters (32 tokens) of a chunk, weighted and in three parts, as rows of the A operand: row 32 (warp & 3) +
-    // lane. Warps 16-19 take quarters 0 and 2, warps 20-23 quarters 1 and 3, each in a TMEM buffer of its own.
+    // lane. Warps 16-19 take quarters 0 and 2, warps 20-23 quarters 1 and 3.
     regs_down<kRegsC>();
     const int quad = warp & 3, set = (warp - 16) >> 2, row = 32 * quad + lane;
     const uint32_t Vrow = sb + 2 * kTile + (row >> 6) * 16384 + (row & 7) * 2;
     const uint32_t swz = ((row & 63) >> 3) << 4;  // 16-byte chunk of the row's channel, swizzled by the token mod 8
-    const uint32_t to = tm + ((uint32_t)(32 * quad) << 16) + kV3 + 48 * set;
+    const uint32_t to = tm + ((uint32_t)(32 * quad) << 16) + kV3<OUT>;
     for (int u = 0; u < 2 * nc; ++u) {
       const int c = u >> 1, qt = 2 * (u & 1) + set;
       if (!(u & 1)) {
@@ -566,14 +574,15 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
         p1[e] = __byte_perm((uint32_t)r, (uint32_t)(r >> 32), 0x7632);
         p2[e] = __byte_perm((uint32_t)d, (uint32_t)(d >> 32), 0x7632);
       }
-      if (u && !wait_warp(&ms.vfree[set], (u - 1) & 1, ab)) break;
+      const int buf = OUT ? set : qt, use = OUT ? u : c;
+      if (use && !wait_warp(&ms.vfree[buf], (use - 1) & 1, ab)) break;
       tc_after();
-      tm_st16(to, p0);
-      tm_st16(to + 16, p1);
-      tm_st16(to + 32, p2);
+      tm_st16(to + 48 * buf, p0);
+      tm_st16(to + 48 * buf + 16, p1);
+      tm_st16(to + 48 * buf + 32, p2);
       wait_st();
       tc_before();
-      arrive(&ms.vfull[set]);
+      arrive(&ms.vfull[buf]);
     }
     roles_done();
     regs_up<kRegs>();
@@ -688,12 +697,16 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
       if (c >= 0) {
         const uint32_t Q = at | kByRow, Kc = (at + kTile / 16) | kByChannel, Vc = (at + 2 * kTile / 16) | kByChannel;
         if (!OUT && !wait_warp(&ms.full[c & 1], (c >> 1) & 1, ab)) break;
-        if (!wait_warp(&ms.uread, c & 1, ab)) break;
+        // U is free: read up to the last chunk's, or, where there are two, the one's before. (Chunk 0 waits as well, so
+        // that no chunk is through before B has seen its sums.)
+        const int r = OUT ? c : max(c - 1, 0);
+        if (!wait_warp(&ms.uread[r & 1], (r >> 1) & 1, ab)) break;
         tc_after();
+        const uint32_t U = tmu + kU + (OUT ? 0 : 128 * (c & 1));
         bool ok = true;
 #pragma unroll 1
         for (int qt = 0; qt < 4; ++qt) {
-          const int buf = qt & 1, use = 2 * c + (qt >> 1);
+          const int buf = OUT ? qt & 1 : qt, use = OUT ? 2 * c + (qt >> 1) : c;
           if (OUT && qt == 2) {  // while quarter 2 is in the making
             if (!(ok = wait_warp(&ms.sready, c & 1, ab))) break;
             if (c && !(ok = wait_warp(&ms.ofree, (c - 1) & 1, ab))) break;
@@ -707,17 +720,17 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
           if (!(ok = wait_warp(&ms.vfull[buf], use & 1, ab))) break;
           tc_after();
           if (elect()) {
-            const uint32_t a = tmu + kV3 + 48 * buf, b = Kc + 2 * qt * 128;
+            const uint32_t a = tmu + kV3<OUT> + 48 * buf, b = Kc + 2 * qt * 128;
             // the small parts first
-            if (qt == 0) mma_ts<false>(tmu + kU, a + 32, b, kIdescMn);
-            else mma_ts<true>(tmu + kU, a + 32, b, kIdescMn);
-            mma_ts<true>(tmu + kU, a + 40, b + 128, kIdescMn);
+            if (qt == 0) mma_ts<false>(U, a + 32, b, kIdescMn);
+            else mma_ts<true>(U, a + 32, b, kIdescMn);
+            mma_ts<true>(U, a + 40, b + 128, kIdescMn);
 #pragma unroll
             for (int part = 1; part >= 0; --part)
 #pragma unroll
-              for (int s = 0; s < 2; ++s) mma_ts<true>(tmu + kU, a + 16 * part + 8 * s, b + 128 * s, kIdescMn);
+              for (int s = 0; s < 2; ++s) mma_ts<true>(U, a + 16 * part + 8 * s, b + 128 * s, kIdescMn);
             commit(&ms.vfree[buf]);
-            if (qt == 3) commit(&ms.grown);
+            if (qt == 3) commit(&ms.grown[c & 1]);
             if (qt == 3 && !OUT) commit(&ms.empty[c & 1]);
           }
           __syncwarp();
