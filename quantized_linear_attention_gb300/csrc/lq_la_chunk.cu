@@ -42,12 +42,21 @@ constexpr int kThreadsLa = 896;
 // thing and take them back only after B has (roles_done), so each increase finds what it needs.
 constexpr int kRegs = 72, kRegsA = 64, kRegsB = 96, kRegsC = 64, kRegsRest = 48;
 constexpr uint32_t kTile = 32768;             // 128 x 128 bf16: two halves of 64 channels, 128-byte rows, swizzled
-constexpr uint32_t kStage = 3 * kTile;        // Q, K, V
-constexpr uint32_t kS16 = 2 * kStage;         // the state in bf16
+constexpr uint32_t kS16 = 6 * kTile;          // the state in bf16
 constexpr uint32_t kSums = kS16 + kTile;      // G[2][128], w[2][128]
 constexpr uint32_t kMisc = kSums + 2048;      // gammas, barriers
 constexpr uint32_t kSmem = kMisc + 512;
 static_assert(kSmem <= 232448, "shared memory of a CTA");
+// The stages of tiles below kS16: two of Q, K, V with outputs, else three of K, V (with two, the next chunk but one
+// was asked for too late: 2.2 us a chunk of 64 KB).
+template <bool OUT>
+struct Tiles {
+  static constexpr int kN = OUT ? 2 : 3;
+  static constexpr uint32_t kK = OUT ? kTile : 0, kV = kK + kTile, kStage = kV + kTile;
+  static __device__ __forceinline__ int at(int c) { return c % kN; }
+  static __device__ __forceinline__ uint32_t phase(int c) { return (uint32_t)(c / kN) & 1u; }
+  static __device__ __forceinline__ uint32_t offset(int c) { return (uint32_t)at(c) * kStage; }
+};
 // TMEM columns. With outputs: U, P, O and two buffers for a quarter of wV (3 parts x 16 columns). Without: U twice, so
 // that its products run ahead of the state, and a buffer for each quarter.
 constexpr uint32_t kU = 0, kP = 128, kO = 256;
@@ -56,7 +65,7 @@ constexpr uint32_t kV3 = OUT ? 384 : 256;
 
 struct Misc {
   float2 gamma[4];
-  uint64_t land[2], full[2], empty[2], sums[2], oready[2], qk, qs, pv, pvok, ofree, uread[2], sready, grown[2], vfull[4], vfree[4], drain;
+  uint64_t land[3], full[3], empty[3], sums[2], oready[2], qk, qs, pv, pvok, ofree, uread[2], sready, grown[2], vfull[4], vfree[4], drain;
   uint32_t tmem;
   int abort, flag;
   double prod[2];
@@ -328,13 +337,15 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   } else if (tid == 64) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ms.land[i], 1);
-      mbar_init(&ms.full[i], 1);
-      mbar_init(&ms.empty[i], 1);
       mbar_init(&ms.sums[i], 32);
       mbar_init(&ms.oready[i], 256);
       mbar_init(&ms.grown[i], 1);
       mbar_init(&ms.uread[i], 256);
+    }
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&ms.land[i], 1);
+      mbar_init(&ms.full[i], 1);
+      mbar_init(&ms.empty[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&ms.vfull[i], 128);
@@ -369,8 +380,52 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
   float* sG = reinterpret_cast<float*>(la_smem + kSums);
   float* sw = sG + 2 * kC;
   int* ab = &ms.abort;
+  using Ti = Tiles<OUT>;
 
-  if (warp < 8) {
+  if (OUT ? warp >= 16 && warp < 24 : warp < 8 || (warp >= 16 && warp < 24)) {
+    // C: quarters (32 tokens) of a chunk, weighted and in three parts, as rows of the A operand: row 32 (warp & 3) +
+    // lane. Warps 16-19 take quarters 0 and 2, warps 20-23 quarters 1 and 3; without outputs A's warps help, and each
+    // four have one quarter.
+    regs_down<kRegsC>();
+    constexpr int kSteps = OUT ? 2 : 1;  // quarters of a chunk for a warp
+    const int quad = warp & 3, set = warp < 8 ? 2 + (warp >> 2) : (warp - 16) >> 2, row = 32 * quad + lane;
+    const uint32_t Vrow = sb + Ti::kV + (row >> 6) * 16384 + (row & 7) * 2;
+    const uint32_t swz = ((row & 63) >> 3) << 4;  // 16-byte chunk of the row's channel, swizzled by the token mod 8
+    const uint32_t to = tm + ((uint32_t)(32 * quad) << 16) + kV3<OUT> + 48 * set;
+    for (int u = 0; u < kSteps * nc; ++u) {
+      const int c = u / kSteps, qt = 2 * (u % kSteps) + set;
+      if (u % kSteps == 0) {
+        if (!wait_warp(&ms.sums[c & 1], (c >> 1) & 1, ab)) break;
+        if (!wait_warp(&ms.full[Ti::at(c)], Ti::phase(c), ab)) break;
+      }
+      const uint32_t V = Vrow + Ti::offset(c) + qt * 4096;
+      const float* w = sw + (c & 1) * kC + 32 * qt;
+      uint32_t p0[16], p1[16], p2[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const ulonglong2 w2 = *reinterpret_cast<const ulonglong2*>(w + 4 * (e / 2));
+        const uint32_t v0 = lds_u16(V + 256 * e + (swz ^ (((2 * e) & 7) << 4)));
+        const uint32_t v1 = lds_u16(V + 256 * e + 128 + (swz ^ (((2 * e + 1) & 7) << 4)));
+        // two tokens at once; the top 8 bits, the next 8, the last 8: each difference is exact
+        const f32x2 x = f2_mul(f2_bits(v0 << 16, v1 << 16), e & 1 ? w2.y : w2.x);
+        const f32x2 r = f2_sub(x, x & 0xffff0000ffff0000ull);
+        const f32x2 d = f2_sub(r, r & 0xffff0000ffff0000ull);
+        p0[e] = __byte_perm((uint32_t)x, (uint32_t)(x >> 32), 0x7632);
+        p1[e] = __byte_perm((uint32_t)r, (uint32_t)(r >> 32), 0x7632);
+        p2[e] = __byte_perm((uint32_t)d, (uint32_t)(d >> 32), 0x7632);
+      }
+      if (u && !wait_warp(&ms.vfree[set], (u - 1) & 1, ab)) break;
+      tc_after();
+      tm_st16(to, p0);
+      tm_st16(to + 16, p1);
+      tm_st16(to + 32, p2);
+      wait_st();
+      tc_before();
+      arrive(&ms.vfull[set]);
+    }
+    roles_done();
+    regs_up<kRegs>();
+  } else if (warp < 8) {
     regs_down<kRegsA>();
     if (OUT) {
       // A: row i = 32 (warp & 3) + lane of the chunk, columns 64 half .. 64 half + 63
@@ -428,7 +483,7 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
         if (!wait_warp(&ms.pv, c & 1, ab)) break;
         tc_after();
         // o goes out by way of Q's tile, which nothing reads any more: rows of 128 bytes, swizzled as Q's were
-        char* tile = la_smem + (c & 1) * kStage + half * 16384;
+        char* tile = la_smem + Ti::offset(c) + half * 16384;
 #pragma unroll 1
         for (int blk = 0; blk < 4; ++blk) {
           uint32_t x[16];
@@ -545,47 +600,6 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
     }
     regs_down<kRegs>();
     roles_done();
-  } else if (warp < 24) {
-    // C: quarters (32 tokens) of a chunk, weighted and in three parts, as rows of the A operand: row 32 (warp & 3) +
-    // lane. Warps 16-19 take quarters 0 and 2, warps 20-23 quarters 1 and 3.
-    regs_down<kRegsC>();
-    const int quad = warp & 3, set = (warp - 16) >> 2, row = 32 * quad + lane;
-    const uint32_t Vrow = sb + 2 * kTile + (row >> 6) * 16384 + (row & 7) * 2;
-    const uint32_t swz = ((row & 63) >> 3) << 4;  // 16-byte chunk of the row's channel, swizzled by the token mod 8
-    const uint32_t to = tm + ((uint32_t)(32 * quad) << 16) + kV3<OUT>;
-    for (int u = 0; u < 2 * nc; ++u) {
-      const int c = u >> 1, qt = 2 * (u & 1) + set;
-      if (!(u & 1)) {
-        if (!wait_warp(&ms.sums[c & 1], (c >> 1) & 1, ab)) break;
-        if (!wait_warp(&ms.full[c & 1], (c >> 1) & 1, ab)) break;
-      }
-      const uint32_t V = Vrow + (c & 1) * kStage + qt * 4096;
-      const float* w = sw + (c & 1) * kC + 32 * qt;
-      uint32_t p0[16], p1[16], p2[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const uint32_t v0 = lds_u16(V + 256 * e + (swz ^ (((2 * e) & 7) << 4)));
-        const uint32_t v1 = lds_u16(V + 256 * e + 128 + (swz ^ (((2 * e + 1) & 7) << 4)));
-        // two tokens at once; the top 8 bits, the next 8, the last 8: each difference is exact
-        const f32x2 x = f2_mul(f2_bits(v0 << 16, v1 << 16), *reinterpret_cast<const f32x2*>(w + 2 * e));
-        const f32x2 r = f2_sub(x, x & 0xffff0000ffff0000ull);
-        const f32x2 d = f2_sub(r, r & 0xffff0000ffff0000ull);
-        p0[e] = __byte_perm((uint32_t)x, (uint32_t)(x >> 32), 0x7632);
-        p1[e] = __byte_perm((uint32_t)r, (uint32_t)(r >> 32), 0x7632);
-        p2[e] = __byte_perm((uint32_t)d, (uint32_t)(d >> 32), 0x7632);
-      }
-      const int buf = OUT ? set : qt, use = OUT ? u : c;
-      if (use && !wait_warp(&ms.vfree[buf], (use - 1) & 1, ab)) break;
-      tc_after();
-      tm_st16(to + 48 * buf, p0);
-      tm_st16(to + 48 * buf + 16, p1);
-      tm_st16(to + 48 * buf + 32, p2);
-      wait_st();
-      tc_before();
-      arrive(&ms.vfull[buf]);
-    }
-    roles_done();
-    regs_up<kRegs>();
   } else {
   regs_down<kRegsRest>();
   if (warp == 24) {
@@ -593,16 +607,16 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
     // zero in K and V (a weight of zero does not stop an infinity; Q's only reach rows that are not written).
     // Full chunks of o leave from Q's tile before the next Q comes in.
     int issued = 0;
-    for (int c = 0; c < nc + 2; ++c) {
-      const int s = c & 1, n = (int)min((int64_t)kC, pc.len - (int64_t)c * kC);  // (n <= 0: nothing more comes in)
-      const uint32_t dst = sb + s * kStage;
+    for (int c = 0; c < nc + Ti::kN; ++c) {
+      const int s = Ti::at(c), n = (int)min((int64_t)kC, pc.len - (int64_t)c * kC);  // (n <= 0: nothing more comes in)
+      const uint32_t dst = sb + Ti::offset(c);
       const int t0 = (int)(pc.begin + (int64_t)c * kC);
       uint64_t* bar = n == kC ? &ms.full[s] : &ms.land[s];
-      if (c >= 2 && c - 2 < nc && !wait_warp(&ms.empty[s], ((c - 2) >> 1) & 1, ab)) break;
+      if (c >= Ti::kN && !wait_warp(&ms.empty[s], Ti::phase(c - Ti::kN), ab)) break;
       if (n > 0 && lane == 0) {
-        mbar_expect_tx(bar, OUT ? kStage : 2 * kTile);
-        for (int x = 0; x < 2; ++x) tma_tile(dst + kTile + 16384 * x, &mk, kh * kD + 64 * x, t0, bar);
-        for (int x = 0; x < 2; ++x) tma_tile(dst + 2 * kTile + 16384 * x, &mv, h * kD + 64 * x, t0, bar);
+        mbar_expect_tx(bar, Ti::kStage);
+        for (int x = 0; x < 2; ++x) tma_tile(dst + Ti::kK + 16384 * x, &mk, kh * kD + 64 * x, t0, bar);
+        for (int x = 0; x < 2; ++x) tma_tile(dst + Ti::kV + 16384 * x, &mv, h * kD + 64 * x, t0, bar);
       }
       if (n > 0) issued = c + 1;
       if (OUT && c >= 2 && pc.len >= (int64_t)(c - 1) * kC) {  // chunk c - 2 is a full one
@@ -618,7 +632,7 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
       __syncwarp();
       if (n > 0 && n < kC) {
         if (!wait_warp(&ms.land[s], 0, ab)) break;
-        uint4* tile = reinterpret_cast<uint4*>(la_smem + s * kStage + kTile);
+        uint4* tile = reinterpret_cast<uint4*>(la_smem + Ti::offset(c) + Ti::kK);
         for (int x = lane; x < (kC - n) * 32; x += 32)  // 8 chunks of 16 bytes x 4 half tiles a row
           tile[((x >> 3) & 3) * 1024 + (n + (x >> 5)) * 8 + (x & 7)] = make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async();
@@ -631,9 +645,9 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
     // for, the barrier cannot complete: that wait runs into its limit.)
     int ignored = 0;
     if (*reinterpret_cast<volatile int*>(ab))
-      for (int c = max(0, issued - 2); c < issued; ++c) {
+      for (int c = max(0, issued - Ti::kN); c < issued; ++c) {
         const bool whole = pc.len >= (int64_t)(c + 1) * kC;
-        wait(whole ? &ms.full[c & 1] : &ms.land[c & 1], whole ? (c >> 1) & 1 : 0, &ignored);
+        wait(whole ? &ms.full[Ti::at(c)] : &ms.land[Ti::at(c)], whole ? Ti::phase(c) : 0, &ignored);
       }
   } else if (warp < 27) {
     // Sums of log2 alpha in whole numbers of 2^-40, four tokens to a lane. A decay of
@@ -680,7 +694,7 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
         G[e] = __fmul_rn(__ll2float_rn(g[e]), 9.094947017729282e-13f);
         w[e] = exp2f(__fmul_rn(__ll2float_rn(end - g[e]), 9.094947017729282e-13f));
       }
-      if (c >= 2 && !wait_warp(&ms.empty[c & 1], ((c - 2) >> 1) & 1, ab)) break;
+      if (c >= 2 && !wait_warp(&ms.empty[Ti::at(c - 2)], Ti::phase(c - 2), ab)) break;
       *reinterpret_cast<float4*>(sG + (c & 1) * kC + 4 * lane) = make_float4(G[0], G[1], G[2], G[3]);
       *reinterpret_cast<float4*>(sw + (c & 1) * kC + 4 * lane) = make_float4(w[0], w[1], w[2], w[3]);
       if (lane == 0) ms.gamma[c & 3] = gm;
@@ -693,10 +707,10 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
     const uint32_t tmu = __shfl_sync(0xffffffffu, tm, 0);
     const uint32_t S16 = ((sb + kS16) >> 4) | kByRow;
     for (int c = -1; c < nc; ++c) {
-      const uint32_t at = (sb + (c & 1) * kStage) >> 4;
       if (c >= 0) {
-        const uint32_t Q = at | kByRow, Kc = (at + kTile / 16) | kByChannel, Vc = (at + 2 * kTile / 16) | kByChannel;
-        if (!OUT && !wait_warp(&ms.full[c & 1], (c >> 1) & 1, ab)) break;
+        const uint32_t at = (sb + Ti::offset(c)) >> 4;
+        const uint32_t Q = at | kByRow, Kc = (at + Ti::kK / 16) | kByChannel, Vc = (at + Ti::kV / 16) | kByChannel;
+        if (!OUT && !wait_warp(&ms.full[Ti::at(c)], Ti::phase(c), ab)) break;
         // U is free: read up to the last chunk's, or, where there are two, the one's before. (Chunk 0 waits as well, so
         // that no chunk is through before B has seen its sums.)
         const int r = OUT ? c : max(c - 1, 0);
@@ -731,7 +745,7 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
               for (int s = 0; s < 2; ++s) mma_ts<true>(U, a + 16 * part + 8 * s, b + 128 * s, kIdescMn);
             commit(&ms.vfree[buf]);
             if (qt == 3) commit(&ms.grown[c & 1]);
-            if (qt == 3 && !OUT) commit(&ms.empty[c & 1]);
+            if (qt == 3 && !OUT) commit(&ms.empty[Ti::at(c)]);
           }
           __syncwarp();
         }
@@ -744,17 +758,17 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
             for (int s = 0; s < 8; ++s)
               mma_ts<true>(tmu + kO, tmu + kP + 64 * (s >> 2) + 8 * (s & 3), Vc + s * 128, kIdescMn);
             commit(&ms.pv);
-            commit(&ms.empty[c & 1]);
+            commit(&ms.empty[Ti::at(c)]);
           }
           __syncwarp();
         }
       }
       if (OUT && c + 1 < nc) {  // the next chunk's scores: they follow P's last use in order
-        if (!wait_warp(&ms.full[(c + 1) & 1], ((c + 1) >> 1) & 1, ab)) break;
+        if (!wait_warp(&ms.full[Ti::at(c + 1)], Ti::phase(c + 1), ab)) break;
         tc_after();
-        const uint32_t next = (sb + ((c + 1) & 1) * kStage) >> 4;
+        const uint32_t next = (sb + Ti::offset(c + 1)) >> 4;
         if (elect()) {
-          product(tmu + kP, next | kByRow, (next + kTile / 16) | kByRow);
+          product(tmu + kP, next | kByRow, (next + Ti::kK / 16) | kByRow);
           commit(&ms.qk);
         }
         __syncwarp();
