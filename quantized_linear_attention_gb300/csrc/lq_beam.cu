@@ -38,6 +38,7 @@ constexpr int kNT = 256;
 constexpr double kLn2 = 0.693147180559945309417;
 constexpr float kL2Ehi = 1.44269502162933349609375f, kL2Elo = 1.92596299e-8f;  // log2 e in two parts
 constexpr int kList = 512;   // candidates a slice collects before ranking
+constexpr int kFours = 256;  // groups of four words with one among them
 constexpr int kPick = 2048;  // candidates a request collects before ranking
 
 struct Cand {
@@ -149,7 +150,8 @@ __global__ void __launch_bounds__(kNT, W == 32 ? 4 : 8) k_beam_scan(BeamParams p
   __shared__ uint64_t wsum[8];
   __shared__ int bad;
   __shared__ uint64_t list[kList];
-  __shared__ uint16_t fours[kNT * (W / 4)];
+  __shared__ uint4 fourw[kFours];
+  __shared__ uint16_t fours[kFours];
   __shared__ float sT;
   __shared__ int cnt, nfour;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -256,7 +258,13 @@ __global__ void __launch_bounds__(kNT, W == 32 ? 4 : 8) k_beam_scan(BeamParams p
   for (int j = 0; j < W / 4; ++j) {
     const uint32_t g = max_words<T>(max_words<T>(w[4 * j], w[4 * j + 1]), max_words<T>(w[4 * j + 2], w[4 * j + 3]));
     const float v = fmaxf(Elem<T>::get(&g, 0), Elem<T>::get(&g, EPW - 1));
-    if (v >= T0 && v > -INFINITY) fours[atomicAdd(&nfour, 1)] = (uint16_t)(j * kNT + tid);
+    if (v >= T0 && v > -INFINITY) {
+      const int f = atomicAdd(&nfour, 1);
+      if (f < kFours) {
+        fours[f] = (uint16_t)(j * kNT + tid);
+        fourw[f] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+      }
+    }
   }
   uint64_t s = __float2ull_rn(__fmul_rn(sum, 1099511627776.f));  // (a thread has at most 64 terms of at most 1)
 #pragma unroll
@@ -264,10 +272,10 @@ __global__ void __launch_bounds__(kNT, W == 32 ? 4 : 8) k_beam_scan(BeamParams p
   if (lane == 0) wsum[warp] = s;
   if (!(sum < 1e30f)) bad = 1;
   __syncthreads();
-  for (int h = tid; h < nfour * G; h += kNT) {
+  for (int h = tid; h < min(nfour, kFours) * G; h += kNT) {
     const int f = fours[h / G], i = f / kNT * G + h % G;  // element i of thread f % kNT
     const int e = ((i / VE) * kNT + f % kNT) * VE + i % VE;
-    const float v = e < left ? (float)x[e] : -INFINITY;
+    const float v = (float)reinterpret_cast<const T*>(fourw)[h];
     if (v >= T0 && v > -INFINITY) {
       const int at1 = atomicAdd(&cnt, 1);
       if (at1 < kList) list[at1] = key_of(v, base + e);
@@ -275,7 +283,7 @@ __global__ void __launch_bounds__(kNT, W == 32 ? 4 : 8) k_beam_scan(BeamParams p
   }
   __syncthreads();
   int n = cnt;
-  if (n > kList) {
+  if (n > kList || nfour > kFours) {
     // Too many at or above the group threshold: the largest key with at least n_best keys not below it, bit by bit.
     __shared__ int above;
     uint64_t key = 0;
