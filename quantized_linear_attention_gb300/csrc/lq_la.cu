@@ -239,10 +239,9 @@ __global__ void __launch_bounds__(256, 2) k_la_recurrent(LaParams p) {
 
 // Between the passes: each segment's growth becomes the state before it, S_{i+1} = decay_i S_i + growth_i from S0 on.
 // One thread per four entries; the segments of a sequence are read a few ahead.
-__global__ void __launch_bounds__(256) k_la_scan(LaParams p) {
+__device__ __forceinline__ void scan_sequence(const LaParams& p, int64_t b, int h) {
   __shared__ int64_t sfirst, sn;
-  const int h = blockIdx.y;
-  const int64_t b = blockIdx.z;
+  __syncthreads();
   if (threadIdx.x < 32) {
     int64_t first = 0, n = 1, begin, len;
     for (int64_t x = threadIdx.x; x < b; x += 32) {
@@ -282,6 +281,10 @@ __global__ void __launch_bounds__(256) k_la_scan(LaParams p) {
       }
     }
   }
+}
+
+__global__ void __launch_bounds__(256) k_la_scan(LaParams p) {
+  for (int64_t b = blockIdx.z; b < p.n_seqs; b += gridDim.z) scan_sequence(p, b, blockIdx.y);
 }
 
 // The states of split sequences that were staged in the workspace (last states that replace S0 in place).
@@ -372,7 +375,8 @@ cudaError_t step(const LaParams& p, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_la_scan(const LaParams& p, cudaStream_t st) {
-  k_la_scan<<<dim3(kD * kD / 1024, (unsigned)p.heads, (unsigned)p.n_seqs), 256, 0, st>>>(p);
+  const unsigned z = (unsigned)(p.n_seqs < 65535 ? p.n_seqs : 65535);
+  k_la_scan<<<dim3(kD * kD / 1024, (unsigned)p.heads, z), 256, 0, st>>>(p);
   return cudaGetLastError();
 }
 

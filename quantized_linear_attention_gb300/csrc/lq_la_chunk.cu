@@ -839,13 +839,11 @@ cudaError_t launch_la_chunk_bf16(const LaParams& p0, cudaStream_t st) {
                      (e = tile_map(&mv, p.v, p.heads, p.sv, p.n_tokens)) != cudaSuccess ||
                      (e = tile_map(&mo, p.o, p.heads, p.so, p.n_tokens)) != cudaSuccess))
     return e;
-  if ((e = cudaFuncSetAttribute(k_la_chunk<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) != cudaSuccess)
-    return e;
+  if ((e = set_smem(k_la_chunk<true>, kSmem)) != cudaSuccess) return e;
   const int64_t slots = p.seg ? p.slots : p.n_seqs;
   const unsigned grid = (unsigned)(slots * p.heads);
   if (p.seg) {
-    e = cudaFuncSetAttribute(k_la_chunk<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
+    if ((e = set_smem(k_la_chunk<false>, kSmem)) != cudaSuccess) return e;
     k_la_chunk<false><<<grid, kThreadsLa, kSmem, st>>>(p, mq, mk, mv, mo);
     if ((e = cudaGetLastError()) != cudaSuccess || (e = launch_la_scan(p, st)) != cudaSuccess) return e;
   }
