@@ -27,7 +27,8 @@
  *     and creates no streams or events.
  *   - Pointers: device pointers on the current CUDA device (device or managed
  *     memory). Token inputs and outputs are contiguous fp32 arrays, 16-byte
- *     aligned; the state buffer is 256-byte aligned.
+ *     aligned (the generation calls at the end say what they take); the state
+ *     buffer is 256-byte aligned.
  *   - Layout of token inputs: [n_states][d] row-major, state index
  *     s = (request * layers + layer) * heads + head, or any order the caller
  *     keeps fixed.
@@ -375,8 +376,12 @@ size_t lq_la_workspace_bytes(const lq_la_config* cfg, int64_t n_seqs, int64_t n_
  * that only o needs are taken to that type's accuracy).
  * A token's value, however large, infinite or NaN, reaches its own and later tokens
  * of its sequence only. Tokens that belong to no sequence get no output. o must not
- * overlap an input. Errors: LQ_ERR_INVALID_ARG, LQ_ERR_UNSUPPORTED; nothing is
- * reported from the device.
+ * overlap an input. Sequences must not overlap one another. Errors:
+ * LQ_ERR_INVALID_ARG, LQ_ERR_UNSUPPORTED; nothing is reported from the device, but
+ * should a bounded wait inside the kernel for bf16 tokens give up (2 s; it never
+ * should), the sequence's outputs and last state are NaN.
+ * With bf16 tokens decays outside 0..1 and values that are not finite take a slow
+ * path, token by token.
  */
 int lq_la_prefill(const lq_la_config* cfg, int64_t n_seqs, int64_t n_tokens, int64_t max_len,
                   const int32_t* cu_seqlens, const void* q, const void* k, const void* v, const float* alpha,
