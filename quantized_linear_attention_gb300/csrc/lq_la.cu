@@ -49,6 +49,7 @@ __global__ void __launch_bounds__(256, 2) k_la_recurrent(LaParams p) {
   __shared__ bool even[4];  // no token of the block needs A put back before it
   __shared__ float2 sprod[8];
   __shared__ Piece spc;
+  cudaTriggerProgrammaticLaunchCompletion();
   const int tid = threadIdx.x, tx = tid & 15, row = 8 * (tid >> 4), warp = tid >> 5, lane = tid & 31;
   const int h = (int)(blockIdx.x % (unsigned)p.heads), kh = h / p.group;
   const int64_t slot = blockIdx.x / (unsigned)p.heads;
@@ -66,6 +67,7 @@ __global__ void __launch_bounds__(256, 2) k_la_recurrent(LaParams p) {
   const T* v = static_cast<const T*>(p.v) + h * kD;
   T* o = static_cast<T*>(p.o) + h * kD;
 
+  if (OUT && p.seg) cudaGridDependencySynchronize();
   f32x2 S[8][4];  // row + x, columns 4 tx .. + 3 (pairs 0, 1) and 64 + 4 tx .. + 3 (pairs 2, 3)
   const float* from = OUT ? start_state(p, pc, slot, h) : nullptr;
 #pragma unroll
@@ -244,29 +246,31 @@ __global__ void __launch_bounds__(256, 2) k_la_recurrent(LaParams p) {
 // Between the passes: each segment's growth becomes the state before it, S_{i+1} = decay_i S_i + growth_i from S0 on.
 // One thread per four entries; the segments of a sequence are read a few ahead.
 __device__ __forceinline__ void scan_sequence(const LaParams& p, int64_t b, int h) {
-  __shared__ int64_t sfirst, sn;
+  int64_t begin, len;
+  bounds(p, b, begin, len);
+  if (len <= p.seg) return;  // (most sequences of a batch)
+  __shared__ int64_t sfirst;
   __syncthreads();
   if (threadIdx.x < 32) {
-    int64_t first = 0, n = 1, begin, len;
+    int64_t first = 0, b1, l1;
     for (int64_t x = threadIdx.x; x < b; x += 32) {
-      bounds(p, x, begin, len);
-      first += len > p.seg ? (len + p.seg - 1) / p.seg : 1;
+      bounds(p, x, b1, l1);
+      first += l1 > p.seg ? (l1 + p.seg - 1) / p.seg : 1;
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) first += __shfl_xor_sync(0xffffffffu, first, o);
-    bounds(p, b, begin, len);
-    if (len > p.seg) n = (len + p.seg - 1) / p.seg;
-    if (threadIdx.x == 0) sfirst = first, sn = n;
+    if (threadIdx.x == 0) sfirst = first;
   }
   __syncthreads();
-  const int64_t first = sfirst, n = sn;
-  if (n == 1 || first + n > p.slots) return;
+  const int64_t first = sfirst, n = (len + p.seg - 1) / p.seg;
+  if (first + n > p.slots) return;
+  cudaGridDependencySynchronize();
   const int at = 4 * (blockIdx.x * 256 + threadIdx.x);
   float s[4] = {0.f, 0.f, 0.f, 0.f};
   if (p.S0) ld4(p.S0 + (b * p.heads + h) * (kD * kD) + at, s);
   float* w = p.ws_state + (first * p.heads + h) * (kD * kD) + at;
   const int64_t pitch = (int64_t)p.heads * (kD * kD);
-  constexpr int kAhead = 8;
+  constexpr int kAhead = 4;
   for (int64_t i = 0; i < n; i += kAhead) {
     float u[kAhead][4];
     float2 d[kAhead];
@@ -287,7 +291,8 @@ __device__ __forceinline__ void scan_sequence(const LaParams& p, int64_t b, int 
   }
 }
 
-__global__ void __launch_bounds__(256) k_la_scan(LaParams p) {
+__global__ void __launch_bounds__(256, 5) k_la_scan(LaParams p) {
+  cudaTriggerProgrammaticLaunchCompletion();
   for (int64_t b = blockIdx.z; b < p.n_seqs; b += gridDim.z) scan_sequence(p, b, blockIdx.y);
 }
 
@@ -362,8 +367,13 @@ cudaError_t prefill(const LaParams& p0, cudaStream_t st) {
     if ((e = cudaGetLastError()) != cudaSuccess || (e = launch_la_scan(p, st)) != cudaSuccess) return e;
   }
   if (la_staged(p)) p.S = p.ws_last;
-  k_la_recurrent<T, true><<<grid, 256, 0, st>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (p.seg) {
+    e = launch_upon(k_la_recurrent<T, true>, dim3(grid), 256, 0, st, p);
+  } else {
+    k_la_recurrent<T, true><<<grid, 256, 0, st>>>(p);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess) return e;
   return la_staged(p0) ? launch_la_unstage(p0, st) : cudaSuccess;
 }
 
@@ -380,8 +390,7 @@ cudaError_t step(const LaParams& p, cudaStream_t st) {
 
 cudaError_t launch_la_scan(const LaParams& p, cudaStream_t st) {
   const unsigned z = (unsigned)(p.n_seqs < 65535 ? p.n_seqs : 65535);
-  k_la_scan<<<dim3(kD * kD / 1024, (unsigned)p.heads, z), 256, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_upon(k_la_scan, dim3(kD * kD / 1024, (unsigned)p.heads, z), 256, 0, st, p);
 }
 
 cudaError_t launch_la_unstage(const LaParams& p, cudaStream_t st) {

@@ -130,6 +130,24 @@ __device__ __forceinline__ const float* start_state(const LaParams& p, const Pie
 
 cudaError_t launch_la_chunk_bf16(const LaParams& p, cudaStream_t st);
 
+// The kernels of a split prompt are launched one upon the other: a kernel is set up while the one before still
+// runs (each lets its successor in as soon as all its CTAs have begun) and waits for that one's end
+// (cudaGridDependencySynchronize) before it reads what it left.
+template <typename... A>
+inline cudaError_t launch_upon(void (*kernel)(A...), dim3 grid, int threads, int smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Split sequences: the states before the segments, from what the first pass left in the workspace.
 cudaError_t launch_la_scan(const LaParams& p, cudaStream_t st);
 // Split sequences whose last states replace S0: other segments may not have read it yet, so the second pass leaves

@@ -261,6 +261,7 @@ __device__ __noinline__ void redo(const LaParams& p, const Piece& pc, int64_t sl
   const bf16* k = static_cast<const bf16*>(p.k) + kh * kD;
   const bf16* v = static_cast<const bf16*>(p.v) + h * kD;
   bf16* o = static_cast<bf16*>(p.o) + h * kD;
+  if (OUT && p.seg) cudaGridDependencySynchronize();
   float S[8][4];
   double prod = 1.0;
   if (tid < 512) {
@@ -325,6 +326,7 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
                const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo) {
   extern __shared__ __align__(1024) char la_smem[];
   Misc& ms = *reinterpret_cast<Misc*>(la_smem + kMisc);
+  cudaTriggerProgrammaticLaunchCompletion();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = (int)(blockIdx.x % (unsigned)p.heads), kh = h / p.group;
   const int64_t slot = blockIdx.x / (unsigned)p.heads;
@@ -519,6 +521,7 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
     const uint32_t tl = tm + ((uint32_t)(32 * quad) << 16);
     f32x2 S[32];  // row `row` of the state, columns 64 half .., in pairs
     {
+      if (OUT && p.seg) cudaGridDependencySynchronize();
       const float* from = OUT ? start_state(p, pc, slot, h) : nullptr;
 #pragma unroll
       for (int e = 0; e < 32; ++e) S[e] = 0ull;
@@ -848,8 +851,13 @@ cudaError_t launch_la_chunk_bf16(const LaParams& p0, cudaStream_t st) {
     if ((e = cudaGetLastError()) != cudaSuccess || (e = launch_la_scan(p, st)) != cudaSuccess) return e;
   }
   if (la_staged(p)) p.S = p.ws_last;
-  k_la_chunk<true><<<grid, kThreadsLa, kSmem, st>>>(p, mq, mk, mv, mo);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (p.seg) {
+    e = launch_upon(k_la_chunk<true>, dim3(grid), kThreadsLa, (int)kSmem, st, p, mq, mk, mv, mo);
+  } else {
+    k_la_chunk<true><<<grid, kThreadsLa, kSmem, st>>>(p, mq, mk, mv, mo);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess) return e;
   return la_staged(p0) ? launch_la_unstage(p0, st) : cudaSuccess;
 }
 
