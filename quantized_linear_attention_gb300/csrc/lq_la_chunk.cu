@@ -84,8 +84,8 @@ __device__ __forceinline__ uint64_t desc(uint32_t lo) {
 constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (16u << 17) | (8u << 24);
 constexpr uint32_t kIdescMn = kIdesc | (1u << 16);
 
-// The products are issued by one thread of a converged warp, chosen by elect.sync with warp-uniform operands:
-// from a thread chosen by its lane number the same instructions took 220 cycles each to issue (64 to run).
+// The products are issued by one thread, chosen by elect.sync, with warp-uniform operands: from a thread chosen by its
+// lane number the same instructions took 220 cycles each to issue (64 to run).
 __device__ __forceinline__ bool elect() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n}" : "=r"(r));
@@ -709,34 +709,31 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
     // The products.
     const uint32_t tmu = __shfl_sync(0xffffffffu, tm, 0);
     const uint32_t S16 = ((sb + kS16) >> 4) | kByRow;
-    for (int c = -1; c < nc; ++c) {
-      if (c >= 0) {
-        const uint32_t at = (sb + Ti::offset(c)) >> 4;
-        const uint32_t Q = at | kByRow, Kc = (at + Ti::kK / 16) | kByChannel, Vc = (at + Ti::kV / 16) | kByChannel;
-        if (!OUT && !wait_warp(&ms.full[Ti::at(c)], Ti::phase(c), ab)) break;
-        // U is free: read up to the last chunk's, or, where there are two, the one's before. (Chunk 0 waits as well, so
-        // that no chunk is through before B has seen its sums.)
-        const int r = OUT ? c : max(c - 1, 0);
-        if (!wait_warp(&ms.uread[r & 1], (r >> 1) & 1, ab)) break;
-        tc_after();
-        const uint32_t U = tmu + kU + (OUT ? 0 : 128 * (c & 1));
-        bool ok = true;
-#pragma unroll 1
-        for (int qt = 0; qt < 4; ++qt) {
-          const int buf = OUT ? qt & 1 : qt, use = OUT ? 2 * c + (qt >> 1) : c;
-          if (OUT && qt == 2) {  // while quarter 2 is in the making
-            if (!(ok = wait_warp(&ms.sready, c & 1, ab))) break;
-            if (c && !(ok = wait_warp(&ms.ofree, (c - 1) & 1, ab))) break;
-            tc_after();
-            if (elect()) {
+    if (elect()) {
+      for (int c = -1; c < nc; ++c) {
+        if (c >= 0) {
+          const uint32_t at = (sb + Ti::offset(c)) >> 4;
+          const uint32_t Q = at | kByRow, Kc = (at + Ti::kK / 16) | kByChannel, Vc = (at + Ti::kV / 16) | kByChannel;
+          if (!OUT && !wait(&ms.full[Ti::at(c)], Ti::phase(c), ab)) break;
+          // U is free: read up to the last chunk's, or, where there are two, the one's before. (Chunk 0 waits as well,
+          // so that no chunk is through before B has seen its sums.)
+          const int r = OUT ? c : max(c - 1, 0);
+          if (!wait(&ms.uread[r & 1], (r >> 1) & 1, ab)) break;
+          tc_after();
+          const uint32_t U = tmu + kU + (OUT ? 0 : 128 * (c & 1));
+          bool ok = true;
+#pragma unroll
+          for (int qt = 0; qt < 4; ++qt) {
+            const int buf = OUT ? qt & 1 : qt, use = OUT ? 2 * c + (qt >> 1) : c;
+            if (OUT && qt == 2) {  // while quarter 2 is in the making
+              if (!(ok = wait(&ms.sready, c & 1, ab))) break;
+              if (c && !(ok = wait(&ms.ofree, (c - 1) & 1, ab))) break;
+              tc_after();
               product(tmu + kO, Q, S16);
               commit(&ms.qs);
             }
-            __syncwarp();
-          }
-          if (!(ok = wait_warp(&ms.vfull[buf], use & 1, ab))) break;
-          tc_after();
-          if (elect()) {
+            if (!(ok = wait(&ms.vfull[buf], use & 1, ab))) break;
+            tc_after();
             const uint32_t a = tmu + kV3<OUT> + 48 * buf, b = Kc + 2 * qt * 128;
             // the small parts first
             if (qt == 0) mma_ts<false>(U, a + 32, b, kIdescMn);
@@ -750,35 +747,28 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
             if (qt == 3) commit(&ms.grown[c & 1]);
             if (qt == 3 && !OUT) commit(&ms.empty[Ti::at(c)]);
           }
-          __syncwarp();
-        }
-        if (!ok) break;
-        if (OUT) {  // while the state is brought up to date
-          if (!wait_warp(&ms.pvok, c & 1, ab)) break;
-          tc_after();
-          if (elect()) {
+          if (!ok) break;
+          if (OUT) {  // while the state is brought up to date
+            if (!wait(&ms.pvok, c & 1, ab)) break;
+            tc_after();
 #pragma unroll
             for (int s = 0; s < 8; ++s)
               mma_ts<true>(tmu + kO, tmu + kP + 64 * (s >> 2) + 8 * (s & 3), Vc + s * 128, kIdescMn);
             commit(&ms.pv);
             commit(&ms.empty[Ti::at(c)]);
           }
-          __syncwarp();
         }
-      }
-      if (OUT && c + 1 < nc) {  // the next chunk's scores: they follow P's last use in order
-        if (!wait_warp(&ms.full[Ti::at(c + 1)], Ti::phase(c + 1), ab)) break;
-        tc_after();
-        const uint32_t next = (sb + Ti::offset(c + 1)) >> 4;
-        if (elect()) {
+        if (OUT && c + 1 < nc) {  // the next chunk's scores: they follow P's last use in order
+          if (!wait(&ms.full[Ti::at(c + 1)], Ti::phase(c + 1), ab)) break;
+          tc_after();
+          const uint32_t next = (sb + Ti::offset(c + 1)) >> 4;
           product(tmu + kP, next | kByRow, (next + Ti::kK / 16) | kByRow);
           commit(&ms.qk);
         }
-        __syncwarp();
       }
+      // nothing may be in flight when TMEM is given back
+      commit(&ms.drain);
     }
-    // nothing may be in flight when TMEM is given back
-    if (elect()) commit(&ms.drain);
     __syncwarp();
     int ignored = 0;
     wait_warp(&ms.drain, 0, &ignored);
