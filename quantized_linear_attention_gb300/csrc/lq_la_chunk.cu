@@ -13,15 +13,28 @@
 //   O += P V         P (weighted, masked, rounded to bf16) from TMEM
 //   U  = (wV)^T K    the state's growth. wV is an fp32 number; it goes in as three
 //                    bf16 parts that hold all its 24 bits, so the state keeps fp32's
-//                    accuracy (two parts, 16 bits, were not enough: 2.8e-6).
+//                    accuracy (two parts, 16 bits, round to 2.8e-6 of it).
 // S itself stays in fp32 registers: S <- gamma S + U in one rounding to nearest
 // per step, with gamma in two parts, because a rounded gamma would be off in the
 // same direction chunk after chunk. Sums of logarithms are whole numbers of 2^-40.
 //
-// Warps: 0-7 weigh P, scale O and write o (A); 8-15 keep the state and make
-// the parts of wV (B); 16 copies tiles in and out (TMA); 17 and 18 sum the logarithms
-// (even and odd chunks); 19 issues the products. They meet at mbarriers only. Every wait is bounded; one that gives up
-// ends the CTA's work, and the outputs become NaN.
+// Warps: 0-7 weigh P, scale O and write o (A); 8-15 keep the state (B); 16-23 make the
+// parts of wV (C); 24 copies tiles in and out (TMA); 25 and 26 sum the logarithms (even
+// and odd chunks); 27 issues the products. They meet at mbarriers only. Every wait is
+// bounded; one that gives up ends the CTA's work, and the outputs become NaN. What a
+// chunk waits for is the chain U -> S -> bf16 copy of S -> products -> U; the rest is
+// placed beside it: the first half of wV before the state is there, S q between the
+// halves, P v and the next chunk's scores while the state is brought up to date.
+//
+// A barrier's phases are told apart by one bit, so whoever waits for a phase must do so before
+// the phase after the next can end: every wait below comes before an arrival of
+// the same warp that this next phase needs. (Slow loads bring a mistake in this to light.)
+//
+// What bounds it, at 32,768 tokens x 32 heads (345 us, three times the bytes' 159 us less the
+// split's second reading of k and v): 121 us in the first pass and 225 in the second, 2.0 and
+// 3.6 us a chunk of an SM, of which the tensor cores take 0.8 and 1.6, HBM at its full rate 1.5 and 2.9.
+// The chain's hand-overs make up the rest; taking out the exponentials, the
+// loads of V or the stores, one at a time, changes less than 6%.
 //
 // A masked product cannot hold back 0 x inf: where the state comes out not finite
 // (any value or key that is not makes it so), or a decay is not in [0, 1], the CTA
@@ -65,7 +78,17 @@ constexpr uint32_t kV3 = OUT ? 384 : 256;
 
 struct Misc {
   float2 gamma[4];
-  uint64_t land[3], full[3], empty[3], sums[2], oready[2], qk, qs, pv, pvok, ofree, uread[2], sready, grown[2], vfull[4], vfree[4], drain;
+  // barriers; of a chunk unless it says otherwise
+  uint64_t land[3], full[3];    // tiles of the last, ragged chunk have landed; tiles are ready
+  uint64_t empty[3];            // everything that reads the tiles is done
+  uint64_t sums[2];             // G, w and gamma are there
+  uint64_t qk, qs, pv;          // products done: P; S q in O; P v added to O
+  uint64_t pvok, ofree;         // P and the scaled O are in TMEM; O has been read
+  uint64_t oready[2];           // o is in Q's tile
+  uint64_t uread[2], sready;    // U has been read; the bf16 copy of S is in place
+  uint64_t grown[2];            // U is complete
+  uint64_t vfull[4], vfree[4];  // of a quarter's buffer: parts are in TMEM; products have read them
+  uint64_t drain;               // all products are done
   uint32_t tmem;
   int abort, flag;
   double prod[2];
@@ -434,6 +457,7 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
       const int quad = warp & 3, half = warp >> 2, i = 32 * quad + lane;
       const uint32_t tl = tm + ((uint32_t)(32 * quad) << 16);
       bf16* o = static_cast<bf16*>(p.o) + h * kD + 64 * half;
+      const bool two = nc == 1;  // P in two parts (see the products)
       for (int c = 0; c < nc; ++c) {
         const float* G = sG + (c & 1) * kC;
         if (!wait_warp(&ms.sums[c & 1], (c >> 1) & 1, ab)) break;
@@ -445,10 +469,10 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
         // waited for instructions more than for data.
 #pragma unroll 1
         for (int j0 = 64 * half; j0 < 64 * half + 64; j0 += 16) {
-          uint32_t w[8];
+          uint32_t w[8], w2[8];
           if (j0 > 32 * quad + 31) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = 0u;
+            for (int e = 0; e < 8; ++e) w[e] = w2[e] = 0u;
           } else {
             uint32_t x[16];
             tm_ld16(tl + kP + j0, x);
@@ -461,12 +485,18 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
 #pragma unroll
               for (int f = 0; f < 4; ++f)
                 y[f] = j0 + e + f <= i ? __fmul_rn(__uint_as_float(x[e + f]), ex2(__fsub_rn(gi, gj[f]))) : 0.f;
-              w[e / 2] = pack_bf16(y[0], y[1]);
-              w[e / 2 + 1] = pack_bf16(y[2], y[3]);
+#pragma unroll
+              for (int f = 0; f < 4; f += 2) {
+                const uint32_t p2 = pack_bf16(y[f], y[f + 1]);
+                w[(e + f) / 2] = p2;
+                w2[(e + f) / 2] = pack_bf16(__fsub_rn(y[f], __uint_as_float(p2 << 16)),
+                                            __fsub_rn(y[f + 1], __uint_as_float(p2 & 0xffff0000u)));
+              }
             }
           }
-          // P's tokens 64 half .. go to columns 64 half .. of its own accumulator: a warp overwrites what it has read
-          tm_st8(tl + kP + 64 * half + (j0 & 63) / 2, w);
+          // 16 tokens of P take 8 columns; they go where their accumulators were, which this warp has read
+          tm_st8(tl + kP + j0, w);
+          if (two) tm_st8(tl + kP + j0 + 8, w2);
         }
         if (!wait_warp(&ms.qs, c & 1, ab)) break;
         tc_after();
@@ -753,7 +783,14 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
             tc_after();
 #pragma unroll
             for (int s = 0; s < 8; ++s)
-              mma_ts<true>(tmu + kO, tmu + kP + 64 * (s >> 2) + 8 * (s & 3), Vc + s * 128, kIdescMn);
+              mma_ts<true>(tmu + kO, tmu + kP + 16 * s, Vc + s * 128, kIdescMn);
+            // Where a single chunk is all, o hangs on few weights, whose roundings need not even out: there what
+            // rounding P took off is added.
+            if (nc == 1) {
+#pragma unroll 1
+              for (int s = 0; s < 8; ++s)
+                mma_ts<true>(tmu + kO, tmu + kP + 16 * s + 8, Vc + s * 128, kIdescMn);
+            }
             commit(&ms.pv);
             commit(&ms.empty[Ti::at(c)]);
           }
