@@ -30,11 +30,11 @@
 // the phase after the next can end: every wait below comes before an arrival of
 // the same warp that this next phase needs. (Slow loads bring a mistake in this to light.)
 //
-// What bounds it, at 32,768 tokens x 32 heads (345 us, three times the bytes' 159 us less the
-// split's second reading of k and v): 121 us in the first pass and 225 in the second, 2.0 and
-// 3.6 us a chunk of an SM, of which the tensor cores take 0.8 and 1.6, HBM at its full rate 1.5 and 2.9.
-// The chain's hand-overs make up the rest; taking out the exponentials, the
-// loads of V or the stores, one at a time, changes less than 6%.
+// What bounds it, at 32,768 tokens x 32 heads: 349 us, 114 in the first pass and 230 in
+// the second, 1.9 and 3.7 us a chunk of an SM. Of these the tensor cores take 0.8 and
+// 1.6, HBM at its full rate would take 1.5 and 2.9. The chain's hand-overs make up the rest;
+// taking out the exponentials, the loads of V or the stores, one at a time,
+// changes less than 6%. (The tensors' bytes once: 159 us; the split reads k and v twice.)
 //
 // A masked product cannot hold back 0 x inf: where the state comes out not finite
 // (any value or key that is not makes it so), or a decay is not in [0, 1], the CTA
