@@ -207,12 +207,16 @@ __device__ __forceinline__ void arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Waits for phase `parity`; false once this or any other wait of the CTA has given up.
+// Waits for phase `parity`; false once this or any other wait of the CTA has given up. The clock is read only after
+// a good many tries (a try waits by itself for a while): reading it first held up every wait.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort) {
-  if (mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+  for (int i = 0; i < 4096; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   for (;;) {
-    for (int i = 0; i < 16; ++i)
+#pragma unroll 1
+    for (int i = 0; i < 256; ++i)
       if (mbar_try_wait(bar, parity)) return true;
     if (*reinterpret_cast<volatile int*>(abort)) return false;
     if (globaltimer_ns() - t0 > 2000000000ull) {
@@ -342,6 +346,45 @@ __device__ __noinline__ void redo(const LaParams& p, const Piece& pc, int64_t sl
   if (decay && tid == 0) *decay = in_two(prod);
 }
 
+// A's first step: the scores of row i, columns 64 half .. + 63, weighted, masked and rounded to bf16 as an A operand; TWO:
+// what the rounding took off as well (see the products). Loops are kept rolled here and below: five roles run at once,
+// and with everything unrolled the warps waited for instructions more than for data.
+template <bool TWO>
+__device__ __forceinline__ void weigh_scores(uint32_t tl, const float* G, float gi, int i, int quad, int half) {
+#pragma unroll 1
+  for (int j0 = 64 * half; j0 < 64 * half + 64; j0 += 16) {
+    uint32_t w[8], w2[8];
+    if (j0 > 32 * quad + 31) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = w2[e] = 0u;
+    } else {
+      uint32_t x[16];
+      tm_ld16(tl + kP + j0, x);
+      wait_ld();
+#pragma unroll
+      for (int e = 0; e < 16; e += 4) {
+        const float4 g = *reinterpret_cast<const float4*>(G + j0 + e);
+        const float gj[4] = {g.x, g.y, g.z, g.w};
+        float y[4];
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+          y[f] = j0 + e + f <= i ? __fmul_rn(__uint_as_float(x[e + f]), ex2(__fsub_rn(gi, gj[f]))) : 0.f;
+#pragma unroll
+        for (int f = 0; f < 4; f += 2) {
+          const uint32_t p2 = pack_bf16(y[f], y[f + 1]);
+          w[(e + f) / 2] = p2;
+          if (TWO)
+            w2[(e + f) / 2] = pack_bf16(__fsub_rn(y[f], __uint_as_float(p2 << 16)),
+                                        __fsub_rn(y[f + 1], __uint_as_float(p2 & 0xffff0000u)));
+        }
+      }
+    }
+    // 16 tokens of P take 8 columns; they go where their accumulators were, which this warp has read
+    tm_st8(tl + kP + j0, w);
+    if (TWO) tm_st8(tl + kP + j0 + 8, w2);
+  }
+}
+
 // OUT: outputs and last states. Otherwise the first pass over split sequences: what a segment adds to the state.
 template <bool OUT>
 __global__ void __launch_bounds__(kThreadsLa, 1)
@@ -457,7 +500,6 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
       const int quad = warp & 3, half = warp >> 2, i = 32 * quad + lane;
       const uint32_t tl = tm + ((uint32_t)(32 * quad) << 16);
       bf16* o = static_cast<bf16*>(p.o) + h * kD + 64 * half;
-      const bool two = nc == 1;  // P in two parts (see the products)
       for (int c = 0; c < nc; ++c) {
         const float* G = sG + (c & 1) * kC;
         if (!wait_warp(&ms.sums[c & 1], (c >> 1) & 1, ab)) break;
@@ -465,39 +507,8 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
         const float ei = ex2(gi);
         if (!wait_warp(&ms.qk, c & 1, ab)) break;
         tc_after();
-        // Loops are kept rolled here and below: five roles run at once, and with everything unrolled the warps
-        // waited for instructions more than for data.
-#pragma unroll 1
-        for (int j0 = 64 * half; j0 < 64 * half + 64; j0 += 16) {
-          uint32_t w[8], w2[8];
-          if (j0 > 32 * quad + 31) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = w2[e] = 0u;
-          } else {
-            uint32_t x[16];
-            tm_ld16(tl + kP + j0, x);
-            wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              const float4 g = *reinterpret_cast<const float4*>(G + j0 + e);
-              const float gj[4] = {g.x, g.y, g.z, g.w};
-              float y[4];
-#pragma unroll
-              for (int f = 0; f < 4; ++f)
-                y[f] = j0 + e + f <= i ? __fmul_rn(__uint_as_float(x[e + f]), ex2(__fsub_rn(gi, gj[f]))) : 0.f;
-#pragma unroll
-              for (int f = 0; f < 4; f += 2) {
-                const uint32_t p2 = pack_bf16(y[f], y[f + 1]);
-                w[(e + f) / 2] = p2;
-                w2[(e + f) / 2] = pack_bf16(__fsub_rn(y[f], __uint_as_float(p2 << 16)),
-                                            __fsub_rn(y[f + 1], __uint_as_float(p2 & 0xffff0000u)));
-              }
-            }
-          }
-          // 16 tokens of P take 8 columns; they go where their accumulators were, which this warp has read
-          tm_st8(tl + kP + j0, w);
-          if (two) tm_st8(tl + kP + j0 + 8, w2);
-        }
+        if (nc == 1) weigh_scores<true>(tl, G, gi, i, quad, half);
+        else weigh_scores<false>(tl, G, gi, i, quad, half);
         if (!wait_warp(&ms.qs, c & 1, ab)) break;
         tc_after();
 #pragma unroll 1
