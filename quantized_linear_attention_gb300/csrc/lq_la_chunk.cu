@@ -30,8 +30,8 @@
 // the phase after the next can end: every wait below comes before an arrival of
 // the same warp that this next phase needs. (Slow loads bring a mistake in this to light.)
 //
-// What bounds it, at 32,768 tokens x 32 heads: 349 us, 114 in the first pass and 230 in
-// the second, 1.9 and 3.7 us a chunk of an SM. Of these the tensor cores take 0.8 and
+// What bounds it, at 32,768 tokens x 32 heads: 333 us, 112 in the first pass and 217 in
+// the second, 1.9 and 3.5 us a chunk of an SM. Of these the tensor cores take 0.8 and
 // 1.6, HBM at its full rate would take 1.5 and 2.9. The chain's hand-overs make up the rest;
 // taking out the exponentials, the loads of V or the stores, one at a time,
 // changes less than 6%. (The tensors' bytes once: 159 us; the split reads k and v twice.)
@@ -54,6 +54,9 @@ constexpr int kThreadsLa = 896;
 // An increase waits until the registers are there, and nothing bounds that wait: all but B give theirs up first
 // thing and take them back only after B has (roles_done), so each increase finds what it needs.
 constexpr int kRegs = 72, kRegsA = 64, kRegsB = 96, kRegsC = 64, kRegsRest = 48;
+// (without outputs A's warps work as C's)
+static_assert(256 * ((kRegsA > kRegsC ? kRegsA : kRegsC) + kRegsB + kRegsC) + 128 * kRegsRest <= kThreadsLa * kRegs,
+              "the roles' registers come out of those of the launch");
 constexpr uint32_t kTile = 32768;             // 128 x 128 bf16: two halves of 64 channels, 128-byte rows, swizzled
 constexpr uint32_t kS16 = 6 * kTile;          // the state in bf16
 constexpr uint32_t kSums = kS16 + kTile;      // G[2][128], w[2][128]
@@ -155,16 +158,6 @@ __device__ __forceinline__ void tm_ld32(uint32_t a, uint32_t (&r)[32]) {
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(a));
-}
-__device__ __forceinline__ void tm_st32(uint32_t a, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(a),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
 }
 __device__ __forceinline__ void tm_ld16(uint32_t a, uint32_t (&r)[16]) {
   asm volatile(
@@ -528,15 +521,16 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
         // o goes out by way of Q's tile, which nothing reads any more: rows of 128 bytes, swizzled as Q's were
         char* tile = la_smem + Ti::offset(c) + half * 16384;
 #pragma unroll 1
-        for (int blk = 0; blk < 4; ++blk) {
-          uint32_t x[16];
-          tm_ld16(tl + kO + 64 * half + 16 * blk, x);
+        for (int blk = 0; blk < 2; ++blk) {
+          uint32_t x[32];
+          tm_ld32(tl + kO + 64 * half + 32 * blk, x);
           wait_ld();
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = pack_bf16(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
-          *reinterpret_cast<uint4*>(tile + i * 128 + (((2 * blk) ^ (i & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
-          *reinterpret_cast<uint4*>(tile + i * 128 + (((2 * blk + 1) ^ (i & 7)) << 4)) =
-              make_uint4(x[4], x[5], x[6], x[7]);
+          for (int e = 0; e < 16; ++e) x[e] = pack_bf16(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4*>(tile + i * 128 + (((4 * blk + e) ^ (i & 7)) << 4)) =
+                make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
         }
         tc_before();
         arrive(&ms.ofree);
@@ -880,6 +874,13 @@ cudaError_t launch_la_chunk_bf16(const LaParams& p0, cudaStream_t st) {
                      (e = tile_map(&mv, p.v, p.heads, p.sv, p.n_tokens)) != cudaSuccess ||
                      (e = tile_map(&mo, p.o, p.heads, p.so, p.n_tokens)) != cudaSuccess))
     return e;
+  // The roles' shares of registers count on this many at launch.
+  static const bool regs = [] {
+    cudaFuncAttributes t, f;
+    return cudaFuncGetAttributes(&t, k_la_chunk<true>) == cudaSuccess &&
+           cudaFuncGetAttributes(&f, k_la_chunk<false>) == cudaSuccess && t.numRegs == kRegs && f.numRegs == kRegs;
+  }();
+  if (!regs) return cudaErrorLaunchOutOfResources;
   if ((e = set_smem(k_la_chunk<true>, kSmem)) != cudaSuccess) return e;
   const int64_t slots = p.seg ? p.slots : p.n_seqs;
   const unsigned grid = (unsigned)(slots * p.heads);
