@@ -382,8 +382,8 @@ int check_beams(int64_t batch, int32_t beams, int64_t vocab, int32_t n_best) {
     return fail(LQ_ERR_INVALID_ARG, "vocab must be 1..(2^31 - 1) / beams (got %lld)", (long long)vocab);
   if (n_best < 1 || n_best > lqi::kMaxBest || n_best > beams * vocab)
     return fail(LQ_ERR_INVALID_ARG, "n_best must be 1..%d and at most beams x vocab (got %d)", lqi::kMaxBest, n_best);
-  // one CTA per slice of a row, at the least 2,048 elements
-  if (batch > kMaxStates / beams / ((vocab + 2047) / 2048))
+  // one CTA per slice of a row
+  if (batch > kMaxStates / beams / lqi::beam_splits(LQ_F32, vocab))
     return fail(LQ_ERR_INVALID_ARG, "batch %lld is too large", (long long)batch);
   return LQ_OK;
 }
@@ -825,9 +825,7 @@ int lq_beam_select(int32_t dtype, int64_t batch, int32_t beams, int64_t vocab, i
   p.dtype = dtype;
   p.beams = beams;
   p.n_best = n_best;
-  int64_t splits;
-  lqi::beam_plan(dtype, batch * beams, vocab, &p.words, &splits);
-  p.splits = (int)splits;
+  p.splits = lqi::beam_splits(dtype, vocab);
   p.batch = batch;
   p.vocab = vocab;
   p.row_stride = row_stride;

@@ -40,6 +40,7 @@ namespace lqi {
 namespace {
 
 constexpr int kNT = 256;
+constexpr int kWords = 32;   // words of a slice in a thread's registers
 constexpr double kLn2 = 0.693147180559945309417;
 constexpr float kL2Ehi = 1.44269502162933349609375f, kL2Elo = 1.92596299e-8f;  // log2 e in two parts
 constexpr int kList = 512;   // candidates a slice collects before ranking
@@ -146,10 +147,14 @@ __device__ __forceinline__ uint32_t max_words<__half>(uint32_t a, uint32_t b) {
   return r;
 }
 
-// A slice of a row: W words (of 32 bits) to a thread, VE elements to a load. Element i of
-// thread t is element ((i / VE) * 256 + t) * VE + i % VE of the slice.
-template <typename T, int VE, int W>
-__global__ void __launch_bounds__(kNT, W == 32 ? 4 : 8) k_beam_scan(BeamParams p) {
+// A slice of a row: 32 words (of 32 bits) to a thread, VE elements to a load. Element i of
+// thread t is element ((i / VE) * 256 + t) * VE + i % VE of the slice. (Slices a quarter the
+// size were no faster even for four rows, and 12.1 -> 15.9 us for 256 rows of 32,000.)
+// Loads of single 16-bit elements need more registers than four CTAs on an SM leave: three
+// take 80 us at 64 x 8 x 131,071, four 94 (spills), two 91.
+template <typename T, int VE>
+__global__ void __launch_bounds__(kNT, VE == 1 && sizeof(T) == 2 ? 3 : 4) k_beam_scan(BeamParams p) {
+  constexpr int W = kWords;
   constexpr int EPW = 4 / (int)sizeof(T), E = W * EPW;  // elements per word, per thread
   __shared__ float gmax[64];
   __shared__ uint64_t wsum[8];
@@ -420,7 +425,7 @@ __global__ void __launch_bounds__(kNT) k_beam_pick(BeamParams p) {
   __shared__ int cnt;
   const int tid = threadIdx.x, lane = tid & 31, M = p.n_best;
   const int64_t r = blockIdx.x;
-  const int NL = p.beams * p.splits, NC = NL * M;  // (below 2^27: a slice has 2,048 tokens at least)
+  const int NL = p.beams * p.splits, NC = NL * M;  // (below 2^25: a slice has 8,192 tokens at least)
   const float mine = tid < p.beams ? p.scores[r * p.beams + tid] : 0.f;
   if (tid == 0) cnt = 0, sT = 0;
   cudaGridDependencySynchronize();
@@ -576,17 +581,18 @@ __global__ void __launch_bounds__(kNT) k_beam_pick(BeamParams p) {
 template <typename T, int VE>
 cudaError_t scan(const BeamParams& p, cudaStream_t st) {
   const unsigned grid = (unsigned)(p.batch * p.beams * p.splits);
-  if (p.words == 32) k_beam_scan<T, VE, 32><<<grid, kNT, 0, st>>>(p);
-  else k_beam_scan<T, VE, 8><<<grid, kNT, 0, st>>>(p);
+  k_beam_scan<T, VE><<<grid, kNT, 0, st>>>(p);
   return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t select(const BeamParams& p, cudaStream_t st) {
   // The widest load that every row's alignment allows (equal rows must sum in the same order, so all rows load alike).
+  // bf16, 64 x 8 rows with no gap between them: 45 us for 131,072 by 16 bytes, 50 for 131,070 by 4, 79 for 131,071 by 2.
   const uintptr_t a = (uintptr_t)p.logits | (uintptr_t)(p.row_stride * (int64_t)sizeof(T));
   cudaError_t e;
   if (a % 16 == 0) e = scan<T, 16 / (int)sizeof(T)>(p, st);
+  else if (a % 4 == 0) e = scan<T, 4 / (int)sizeof(T)>(p, st);
   else e = scan<T, 1>(p, st);
   if (e != cudaSuccess) return e;
   // k_beam_pick is set up while the scan runs and waits for its end itself.
@@ -603,30 +609,16 @@ cudaError_t select(const BeamParams& p, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, k_beam_pick<T>, p);
 }
 
-int64_t slices(int dtype, int64_t vocab, int words) {
-  const int64_t n = (int64_t)kNT * words * (dtype == LQ_F32 ? 1 : 2);
-  return (vocab + n - 1) / n;
-}
-
 }  // namespace
 
-// Words of a thread: 32 fill the registers and leave least to join; 8 where the rows are too few to give every SM
-// a CTA that way.
-void beam_plan(int dtype, int64_t rows, int64_t vocab, int* words, int64_t* splits) {
-  *words = rows * slices(dtype, vocab, 32) >= 152 ? 32 : 8;
-  *splits = slices(dtype, vocab, *words);
+int beam_splits(int dtype, int64_t vocab) {
+  const int64_t n = (int64_t)kNT * kWords * (dtype == LQ_F32 ? 1 : 2);
+  return (int)((vocab + n - 1) / n);
 }
 
-// Enough for any type.
+// Enough for any type: fp32 has the most slices.
 size_t beam_workspace(int64_t batch, int beams, int64_t vocab, int n_best) {
-  int64_t most = 0;
-  for (int dtype : {LQ_F32, LQ_BF16}) {
-    int words;
-    int64_t n;
-    beam_plan(dtype, batch * beams, vocab, &words, &n);
-    if (n > most) most = n;
-  }
-  const int64_t lists = batch * beams * most;
+  const int64_t lists = batch * beams * beam_splits(LQ_F32, vocab);
   return up256(8 * lists) + 2 * up256(4 * lists) + up256(sizeof(Cand) * lists * n_best);
 }
 

@@ -134,7 +134,7 @@ struct LaParams {
 };
 
 struct BeamParams {
-  int dtype, beams, n_best, splits, words;
+  int dtype, beams, n_best, splits;
   int64_t batch, vocab, row_stride;
   const void* logits;
   const float* scores;
@@ -154,7 +154,7 @@ struct ReorderParams {
 // (Fewer tokens at the same max_len never need more.)
 void la_plan(const lq_la_config* c, int64_t n_seqs, int64_t n_tokens, int64_t max_len, int64_t* seg, int64_t* slots);
 size_t beam_workspace(int64_t batch, int beams, int64_t vocab, int n_best);
-void beam_plan(int dtype, int64_t rows, int64_t vocab, int* words, int64_t* splits);
+int beam_splits(int dtype, int64_t vocab);
 
 cudaError_t launch_la_prefill(const LaParams& p, cudaStream_t st);
 cudaError_t launch_la_step(const LaParams& p, cudaStream_t st);

@@ -384,8 +384,9 @@ cudaError_t prefill(const LaParams& p0, cudaStream_t st) {
 template <typename T>
 cudaError_t step(const LaParams& p, cudaStream_t st) {
   const int64_t n = p.n_seqs * p.heads;
-  // Few head-states: four CTAs share one, so that the loads spread over the SMs.
-  if (n < 2 * 152) k_la_step<T, 4><<<(unsigned)(4 * n), 256, 0, st>>>(p);
+  // Few head-states: four CTAs share one, so that the loads spread over the SMs (8 and 32 head-states 2.1 us against
+  // 3.1; 128 3.1 either way; 256 4.9 against 4.6, 512 7.7 either way).
+  if (n < 128) k_la_step<T, 4><<<(unsigned)(4 * n), 256, 0, st>>>(p);
   else k_la_step<T, 1><<<(unsigned)n, 256, 0, st>>>(p);
   return cudaGetLastError();
 }

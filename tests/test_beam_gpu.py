@@ -156,3 +156,16 @@ def test_row_offsets_past_32_bits():
     rows.copy_(x)
     for y, z in zip(run(rows, s, 6), run(x, s, 6)):
         assert torch.equal(y, z)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("first", [1, 2, 4])
+@pytest.mark.parametrize("V", [1, 2, 3, 9, 8191, 16385, 33334])
+def test_rows_that_start_off_16_bytes(V, first, dtype):
+    """Rows are read by 16 bytes, 4 bytes or single elements, whatever their length; what lies between them is not theirs."""
+    x, s = inputs(100 + V, 2, 3, V, dtype)
+    stride = (V + 8) // 8 * 8 + first
+    all_ = torch.full((6 * stride + 16,), float("nan"), dtype=dtype, device=DEV)
+    rows = all_[first:].as_strided((2, 3, V), (3 * stride, stride, 1))
+    rows.copy_(x)
+    check(rows, s, min(7, 3 * V))
