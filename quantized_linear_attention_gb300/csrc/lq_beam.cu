@@ -12,8 +12,9 @@
 // The sum of a slice: with m = ceil(max * log2 e), a whole number, each term is
 // 2^(x log2 e - m), its exponent formed by two fmas from a two-part log2 e (one
 // rounding, relative to the exponent itself). Threads' sums join as whole numbers of
-// 2^-40 and slices by shifts: exact, and 64-bit floating point is slow here. Rows with equal contents sum in the same order whatever their
-// place in memory, so equal hypotheses tie exactly.
+// 2^-40 and slices by shifts: exact, and 64-bit floating point is slow here. A slice's sum stays below
+// 2^55, but a row of 2^24 terms of 1 passes 2^64: slices join in two words, their upper and lower 32 bits.
+// Rows with equal contents sum in the same order whatever their place in memory, so equal hypotheses tie exactly.
 //
 // The n_best of a slice without a sort: 64 groups of four threads give their
 // maxima; at least n_best elements are not below the n_best-th largest of those
@@ -417,7 +418,7 @@ __global__ void __launch_bounds__(kNT) k_beam_pick(BeamParams p) {
   uint32_t* kf = reinterpret_cast<uint32_t*>(dyn + 8 * kPick);
   Cand* sc = reinterpret_cast<Cand*>(dyn + 12 * kPick);  // the first kPick candidates
   __shared__ double lse[kMaxBeams], sco[kMaxBeams], ref[kMaxBeams];  // log-sum-exps, scores
-  __shared__ uint64_t rsum[kMaxBeams];
+  __shared__ double rsum[kMaxBeams];  // in units of 2^-40; 0 also where a row's is not finite
   __shared__ bool alive[kMaxBeams];
   __shared__ float cut[kMaxBeams];
   __shared__ uint64_t hs[kNT], sT;
@@ -445,12 +446,13 @@ __global__ void __launch_bounds__(kNT) k_beam_pick(BeamParams p) {
       nf |= x == kNotFinite;
     }
     e = __reduce_max_sync(0xffffffffu, e);
-    uint64_t s = 0;
+    uint64_t up = 0, low = 0;  // 2^18 slices at most: neither sum passes 2^50
+    auto join = [&](uint64_t x) { up += x >> 32, low += x & 0xffffffffu; };
     double base = 0.0;
     if (e != kByTop) {
       for (int j = lane; j < p.splits; j += 32) {
         const uint64_t x = ws.sum[l + j];
-        if (x && e - ws.exp2[l + j] < 64) s += x >> (e - ws.exp2[l + j]);
+        if (x && e - ws.exp2[l + j] < 64) join(x >> (e - ws.exp2[l + j]));
       }
     } else {  // logits past 2^20
       auto at = [&](int64_t i) { return ws.exp2[i] == kByTop ? (double)ws.top[i] : ws.exp2[i] * kLn2; };
@@ -458,12 +460,15 @@ __global__ void __launch_bounds__(kNT) k_beam_pick(BeamParams p) {
       for (int j = 0; j < p.splits; ++j)
         if (ws.sum[l + j]) base = fmax(base, at(l + j));
       for (int j = lane; j < p.splits; j += 32)
-        if (ws.sum[l + j]) s += (uint64_t)((double)ws.sum[l + j] * exp(at(l + j) - base));
+        if (ws.sum[l + j]) join((uint64_t)((double)ws.sum[l + j] * exp(at(l + j) - base)));
     }
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    for (int o = 16; o; o >>= 1) {
+      up += __shfl_xor_sync(0xffffffffu, up, o);
+      low += __shfl_xor_sync(0xffffffffu, low, o);
+    }
     nf = __any_sync(0xffffffffu, nf);
     if (lane == 0) {
-      rsum[b] = nf ? 0 : s;
+      rsum[b] = nf ? 0.0 : fma((double)up, 4294967296.0, (double)low);
       ref[b] = e == kByTop ? base : (double)e;
       alive[b] = e == kByTop;  // for the next step
     }
@@ -471,10 +476,10 @@ __global__ void __launch_bounds__(kNT) k_beam_pick(BeamParams p) {
   __syncthreads();
   if (tid < p.beams) {
     const bool byTop = alive[tid];
-    const double x = log_of((double)rsum[tid] * 0x1p-40);  // (of zero: -inf)
+    const double x = log_of(rsum[tid] * 0x1p-40);  // (of zero: -inf)
     lse[tid] = x + (byTop ? ref[tid] : ref[tid] * kLn2);
     sco[tid] = (double)mine;
-    alive[tid] = isfinite(mine) && rsum[tid] != 0;
+    alive[tid] = isfinite(mine) && rsum[tid] != 0.0;
   }
   __syncthreads();
   auto look = [&](int e, uint64_t& s, uint32_t& f) -> bool {  // candidate e % M of list e / M
