@@ -413,7 +413,10 @@ size_t lq_beam_workspace_bytes(int64_t batch, int32_t beams, int64_t vocab, int3
  * A masked token (logit -inf) scores -inf. So does every token of a hypothesis
  * whose score or log-sum-exp is not finite (a dead hypothesis, a row that is all
  * -inf, a NaN or +inf logit): they are chosen only when the finite candidates run
- * out, in the order of their index. Log-sum-exps and scores are compared in 64 bits.
+ * out, in the order of their index. Scores are compared in 64 bits; wherever the
+ * order of the n_best hangs on it, log-sum-exps are good to 1e-10 (out_scores: to a
+ * few 1e-7). Requests in which two hypotheses' candidates lie closer than 5e-6 take
+ * longer: about 50 us for each such hypothesis of 131,071 tokens.
  * workspace: 256-byte aligned, lq_beam_workspace_bytes(...) bytes; contents need
  * not be kept. Outputs must not overlap the inputs or each other.
  */

@@ -7,7 +7,9 @@
 // exponentials and keeps its n_best largest logits. Inside a row the order of the
 // scores is the order of the logits, so no score is needed there. k_beam_pick
 // joins a request's slices: log-sum-exps and scores in 64 bits, because the
-// order of nearly equal candidates of different beams hangs on their rows' sums.
+// order of nearly equal candidates of different beams hangs on their rows' sums. The scan's sums are good to
+// 3e-6 at worst (1e-8 to 1e-7 as a rule); where two candidates of different beams among the n_best lie closer than
+// that leaves certain, their rows' sums are taken again, to 1e-10, and the choice is made anew.
 //
 // The sum of a slice: with m = ceil(max * log2 e), a whole number, each term is
 // 2^(x log2 e - m), its exponent formed by two fmas from a two-part log2 e (one
@@ -353,7 +355,7 @@ __device__ __forceinline__ bool before(uint64_t s1, uint32_t f1, uint64_t s2, ui
 }
 
 // log of a positive finite s to about 1e-13 with few 64-bit steps (64-bit arithmetic is slow here, and the sums are
-// good to 1e-8): s = 2^k m, m in [0.703, 1.406); with r near 1/m from a table of 32, log m = log(1 + u) - log r,
+// good to 1e-10 at best): s = 2^k m, m in [0.703, 1.406); with r near 1/m from a table of 32, log m = log(1 + u) - log r,
 // u = r m - 1, |u| < 0.017, by its series (table-driven, after P. Tang, "Table-driven implementation of the logarithm
 // function", 1990).
 __constant__ double kLog[32][2] = {
@@ -403,6 +405,143 @@ __device__ __forceinline__ double log_of(double s) {
   return fma((double)k, kLn2, kLog[i][1] + fma(u * u, t, u));
 }
 
+// How far a row's sum may be off, relative to it: 2^-22 for each term's ex2, two roundings of 2^-24 |t| for its exponent
+// t (over a row's terms, as they weigh, |t| is at most log2 vocab + 1), 18 roundings in a thread's sum, and a last one
+// for what whole numbers of 2^-40 leave off. Relative to the largest logit: three roundings of t, 66 in the sum.
+__device__ __forceinline__ float sum_bound(int64_t vocab, bool byTop) {
+  const float bits = (float)(65 - __clzll(vocab));
+  return 5.9604645e-8f * (byTop ? 71.f + 2.08f * bits : 23.f + 1.39f * bits);
+}
+
+// The log-sum-exp of a row to 1e-10, by all threads of the CTA, for rows whose order the scan's sums leave open. In pairs
+// of 32-bit numbers throughout: d = x - top with its rounding; d = k ln2 / 64 + h + l, k whole, |h| < 0.0055 (reduction in
+// two parts, after W. Cody and W. Waite, 1980); e^d = 2^(k / 64) (1 + h + (l + h^2 / 2 + h^3 / 6 + h^4 / 24)), the power
+// from a table in two parts; sums by the two-sum of D. Knuth. 26 instructions a term: 131,071 terms take 50 us.
+template <typename T>
+__device__ __noinline__ double row_lse(const BeamParams& p, const float* tops, const T* x, unsigned char* dyn) {
+  float2* table = reinterpret_cast<float2*>(dyn);
+  float* wtop = reinterpret_cast<float*>(dyn + 512);
+  double* wsum = reinterpret_cast<double*>(dyn + 576);
+  const int tid = threadIdx.x;
+  float top = -INFINITY;
+  for (int j = tid; j < p.splits; j += kNT) top = fmaxf(top, tops[j]);
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if ((tid & 31) == 0) wtop[tid >> 5] = top;
+  if (tid < 64) {
+    const double t = exp2(tid / 64.0);
+    table[tid] = make_float2((float)t, (float)(t - (double)(float)t));
+  }
+  __syncthreads();
+  for (int w = 0; w < kNT / 32; ++w) top = fmaxf(top, wtop[w]);
+  const f32x2 t2 = f2_dup(top), per = f2_dup(92.3324826f), magic = f2_dup(12582912.f);
+  const f32x2 c1 = f2_dup(-0x1.63p-7f), c2 = f2_dup(0x1.bd0106p-19f);  // -ln2 / 64 in two parts, the first of 9 bits
+  f32x2 S = 0ull, C = 0ull;
+  auto add = [&](float x0, float x1) {
+    const bool on0 = __fsub_rn(x0, top) > -87.f, on1 = __fsub_rn(x1, top) > -87.f;  // the rest is below 2^-125
+    const f32x2 v = f2_pack(on0 ? x0 : top, on1 ? x1 : top);
+    const f32x2 d = f2_sub(v, t2), y = f2_sub(d, v);
+    const f32x2 e = f2_sub(f2_sub(v, f2_sub(d, y)), f2_add(t2, y));  // d + e = x - top
+    const f32x2 kf = f2_fma(d, per, magic), k = f2_sub(kf, magic);
+    const f32x2 r = f2_fma(k, c1, d), rl = f2_fma(k, c2, e);
+    const f32x2 h = f2_add(r, rl), z = f2_sub(h, r), l = f2_add(f2_sub(r, f2_sub(h, z)), f2_sub(rl, z));
+    f32x2 q = f2_fma(h, f2_fma(h, f2_dup(1.f / 24.f), f2_dup(1.f / 6.f)), f2_dup(0.5f));
+    q = f2_fma(f2_mul(h, h), q, l);
+    const int i0 = (int)((uint32_t)kf - 0x4b400000u), i1 = (int)((uint32_t)(kf >> 32) - 0x4b400000u);
+    const float2 u0 = table[i0 & 63], u1 = table[i1 & 63];
+    const f32x2 th = f2_pack(u0.x, u1.x), tl = f2_pack(u0.y, u1.y);
+    const f32x2 scale = f2_bits(on0 ? (uint32_t)((i0 >> 6) + 127) << 23 : 0u, on1 ? (uint32_t)((i1 >> 6) + 127) << 23 : 0u);
+    f32x2 a = f2_fma(th, h, th);
+    f32x2 b = f2_add(f2_fma(th, h, f2_sub(th, a)), f2_fma(th, q, f2_fma(tl, h, tl)));
+    a = f2_mul(a, scale), b = f2_mul(b, scale);  // (exact)
+    const f32x2 s1 = f2_add(S, a), w = f2_sub(s1, S);
+    C = f2_add(C, f2_add(f2_add(f2_sub(S, f2_sub(s1, w)), f2_sub(a, w)), b));
+    S = s1;
+  };
+  int64_t i = tid;
+#pragma unroll 1
+  for (; i + 7 * kNT < p.vocab; i += 8 * kNT) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = (float)x[i + j * kNT];
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) add(v[j], v[j + 1]);
+  }
+#pragma unroll 1
+  for (; i < p.vocab; i += kNT) add((float)x[i], -INFINITY);
+  float s0, s1, e0, e1;
+  f2_unpack(S, s0, s1);
+  f2_unpack(C, e0, e1);
+  double sum = ((double)s0 + (double)s1) + ((double)e0 + (double)e1);
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if ((tid & 31) == 0) wsum[tid >> 5] = sum;
+  __syncthreads();
+  sum = 0.0;
+  for (int w = 0; w < kNT / 32; ++w) sum += wsum[w];
+  __syncthreads();
+  return (double)top + log_of(sum);
+}
+
+// What the choice knows of a request's hypotheses.
+struct Rows {
+  double lse[kMaxBeams], score[kMaxBeams];  // log-sum-exps, scores so far
+  uint64_t up[kMaxBeams], low[kMaxBeams];   // sums in units of 2^-40, 2^32 up + low (0 also where one is not finite),
+  double ref[kMaxBeams];                    // and what they are relative to: an exponent of two, or (byTop) a logit
+  double open;                              // how far apart the scores of two beams' candidates have to be
+  float cut[kMaxBeams];
+  bool alive[kMaxBeams], byTop[kMaxBeams];
+  uint32_t settled, which;  // beams whose sums were taken again, and are to be
+};
+
+// Where candidates of different beams lie closer than `open` among the M best of n (more than kPick: anywhere), their
+// rows' sums are taken again. False if none is.
+template <typename T>
+__device__ __noinline__ bool take_again(const BeamParams& p, int64_t r, int n, Rows& rows, const float* tops,
+                                        unsigned char* dyn) {
+  const uint64_t* ks = reinterpret_cast<const uint64_t*>(dyn);
+  const uint32_t* kf = reinterpret_cast<const uint32_t*>(dyn + 8 * kPick);
+  const int tid = threadIdx.x;
+  if (tid == 0) rows.which = 0;
+  __syncthreads();
+  // Sums that agree in every bit are equal rows', whose errors are equal too.
+  auto both = [&](int b1, int b2) -> uint32_t {
+    const uint32_t open = ~rows.settled & (1u << b1 | 1u << b2);
+    if (b1 == b2 || !rows.alive[b1] || !rows.alive[b2]) return 0;
+    return (open >> b1 & open >> b2 & 1) && rows.up[b1] == rows.up[b2] && rows.low[b1] == rows.low[b2] &&
+                   rows.ref[b1] == rows.ref[b2]
+               ? 0
+               : open;
+  };
+  uint32_t which = 0;
+  if (n <= kPick) {
+#pragma unroll 1
+    for (int c = tid; c < n; c += kNT) {
+      const uint64_t ms = ks[c], low = ordered(unordered(ms) - rows.open), span = ordered(unordered(ms) + rows.open) - low;
+      const uint32_t mf = kf[c], V = (uint32_t)p.vocab, b = mf / V;
+      int rank = 0;
+      uint32_t near = 0;
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        rank += before(ks[j], kf[j], ms, mf) ? 1 : 0;
+        if (ks[j] - low <= span && kf[j] - b * V >= V) near |= both(b, kf[j] / V);
+      }
+      if (rank < p.n_best) which |= near;
+    }
+  } else if (tid < p.beams) {
+    for (int b = 0; b < p.beams; ++b) which |= both(tid, b);
+  }
+  if (which) atomicOr(&rows.which, which);
+  __syncthreads();
+  which = rows.which;
+#pragma unroll 1
+  for (int b = 0; b < p.beams; ++b)
+    if (which >> b & 1) {
+      const T* x = static_cast<const T*>(p.logits) + (r * p.beams + b) * p.row_stride;
+      const double lse = row_lse<T>(p, tops + b * p.splits, x, dyn);
+      if (tid == 0) rows.lse[b] = lse, rows.settled |= 1u << b;
+    }
+  return which != 0;
+}
+
 template <typename T>
 __device__ __forceinline__ bool is_masked(const BeamParams& p, int64_t row, int64_t t) {
   const T x = static_cast<const T*>(p.logits)[row * p.row_stride + t];
@@ -412,15 +551,12 @@ __device__ __forceinline__ bool is_masked(const BeamParams& p, int64_t row, int6
 // One CTA per request. It runs once through little data, so it is bound by latencies, those of its own
 // instructions' fetches among them: loops stay rolled.
 template <typename T>
-__global__ void __launch_bounds__(kNT) k_beam_pick(BeamParams p) {
+__global__ void __launch_bounds__(kNT) k_beam_pick(const __grid_constant__ BeamParams p) {
   extern __shared__ __align__(16) unsigned char dyn[];
   uint64_t* ks = reinterpret_cast<uint64_t*>(dyn);
   uint32_t* kf = reinterpret_cast<uint32_t*>(dyn + 8 * kPick);
   Cand* sc = reinterpret_cast<Cand*>(dyn + 12 * kPick);  // the first kPick candidates
-  __shared__ double lse[kMaxBeams], sco[kMaxBeams], ref[kMaxBeams];  // log-sum-exps, scores
-  __shared__ double rsum[kMaxBeams];  // in units of 2^-40; 0 also where a row's is not finite
-  __shared__ bool alive[kMaxBeams];
-  __shared__ float cut[kMaxBeams];
+  __shared__ Rows rows;
   __shared__ uint64_t hs[kNT], sT;
   __shared__ uint32_t hf[kNT];
   __shared__ int cnt;
@@ -428,7 +564,7 @@ __global__ void __launch_bounds__(kNT) k_beam_pick(BeamParams p) {
   const int64_t r = blockIdx.x;
   const int NL = p.beams * p.splits, NC = NL * M;  // (below 2^25: a slice has 8,192 tokens at least)
   const float mine = tid < p.beams ? p.scores[r * p.beams + tid] : 0.f;
-  if (tid == 0) cnt = 0, sT = 0;
+  if (tid == 0) cnt = 0, sT = 0, rows.settled = 0;
   cudaGridDependencySynchronize();
   const Ws ws = carve(p.ws, p.batch * p.beams * p.splits);
   const int64_t l0 = r * NL;  // the request's first list
@@ -468,85 +604,108 @@ __global__ void __launch_bounds__(kNT) k_beam_pick(BeamParams p) {
     }
     nf = __any_sync(0xffffffffu, nf);
     if (lane == 0) {
-      rsum[b] = nf ? 0.0 : fma((double)up, 4294967296.0, (double)low);
-      ref[b] = e == kByTop ? base : (double)e;
-      alive[b] = e == kByTop;  // for the next step
+      rows.up[b] = nf ? 0 : up;
+      rows.low[b] = nf ? 0 : low;
+      rows.ref[b] = e == kByTop ? base : (double)e;
+      rows.byTop[b] = e == kByTop;
     }
   }
   __syncthreads();
-  if (tid < p.beams) {
-    const bool byTop = alive[tid];
-    const double x = log_of(rsum[tid] * 0x1p-40);  // (of zero: -inf)
-    lse[tid] = x + (byTop ? ref[tid] : ref[tid] * kLn2);
-    sco[tid] = (double)mine;
-    alive[tid] = isfinite(mine) && rsum[tid] != 0.0;
+  if (tid < 32) {
+    const bool mineTop = tid < p.beams && rows.byTop[tid], byTop = __any_sync(0xffffffffu, mineTop);
+    if (tid < p.beams) {
+      const double sum = fma((double)rows.up[tid], 0x1p-8, (double)rows.low[tid] * 0x1p-40);
+      const double x = log_of(sum);  // (of zero: -inf)
+      rows.lse[tid] = x + (mineTop ? rows.ref[tid] : rows.ref[tid] * kLn2);
+      rows.score[tid] = (double)mine;
+      rows.alive[tid] = isfinite(mine) && sum != 0.0;
+    }
+    if (tid == 0) rows.open = p.beams > 1 ? 2.0 * (double)sum_bound(p.vocab, byTop) : 0.0;
   }
   __syncthreads();
   auto look = [&](int e, uint64_t& s, uint32_t& f) -> bool {  // candidate e % M of list e / M
     const Cand c = e < kPick ? sc[e] : gc[e];
     const int b = e / (M * p.splits);
-    if (!(c.x > -INFINITY) || !alive[b] || c.x < cut[b]) return false;
-    s = ordered(sco[b] + ((double)c.x - lse[b]));
+    if (!(c.x > -INFINITY) || !rows.alive[b] || c.x < rows.cut[b]) return false;
+    s = ordered(rows.score[b] + ((double)c.x - rows.lse[b]));
     f = (uint32_t)((int64_t)b * p.vocab + c.t);
     return true;
   };
-  if (tid < p.beams) cut[tid] = -INFINITY;
-  __syncthreads();
-  // A threshold with at least M candidates not below it: the M-th largest of the
-  // threads' best among the lists' first candidates (first few, where there are
-  // fewer lists than M).
   const int first = (M + NL - 1) / NL;
-  uint64_t s, bs = 0;
-  uint32_t f, bf = 0xffffffffu;
-#pragma unroll 1
-  for (int h = tid; h < NL * first; h += kNT)
-    if (look(h / first * M + h % first, s, f) && before(s, f, bs, bf)) bs = s, bf = f;
-  hs[tid] = bs;
-  hf[tid] = bf;
-  __syncthreads();
-  if (bs) {
-    const int n = min(kNT, NL * first);
-    int rank = 0;
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) rank += before(hs[j], hf[j], bs, bf) ? 1 : 0;
-    if (rank == M - 1) sT = bs;
-  }
-  __syncthreads();
-  const uint64_t T0 = sT;  // 0: fewer than M threads have a candidate, so all are taken
-  // Per hypothesis the logit that the threshold stands for, rounded down past every rounding of a score: most
-  // candidates are told by it without 64-bit arithmetic.
-  if (tid < p.beams && T0 && alive[tid]) {
-    const double t = unordered(T0), slack = 4e-15 * (fabs(t) + fabs(sco[tid]) + fabs(lse[tid]));
-    cut[tid] = __double2float_rd((t - sco[tid]) + lse[tid] - slack);
-  }
-  __syncthreads();
-#pragma unroll 1
-  for (int e = tid; e < NC; e += kNT)
-    if (look(e, s, f) && s >= T0) {
-      const int at = atomicAdd(&cnt, 1);
-      if (at < kPick) ks[at] = s, kf[at] = f;
-    }
-  __syncthreads();
-  const int take = min(cnt, M);
+  uint64_t s, bs;
+  uint32_t f, bf;
+  int take;
   float* os = p.out_scores + r * M;
   int32_t* op = p.out_parent + r * M;
   int32_t* ot = p.out_token + r * M;
-  auto put = [&](int at, double score, uint32_t flat) {
+  auto put = [&](int at, double score, uint32_t b, uint32_t flat) {  // (beams x vocab < 2^31)
     os[at] = (float)score;
-    op[at] = (int32_t)(flat / (uint32_t)p.vocab);  // (beams x vocab < 2^31)
-    ot[at] = (int32_t)(flat % (uint32_t)p.vocab);
+    op[at] = (int32_t)b;
+    ot[at] = (int32_t)(flat - b * (uint32_t)p.vocab);
   };
-  if (cnt <= kPick) {
-    const int n = cnt;
-    for (int c = tid; c < n; c += kNT) {
-      const uint64_t ms = ks[c];
-      const uint32_t mf = kf[c];
+#pragma unroll 1
+  for (;;) {  // once, but where sums are taken again
+    if (tid < p.beams) rows.cut[tid] = -INFINITY;
+    __syncthreads();
+    // A threshold with at least M candidates not below it: the M-th largest of the
+    // threads' best among the lists' first candidates (first few, where there are
+    // fewer lists than M).
+    bs = 0, bf = 0xffffffffu;
+#pragma unroll 1
+    for (int h = tid; h < NL * first; h += kNT)
+      if (look(h / first * M + h % first, s, f) && before(s, f, bs, bf)) bs = s, bf = f;
+    hs[tid] = bs;
+    hf[tid] = bf;
+    __syncthreads();
+    if (bs) {
+      const int n = min(kNT, NL * first);
       int rank = 0;
 #pragma unroll 4
-      for (int j = 0; j < n; ++j) rank += before(ks[j], kf[j], ms, mf) ? 1 : 0;
-      if (rank < M) put(rank, unordered(ms), mf);
+      for (int j = 0; j < n; ++j) rank += before(hs[j], hf[j], bs, bf) ? 1 : 0;
+      // Those within `open` below it may yet come before it.
+      if (rank == M - 1) sT = ordered(unordered(bs) - rows.open);
     }
-  } else {
+    __syncthreads();
+    const uint64_t T0 = sT;  // 0: fewer than M threads have a candidate, so all are taken
+    // Per hypothesis the logit that the threshold stands for, rounded down past every rounding of a score: most
+    // candidates are told by it without 64-bit arithmetic.
+    if (tid < p.beams && T0 && rows.alive[tid]) {
+      const double t = unordered(T0), slack = 4e-15 * (fabs(t) + fabs(rows.score[tid]) + fabs(rows.lse[tid]));
+      rows.cut[tid] = __double2float_rd((t - rows.score[tid]) + rows.lse[tid] - slack);
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int e = tid; e < NC; e += kNT)
+      if (look(e, s, f) && s >= T0) {
+        const int at = atomicAdd(&cnt, 1);
+        if (at < kPick) ks[at] = s, kf[at] = f;
+      }
+    __syncthreads();
+    const int n = cnt;
+    take = min(n, M);
+    // In their order, a step from one beam's to another's within `open` says that there may be a closer look to take.
+    bool close = n > kNT;
+    if (n <= kPick) {
+      for (int c = tid; c < n; c += kNT) {
+        const uint64_t ms = ks[c];
+        const uint32_t mf = kf[c];
+        int rank = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) rank += before(ks[j], kf[j], ms, mf) ? 1 : 0;
+        const double score = unordered(ms);
+        const uint32_t b = mf / (uint32_t)p.vocab;
+        if (rank < M) put(rank, score, b, mf);
+        if (rank < kNT) hs[rank] = ms, hf[rank] = b;
+      }
+      __syncthreads();
+      if (tid + 1 < min(n, kNT) && hf[tid] != hf[tid + 1])
+        close = unordered(hs[tid]) - unordered(hs[tid + 1]) <= rows.open;
+    }
+    if (!__syncthreads_or(close) || !take_again<T>(p, r, n, rows, ws.top + l0, dyn)) break;
+    __syncthreads();
+    if (tid == 0) cnt = 0, sT = 0;
+  }
+  if (cnt > kPick) {
     // More at the threshold than the list holds: one after the other, the best of those after the last one.
     uint64_t ls = 0xffffffffffffffffull;
     uint32_t lf = 0;
@@ -563,20 +722,20 @@ __global__ void __launch_bounds__(kNT) k_beam_pick(BeamParams p) {
       for (int j = 0; j < kNT; ++j)
         if (before(hs[j], hf[j], ls, lf)) ls = hs[j], lf = hf[j];
       any = true;
-      if (tid == 0) put(i, unordered(ls), lf);
+      if (tid == 0) put(i, unordered(ls), lf / (uint32_t)p.vocab, lf);
     }
   }
   // Fewer finite candidates than n_best: tokens that score -inf, in the order of their index.
   if (take < M && tid < 32) {
     int at = take;
     for (int b = 0; b < p.beams && at < M; ++b) {
-      const bool dead = !alive[b];
+      const bool dead = !rows.alive[b];
       for (int64_t t0 = 0; t0 < p.vocab && at < M; t0 += 32) {
         const int64_t t = t0 + tid;
         const bool yes = t < p.vocab && (dead || is_masked<T>(p, r * p.beams + b, t));
         const unsigned all = __ballot_sync(0xffffffffu, yes);
         const int mine = at + __popc(all & ((1u << tid) - 1u));
-        if (yes && mine < M) put(mine, -INFINITY, (uint32_t)((int64_t)b * p.vocab + t));
+        if (yes && mine < M) put(mine, -INFINITY, b, (uint32_t)((int64_t)b * p.vocab + t));
         at += __popc(all);
       }
     }
