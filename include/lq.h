@@ -347,10 +347,11 @@ typedef struct {
 void lq_la_config_default(lq_la_config* cfg, int32_t heads, int32_t key_heads, int32_t dtype);
 
 /*
- * Bytes of workspace lq_la_prefill needs for n_seqs sequences with n_tokens tokens
- * in all, the longest of max_len (0: not known); 0 when it needs none or when an
- * argument is invalid. Host only. It needs some where sequences may be split: 64 KB
- * per head and segment, and 64 KB per head and sequence.
+ * Bytes of workspace that are enough for lq_la_prefill with up to n_seqs sequences and
+ * n_tokens tokens in all, none longer than max_len (0: not known); 0 when no such call
+ * needs any or when an argument is invalid. Host only. A call needs some where sequences
+ * may be split: 64 KB per head and segment, and 64 KB per head and sequence. (A call with
+ * fewer tokens may be split where one with more is not: ask for the largest sizes once.)
  */
 size_t lq_la_workspace_bytes(const lq_la_config* cfg, int64_t n_seqs, int64_t n_tokens, int64_t max_len);
 
@@ -369,8 +370,8 @@ size_t lq_la_workspace_bytes(const lq_la_config* cfg, int64_t n_seqs, int64_t n_
  *              it; 0 forgets the state.
  *   S0, S_out  fp32 [n_seqs][heads][128][128]; S_out may be S0 itself (in place)
  *   max_len    the longest sequence, or 0 if the caller does not know it
- *   workspace  256-byte aligned, lq_la_workspace_bytes(...) bytes for the same
- *              arguments (NULL if that is 0); its contents need not be kept.
+ *   workspace  256-byte aligned, lq_la_workspace_bytes(...) bytes for these sizes or
+ *              larger ones (NULL if that is 0); its contents need not be kept.
  * States are kept in fp32 and their products are taken to fp32's accuracy whatever the
  * type of the tokens; o is rounded once to cfg->dtype (with 16-bit types, products
  * that only o needs are taken to that type's accuracy).

@@ -691,8 +691,7 @@ void lq_la_config_default(lq_la_config* cfg, int32_t heads, int32_t key_heads, i
 
 size_t lq_la_workspace_bytes(const lq_la_config* cfg, int64_t n_seqs, int64_t n_tokens, int64_t max_len) {
   if (check_prompt_sizes(cfg, n_seqs, n_tokens, max_len) || n_seqs == 0) return 0;
-  int64_t seg, slots;
-  lqi::la_plan(cfg, n_seqs, n_tokens, max_len, &seg, &slots);
+  const int64_t slots = lqi::la_most_slots(cfg, n_seqs, n_tokens, max_len);
   return slots ? la_workspace(cfg, n_seqs, slots) : 0;
 }
 

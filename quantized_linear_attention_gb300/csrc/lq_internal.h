@@ -151,8 +151,9 @@ struct ReorderParams {
 };
 
 // Tokens per segment (0: whole sequences) and the segments there can be, by size.
-// (Fewer tokens at the same max_len never need more.)
 void la_plan(const lq_la_config* c, int64_t n_seqs, int64_t n_tokens, int64_t max_len, int64_t* seg, int64_t* slots);
+// No call of these sizes or smaller ones has more segments.
+int64_t la_most_slots(const lq_la_config* c, int64_t n_seqs, int64_t n_tokens, int64_t max_len);
 size_t beam_workspace(int64_t batch, int beams, int64_t vocab, int n_best);
 int beam_splits(int dtype, int64_t vocab);
 

@@ -428,6 +428,22 @@ void la_plan(const lq_la_config* c, int64_t n_seqs, int64_t n_tokens, int64_t ma
   *slots = n_tokens / *seg + n_seqs;
 }
 
+// A call with fewer tokens may be split where a larger one is not, and its segments are rounded, so this is not la_plan's
+// answer for the largest. With W CTAs' shares (152 or 304) a call of n tokens is split only if 5 min(longest, n) > 8 (n heads / W),
+// the quotient rounded down: where any n is, one of the shortest or (past 2,048) the longest is. A segment of g tokens
+// has n < (g + 1) pieces / heads, so n / g < pieces / heads (1 + 1 / g), but for the longest segments, of 1,024.
+int64_t la_most_slots(const lq_la_config* c, int64_t n_seqs, int64_t n_tokens, int64_t max_len) {
+  const int64_t longest = max_len > 0 && max_len < n_tokens ? max_len : n_tokens, h = c->heads;
+  const bool bf16 = c->dtype == LQ_BF16;
+  const int64_t share = bf16 ? 152 : 304, least = bf16 ? 1025 : 257;
+  if (longest < least || ((8 * h - 5 * share) * least >= 8 * share && (bf16 || longest <= 2048))) return 0;
+  const int64_t pieces = !bf16 ? 304 : h < 152 ? 304 - h : 152, g = bf16 ? 512 : 128;
+  int64_t n = pieces * (g + 1) / (h * g);
+  if (n > n_tokens / g) n = n_tokens / g;
+  if (!bf16 && n < n_tokens / 1024) n = n_tokens / 1024;
+  return n + n_seqs;
+}
+
 cudaError_t launch_la_prefill(const LaParams& p, cudaStream_t st) {
   const int64_t longest = p.max_len > 0 && p.max_len < p.n_tokens ? p.max_len : p.n_tokens;
   if (p.dtype == LQ_BF16) return longest <= kShort ? prefill<__nv_bfloat16>(p, st) : launch_la_chunk_bf16(p, st);

@@ -287,6 +287,7 @@ def la_config(heads, key_heads=None, dtype=None) -> LaConfig:
 
 
 def la_workspace_bytes(cfg: LaConfig, n_seqs: int, n_tokens: int, max_len: int = 0) -> int:
+    """Bytes that are enough for ``la_prefill`` with up to these sizes (0: no such call needs any)."""
     return int(load().lq_la_workspace_bytes(ctypes.byref(cfg), n_seqs, n_tokens, max_len))
 
 
@@ -335,7 +336,7 @@ def la_prefill(cfg: LaConfig, q, k, v, alpha, o, cu_seqlens=None, max_len=0, S0=
     """Linear attention over packed prompts: q, k [tokens][key_heads][128], v, o [tokens][heads][128] (strided
     tokens allowed), alpha fp32 [tokens][heads] (``expand`` a [heads] vector for fixed decays), cu_seqlens int32
     [n_seqs + 1] on the device (None: one sequence), S0, S_out fp32 [n_seqs][heads][128][128]. workspace:
-    uint8 tensor of ``la_workspace_bytes``."""
+    uint8 tensor of ``la_workspace_bytes`` for these sizes or larger ones."""
     import torch
 
     c, pq, pk, pv, pa, po, n = _la_tokens(cfg, q, k, v, alpha, o)
