@@ -27,7 +27,9 @@ namespace {
 // The decay would take a third multiplication per entry. It is kept apart instead: S = A s with one number A
 // for the whole state, s += (v / A) k^T, o = A (s q). Every 8 tokens A goes back into s, in two parts (rounded
 // to one it would be off in the same direction again and again), and so it does before a token at which it
-// would leave 2^-12 .. 2^12 (a decay of zero among them) or is not a number.
+// would leave 2^-12 .. 2^12 (a decay of zero among them) or is not a number. So s and v / A may pass fp32's largest number
+// where S and v do not, and an infinity in s becomes NaN by the second part of A: where the state or an output comes
+// out not finite, the CTA takes its tokens again as the recurrence is written (redo).
 //
 // 2,764 fp32 tokens of 4 sequences x 16 heads: 174 us, 55 in the first pass and 117 in the second. The packed FMAs
 // alone are 60 of those 117; with 16 warps to an SM the shuffles' and shared memory's latencies are not all covered.
@@ -45,20 +47,25 @@ struct RecTok {
 
 template <typename T, bool OUT>
 __global__ void __launch_bounds__(256, 2) k_la_recurrent(LaParams p) {
-  __shared__ __align__(16) float sk[2][kRecTok][kD], sq[2][OUT ? kRecTok : 1][kD];
   using Val = typename std::conditional<OUT, f32x2, float>::type;
-  __shared__ __align__(16) Val sv[2][kRecTok][kD];
+  constexpr int kQ = OUT ? kRecTok : 1, kBufK = 2 * kRecTok * kD * 4, kBufQ = OUT ? 2 * kQ * kD * 4 : 0;
+  __shared__ __align__(16) char buf[kBufK + kBufQ + 2 * kRecTok * kD * sizeof(Val)];
+  static_assert(sizeof(buf) >= (3 * kD + 1) * kRecTok * 4, "redo's tokens");
+  float(*const sk)[kRecTok][kD] = reinterpret_cast<float(*)[kRecTok][kD]>(buf);
+  float(*const sq)[kQ][kD] = reinterpret_cast<float(*)[kQ][kD]>(buf + kBufK);
+  Val(*const sv)[kRecTok][kD] = reinterpret_cast<Val(*)[kRecTok][kD]>(buf + kBufK + kBufQ);
   __shared__ RecTok tok[4][kRecTok + 1];
   __shared__ bool even[4];  // no token of the block needs A put back before it
   __shared__ float2 sprod[8];
   __shared__ Piece spc;
+  __shared__ int again;
   cudaTriggerProgrammaticLaunchCompletion();
   const int tid = threadIdx.x, tx = tid & 15, row = 8 * (tid >> 4), warp = tid >> 5, lane = tid & 31;
   const int h = (int)(blockIdx.x % (unsigned)p.heads), kh = h / p.group;
   const int64_t slot = blockIdx.x / (unsigned)p.heads;
   if (tid < 32) {
     const Piece f = find_piece(p, slot);
-    if (tid == 0) spc = f;
+    if (tid == 0) spc = f, again = 0;
   }
   __syncthreads();
   const Piece pc = spc;
@@ -154,6 +161,7 @@ __global__ void __launch_bounds__(256, 2) k_la_recurrent(LaParams p) {
       for (int c = 0; c < 4; ++c) S[x][c] = f2_fma(S[x][c], h2, f2_mul(S[x][c], l2));
   };
   T* out = o + pc.begin * p.so + row + (tx >> 1);
+  float odd = 0.f;  // NaN once an output is not finite
   auto token = [&](int s, int t, float A) {
     const ulonglong2 k0 = *reinterpret_cast<const ulonglong2*>(&sk[s][t][4 * tx]);
     const ulonglong2 k1 = *reinterpret_cast<const ulonglong2*>(&sk[s][t][64 + 4 * tx]);
@@ -197,7 +205,9 @@ __global__ void __launch_bounds__(256, 2) k_la_recurrent(LaParams p) {
         }
       }
       r[0] = __fadd_rn(r[0], __shfl_xor_sync(0xffffffffu, r[0], 1));
-      if (!(tx & 1)) *out = from_f<T>(__fmul_rn(r[0], A));
+      r[0] = __fmul_rn(r[0], A);
+      odd = __fmaf_rn(r[0], 0.f, odd);
+      if (!(tx & 1)) *out = from_f<T>(r[0]);
       out += p.so;
     }
   };
@@ -225,7 +235,19 @@ __global__ void __launch_bounds__(256, 2) k_la_recurrent(LaParams p) {
     }
     scale(tk[kRecTok].hi, tk[kRecTok].lo);
   }
-  if (S_out) {
+  f32x2 sum = f2_pack(odd, 0.f);  // (an entry that is not finite never comes back)
+#pragma unroll
+  for (int x = 0; x < 8; ++x)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) sum = f2_fma(S[x][c], 0ull, sum);
+  float s0, s1;
+  f2_unpack(sum, s0, s1);
+  if (s0 != 0.f || s1 != 0.f) again = 1;
+  __syncthreads();
+  if (again) {
+    redo<T, OUT, 256, kRecTok>(p, spc.begin, spc.len, h, OUT ? start_state(p, spc, slot, h) : nullptr,
+                               reinterpret_cast<float*>(buf), S_out, nullptr);
+  } else if (S_out) {
 #pragma unroll
     for (int x = 0; x < 8; ++x)
 #pragma unroll

@@ -128,6 +128,78 @@ __device__ __forceinline__ const float* start_state(const LaParams& p, const Pie
   return p.S0 ? p.S0 + (pc.b * p.heads + h) * (kD * kD) : nullptr;
 }
 
+// A piece again token by token, exactly as the recurrence is written: the first NT threads of the CTA (all of it come here), four
+// lanes to a row, 32 columns each, TOK tokens staged at a time in sm, (3 kD + 1) TOK floats. `from` NULL: from zero.
+// OUT: with outputs. decay, if not NULL, gets the product of the decays. For pieces in which a faster form's own
+// intermediate values have left fp32's range, or may have: their number counts, not their time.
+template <typename T, bool OUT, int NT, int TOK>
+__device__ __noinline__ void redo(const LaParams& p, int64_t begin, int64_t len, int h, const float* from, float* sm,
+                                  float* S_out, float2* decay) {
+  const int tid = threadIdx.x, part = tid & 3, kh = h / p.group;
+  float(*sk)[kD] = reinterpret_cast<float(*)[kD]>(sm);
+  float(*sq)[kD] = sk + TOK;
+  float(*sv)[kD] = sq + TOK;
+  float* sa = reinterpret_cast<float*>(sv + TOK);
+  const T* q = static_cast<const T*>(p.q) + kh * kD;
+  const T* k = static_cast<const T*>(p.k) + kh * kD;
+  const T* v = static_cast<const T*>(p.v) + h * kD;
+  T* o = static_cast<T*>(p.o) + h * kD;
+  double prod = 1.0;
+  for (int row = tid >> 2; row < kD + (tid >> 2); row += NT / 4) {  // (as many rounds for every thread)
+    float S[8][4];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      S[c][0] = S[c][1] = S[c][2] = S[c][3] = 0.f;
+      if (from && tid < NT) ld4(from + row * kD + 4 * (4 * c + part), S[c]);
+    }
+    prod = 1.0;
+    for (int64_t t0 = 0; t0 < len; t0 += TOK) {
+      const int n = (int)min((int64_t)TOK, len - t0);
+      __syncthreads();
+      for (int x = tid; x < 32 * n; x += NT) {
+        if (tid >= NT) break;
+        const int t = x >> 5, c = 4 * (x & 31);
+        const int64_t at = begin + t0 + t;
+        ld4(k + at * p.sk + c, &sk[t][c]);
+        if (OUT) ld4(q + at * p.sq + c, &sq[t][c]);
+        ld4(v + at * p.sv + c, &sv[t][c]);
+        if (c == 0) sa[t] = p.alpha[at * p.sa + h];
+      }
+      __syncthreads();
+      if (tid < NT) {
+        for (int t = 0; t < n; ++t) {
+          const float a = sa[t], vv = sv[t][row];
+          prod *= (double)a;
+          float acc = 0.f;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            float kk[4], qq[4] = {0.f, 0.f, 0.f, 0.f};
+            ld4(&sk[t][4 * (4 * c + part)], kk);
+            if (OUT) ld4(&sq[t][4 * (4 * c + part)], qq);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              S[c][e] = __fmaf_rn(vv, kk[e], __fmul_rn(a, S[c][e]));
+              if (OUT) acc = __fmaf_rn(S[c][e], qq[e], acc);
+            }
+          }
+          if (OUT) {
+            acc += __shfl_xor_sync(0xffffffffu, acc, 1);
+            acc += __shfl_xor_sync(0xffffffffu, acc, 2);
+            if (part == 0) o[(begin + t0 + t) * p.so + row] = from_f<T>(acc);
+          }
+        }
+      }
+    }
+    if (S_out && tid < NT) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        *reinterpret_cast<float4*>(S_out + row * kD + 4 * (4 * c + part)) =
+            make_float4(S[c][0], S[c][1], S[c][2], S[c][3]);
+    }
+  }
+  if (decay && tid == 0) *decay = in_two(prod);
+}
+
 cudaError_t launch_la_chunk_bf16(const LaParams& p, cudaStream_t st);
 
 // The kernels of a split prompt are launched one upon the other: a kernel is set up while the one before still

@@ -267,78 +267,6 @@ using PFN_encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, v
                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// Token by token: 512 threads, four lanes to a row, 32 columns each (as k_la_recurrent).
-// OUT: from the segment's start, with outputs; else from zero, the segment's own sum.
-template <bool OUT>
-__device__ __noinline__ void redo(const LaParams& p, const Piece& pc, int64_t slot, int h, float* sm, float* S_out,
-                                  float2* decay) {
-  const int tid = threadIdx.x, part = tid & 3, row = tid >> 2, kh = h / p.group;
-  float(*sk)[kD] = reinterpret_cast<float(*)[kD]>(sm);
-  float(*sq)[kD] = sk + 16;
-  float(*sv)[kD] = sq + 16;
-  float* sa = reinterpret_cast<float*>(sv + 16);
-  const bf16* q = static_cast<const bf16*>(p.q) + kh * kD;
-  const bf16* k = static_cast<const bf16*>(p.k) + kh * kD;
-  const bf16* v = static_cast<const bf16*>(p.v) + h * kD;
-  bf16* o = static_cast<bf16*>(p.o) + h * kD;
-  if (OUT && p.seg) cudaGridDependencySynchronize();
-  float S[8][4];
-  double prod = 1.0;
-  if (tid < 512) {
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const int col = 4 * (4 * c + part);
-      S[c][0] = S[c][1] = S[c][2] = S[c][3] = 0.f;
-      if (!OUT) continue;
-      const float* from = start_state(p, pc, slot, h);
-      if (from) ld4(from + row * kD + col, S[c]);
-    }
-  }
-  for (int64_t t0 = 0; t0 < pc.len; t0 += 16) {
-    const int n = (int)min((int64_t)16, pc.len - t0);
-    __syncthreads();
-    if (tid < 512 && (tid >> 5) < n) {
-      const int t = tid >> 5, c = 4 * (tid & 31);
-      const int64_t at = pc.begin + t0 + t;
-      ld4(k + at * p.sk + c, &sk[t][c]);
-      if (OUT) ld4(q + at * p.sq + c, &sq[t][c]);
-      ld4(v + at * p.sv + c, &sv[t][c]);
-      if (c == 0) sa[t] = p.alpha[at * p.sa + h];
-    }
-    __syncthreads();
-    if (tid < 512) {
-      for (int t = 0; t < n; ++t) {
-        const float a = sa[t], vv = sv[t][row];
-        prod *= (double)a;
-        float acc = 0.f;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          float kk[4], qq[4] = {0.f, 0.f, 0.f, 0.f};
-          ld4(&sk[t][4 * (4 * c + part)], kk);
-          if (OUT) ld4(&sq[t][4 * (4 * c + part)], qq);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            S[c][e] = __fmaf_rn(vv, kk[e], __fmul_rn(a, S[c][e]));
-            if (OUT) acc = __fmaf_rn(S[c][e], qq[e], acc);
-          }
-        }
-        if (OUT) {
-          acc += __shfl_xor_sync(0xffffffffu, acc, 1);
-          acc += __shfl_xor_sync(0xffffffffu, acc, 2);
-          if (part == 0) o[(pc.begin + t0 + t) * p.so + row] = __float2bfloat16_rn(acc);
-        }
-      }
-    }
-  }
-  if (S_out && tid < 512) {
-#pragma unroll
-    for (int c = 0; c < 8; ++c)
-      *reinterpret_cast<float4*>(S_out + row * kD + 4 * (4 * c + part)) =
-          make_float4(S[c][0], S[c][1], S[c][2], S[c][3]);
-  }
-  if (decay && tid == 0) *decay = in_two(prod);
-}
-
 // A's first step: the scores of row i, columns 64 half .. + 63, weighted, masked and rounded to bf16 as an A operand; TWO:
 // what the rounding took off as well (see the products). Loops are kept rolled here and below: five roles run at once,
 // and with everything unrolled the warps waited for instructions more than for data.
@@ -836,8 +764,9 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
     return;
   }
   if (ms.flag) {
-    redo<OUT>(p, pc, slot, h, reinterpret_cast<float*>(la_smem), S_out,
-              OUT ? nullptr : p.ws_decay + slot * p.heads + h);
+    if (OUT && p.seg) cudaGridDependencySynchronize();
+    redo<bf16, OUT, 512, 16>(p, pc.begin, pc.len, h, OUT ? start_state(p, pc, slot, h) : nullptr,
+                             reinterpret_cast<float*>(la_smem), S_out, OUT ? nullptr : p.ws_decay + slot * p.heads + h);
     return;
   }
   if (!OUT && tid == 0) p.ws_decay[slot * p.heads + h] = in_two(ms.prod[0] * ms.prod[1]);

@@ -1,0 +1,92 @@
+"""Prompts (lq_la_prefill) at the ends of fp32's range: values, states and decays that are large, infinite or not a number,
+compared with the 64-bit recurrence entry by entry, the sign of every infinity included."""
+import numpy as np
+import pytest
+import torch
+
+from quantized_linear_attention_gb300 import lq
+from tests._generation import D, la_reference, output_bound, rel, state_bound
+from tests.test_la_gpu import f64, inputs, run
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+TYPES = [torch.bfloat16, torch.float16, torch.float32]
+INF = float("inf")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    lq.load()
+    torch.cuda.set_device(0)
+
+
+def same(got, want, bound):
+    """NaN, inf and -inf where the reference has them; the finite entries within `bound` of it."""
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    assert np.array_equal(np.isposinf(got), np.isposinf(want)) and np.array_equal(np.isneginf(got), np.isneginf(want))
+    fine = np.isfinite(want)
+    assert rel(got[fine], want[fine]) <= bound, rel(got[fine], want[fine])
+
+
+def check(q, k, v, a, lens, S0, o, S):
+    o_r, S_r = la_reference(f64(q), f64(k), f64(v), f64(a), lens, None if S0 is None else f64(S0))
+    n = max(lens)
+    same(f64(S), S_r, state_bound(n))
+    same(f64(o), o_r, output_bound(q.dtype, n))
+
+
+@pytest.mark.parametrize("dtype,n", [(torch.float32, 5), (torch.float32, 90), (torch.bfloat16, 11), (torch.bfloat16, 200)])
+@pytest.mark.parametrize("decay", [0.4, 0.05])
+def test_large_finite_values(dtype, n, decay):
+    """Values near 1e37: kept divided by the product of a few decays they would pass fp32's largest number."""
+    q, k, v, a, _ = inputs(1, [n], 2, 1, dtype)
+    v *= 1e36
+    a.fill_(decay)
+    o, S = run(q, k, v, a, [n])
+    check(q, k, v, a, [n], None, o, S)
+
+
+@pytest.mark.parametrize("n", [6, 60])
+def test_large_states_and_queries(n):
+    """States near 1e35 that decay at once and queries near 150: divided by the decays the output's sum would pass the
+    largest number."""
+    q, k, v, a, _ = inputs(2, [n], 2, 1, torch.float32)
+    q *= 150
+    a.fill_(0.3)
+    S0 = 1e35 * torch.randn(1, 2, D, D, generator=torch.Generator(device=DEV).manual_seed(1), device=DEV)
+    o, S = run(q, k, v, a, [n], S0)
+    check(q, k, v, a, [n], S0, o, S)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("value", [INF, -INF])
+@pytest.mark.parametrize("what", ["v", "k", "S0"])
+def test_infinite_states_stay_infinite(dtype, value, what):
+    """An infinity keeps its sign from token to token, whatever the decays; it becomes NaN only as the recurrence says."""
+    lens = [40, 9, 130]
+    q, k, v, a, S0 = inputs(3, lens, 2, 2, dtype, first=True)
+    for b, at in enumerate((3, 40 + 2, 49 + 50)):
+        if what == "S0":
+            S0[b, 1, 17, 5] = value
+        else:
+            {"v": v, "k": k}[what][at, 1, 5] = value
+    o, S = run(q, k, v, a, lens, S0)
+    check(q, k, v, a, lens, S0, o, S)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
+@pytest.mark.parametrize("kind", ["zero", "nan", "infinite", "above one", "negative"])
+def test_odd_decays_beside_infinite_states(dtype, kind):
+    lens = [50]
+    q, k, v, a, S0 = inputs(4, lens, 2, 2, dtype, first=True)
+    k[3, 0, 5] = INF
+    if kind == "above one":
+        a[10:16] = 1.7
+    elif kind == "negative":
+        a[10:31] *= -1
+    else:
+        a[20, 1] = {"zero": 0.0, "nan": float("nan"), "infinite": INF}[kind]
+        if kind == "zero":
+            a[20, 0] = 0.0
+    o, S = run(q, k, v, a, lens, S0)
+    check(q, k, v, a, lens, S0, o, S)
