@@ -70,6 +70,8 @@ __global__ void __launch_bounds__(256, 2) k_la_recurrent(LaParams p) {
   __syncthreads();
   const Piece pc = spc;
   if (pc.b < 0 || (!OUT && pc.i == pc.n - 1)) return;
+  float2* const serial = serial_note(p, pc, slot, h);
+  if (!OUT && pc.i == 0 && tid == 0 && serial) *serial = make_float2(0.f, 0.f);
   float* S_out = OUT ? (pc.i == pc.n - 1 && p.S ? p.S + (pc.b * p.heads + h) * (kD * kD) : nullptr)
                      : p.ws_state + (slot * p.heads + h) * (kD * kD);
   const T* q = static_cast<const T*>(p.q) + kh * kD;
@@ -89,6 +91,16 @@ __global__ void __launch_bounds__(256, 2) k_la_recurrent(LaParams p) {
       S[x][2 * c] = f2_pack(y.x, y.y);
       S[x][2 * c + 1] = f2_pack(y.z, y.w);
     }
+
+  if (OUT && serial && serial->x != 0.f) {
+    if (pc.i) return;
+    int64_t begin, len;
+    bounds(p, pc.b, begin, len);
+    const int64_t at = (pc.b * p.heads + h) * (kD * kD);
+    redo<T, true, 256, kRecTok>(p, begin, len, h, p.S0 ? p.S0 + at : nullptr, reinterpret_cast<float*>(buf),
+                                p.S ? p.S + at : nullptr, nullptr);
+    return;
+  }
 
   // Tokens of a block: warp w takes token w of each, a lane four channels.
   float ld[3][4];
@@ -296,6 +308,7 @@ __device__ __forceinline__ void scan_sequence(const LaParams& p, int64_t b, int 
   float* w = p.ws_state + (first * p.heads + h) * (kD * kD) + at;
   const int64_t pitch = (int64_t)p.heads * (kD * kD);
   constexpr int kAhead = 4;
+  float odd = 0.f;  // NaN once a state is not finite
   for (int64_t i = 0; i < n; i += kAhead) {
     float u[kAhead][4];
     float2 d[kAhead];
@@ -312,8 +325,11 @@ __device__ __forceinline__ void scan_sequence(const LaParams& p, int64_t b, int 
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[e] = __fmaf_rn(s[e], d[x].x, __fmaf_rn(s[e], d[x].y, u[x][e]));
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) odd = __fmaf_rn(s[e], 0.f, odd);  // (S0 among them)
     }
   }
+  if (odd != 0.f) p.ws_decay[(first + n - 1) * p.heads + h] = make_float2(1.f, 0.f);
 }
 
 __global__ void __launch_bounds__(256, 5) k_la_scan(LaParams p) {

@@ -128,6 +128,16 @@ __device__ __forceinline__ const float* start_state(const LaParams& p, const Pie
   return p.S0 ? p.S0 + (pc.b * p.heads + h) * (kD * kD) : nullptr;
 }
 
+// Split sequences in which a state between the segments is not finite: where a segment's decays multiply to infinity (a
+// zero state stays zero under them) or a state is infinite (under the second part of a product it is NaN), the sum over
+// segments is not the recurrence any more. k_la_scan notes them, and the second pass takes such a sequence's head token by
+// token in its first segment's CTA. The note is where the last segment's product would be, which nothing needs; slots
+// past the workspace (sequences that overlap, against the rules) have none.
+__device__ __forceinline__ float2* serial_note(const LaParams& p, const Piece& pc, int64_t slot, int h) {
+  const int64_t last = slot - pc.i + pc.n - 1;
+  return pc.n > 1 && last < p.slots ? p.ws_decay + last * p.heads + h : nullptr;
+}
+
 // A piece again token by token, exactly as the recurrence is written: the first NT threads of the CTA (all of it come here), four
 // lanes to a row, 32 columns each, TOK tokens staged at a time in sm, (3 kD + 1) TOK floats. `from` NULL: from zero.
 // OUT: with outputs. decay, if not NULL, gets the product of the decays. For pieces in which a faster form's own

@@ -93,7 +93,7 @@ struct Misc {
   uint64_t vfull[4], vfree[4];  // of a quarter's buffer: parts are in TMEM; products have read them
   uint64_t drain;               // all products are done
   uint32_t tmem;
-  int abort, flag;
+  int abort, flag, serial;
   double prod[2];
   int64_t piece[5];
 };
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
     mbar_init(&ms.ofree, 256);
     mbar_init(&ms.sready, 256);
     mbar_init(&ms.drain, 1);
-    ms.abort = ms.flag = 0;
+    ms.abort = ms.flag = ms.serial = 0;
     ms.prod[0] = ms.prod[1] = 1.0;
   }
   tc_before();
@@ -361,6 +361,8 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
       asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(ms.tmem) : "memory");
     return;
   }
+  float2* const serial = serial_note(p, pc, slot, h);
+  if (!OUT && pc.i == 0 && tid == 0 && serial) *serial = make_float2(0.f, 0.f);
   // Where the state after the piece goes.
   float* S_out = OUT ? (last && p.S ? p.S + (pc.b * p.heads + h) * (kD * kD) : nullptr)
                      : p.ws_state + (slot * p.heads + h) * (kD * kD);
@@ -466,7 +468,8 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
         if (n == kC) {
           fence_proxy_async();
           arrive(&ms.oready[c & 1]);
-        } else {  // the rows past the end are not this sequence's: each warp writes those of its 32 that are
+        } else if (!*reinterpret_cast<volatile int*>(&ms.serial)) {
+          // the rows past the end are not this sequence's: each warp writes those of its 32 that are
           __syncwarp();
           const int e = lane & 7;
           for (int r = 32 * quad + (lane >> 3); r < min(n, 32 * quad + 32); r += 4)
@@ -486,6 +489,8 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
     {
       if (OUT && p.seg) cudaGridDependencySynchronize();
       const float* from = OUT ? start_state(p, pc, slot, h) : nullptr;
+      // (o waits for this thread's part of S, and looks at the note after that)
+      if (OUT && serial && tid == 256 && serial->x != 0.f) *reinterpret_cast<volatile int*>(&ms.serial) = 1;
 #pragma unroll
       for (int e = 0; e < 32; ++e) S[e] = 0ull;
       if (from) {  // a lane has a row: 32 bytes at a time where the address allows
@@ -554,7 +559,8 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
     if (s0 != 0.f || s1 != 0.f) ms.flag = 1;
     asm volatile("bar.sync 1, 256;" ::: "memory");
     // (odd decays were flagged before their sums were handed over)
-    if (S_out && !*reinterpret_cast<volatile int*>(&ms.flag) && !*reinterpret_cast<volatile int*>(ab)) {
+    if (S_out && !*reinterpret_cast<volatile int*>(&ms.flag) && !*reinterpret_cast<volatile int*>(ab) &&
+        !*reinterpret_cast<volatile int*>(&ms.serial)) {
       float* dst = S_out + row * kD + 64 * half;
       if ((uintptr_t)dst % 32 == 0) {
 #pragma unroll
@@ -587,7 +593,7 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
       if (n > 0) issued = c + 1;
       if (OUT && c >= 2 && pc.len >= (int64_t)(c - 1) * kC) {  // chunk c - 2 is a full one
         if (!wait_warp(&ms.oready[s], ((c - 2) >> 1) & 1, ab)) break;
-        if (lane == 0) {
+        if (lane == 0 && !*reinterpret_cast<volatile int*>(&ms.serial)) {
           for (int x = 0; x < 2; ++x) tma_store(&mo, h * kD + 64 * x, t0 - 2 * kC, dst + 16384 * x);
           asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
@@ -753,6 +759,15 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
   tc_after();
   if (warp == 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
+  if (OUT && ms.serial) {  // nothing has been written
+    if (pc.i) return;
+    int64_t begin, len;
+    bounds(p, pc.b, begin, len);
+    const int64_t at = (pc.b * p.heads + h) * (kD * kD);
+    redo<bf16, true, 512, 16>(p, begin, len, h, p.S0 ? p.S0 + at : nullptr, reinterpret_cast<float*>(la_smem),
+                              p.S ? p.S + at : nullptr, nullptr);
+    return;
+  }
   if (ms.abort) {  // a wait gave up: make that visible (nothing of this CTA is in flight any more)
     const bf16 bad = __float2bfloat16_rn(__int_as_float(0x7fc00000));
     if (OUT)

@@ -90,3 +90,75 @@ def test_odd_decays_beside_infinite_states(dtype, kind):
             a[20, 0] = 0.0
     o, S = run(q, k, v, a, lens, S0)
     check(q, k, v, a, lens, S0, o, S)
+
+
+LONG = 2900  # one head: split in every type
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("first", [False, True])
+def test_split_prompts_whose_decays_pass_the_largest_number(dtype, first):
+    """Decays of 2: their product over a segment is infinite, and the state that it multiplies is zero until the last tokens."""
+    q, k, v, a, _ = inputs(5, [LONG], 1, 1, dtype)
+    v[:LONG - 9] = 0
+    a.fill_(2.0)
+    S0 = torch.zeros(1, 1, D, D, device=DEV) if first else None
+    o, S = run(q, k, v, a, [LONG], S0)
+    check(q, k, v, a, [LONG], S0, o, S)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("value", [INF, -INF, float("nan")])
+@pytest.mark.parametrize("what", ["v", "k", "S0", "alpha"])
+def test_infinities_in_split_prompts(dtype, value, what):
+    """Two split sequences and a short one between; the infinity is in the first, in its second segment or before it."""
+    lens = [LONG, 30, LONG - 300]
+    q, k, v, a, S0 = inputs(6, lens, 1, 1, dtype, first=True)
+    clean_o, clean_S = run(q, k, v, a, lens, S0)
+    if what == "S0":
+        S0[0, 0, 17, 5] = value
+    elif what == "alpha":
+        a[700, 0] = value
+    else:
+        {"v": v, "k": k}[what][700, 0, 5] = value
+    o, S = run(q, k, v, a, lens, S0)
+    check(q, k, v, a, lens, S0, o, S)
+    assert torch.equal(o[LONG:], clean_o[LONG:]) and torch.equal(S[1:], clean_S[1:])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("kind", ["negative", "above one", "zeros", "tiny"])
+def test_odd_decays_in_split_prompts(dtype, kind):
+    lens = [LONG, 30]
+    q, k, v, a, S0 = inputs(7, lens, 1, 1, dtype, first=True, half_life=(20.0, 20000.0))
+    if kind == "negative":
+        a[::3] *= -1
+    elif kind == "above one":
+        a[::2] = 1.003
+    elif kind == "zeros":
+        a[::700] = 0
+    else:
+        a[::700] = 1e-42
+    o, S = run(q, k, v, a, lens, S0)
+    check(q, k, v, a, lens, S0, o, S)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_split_prompts_of_large_finite_values(dtype):
+    """Values near 1e36 (2e4 in fp16) that decay fast, in every segment."""
+    q, k, v, a, S0 = inputs(8, [LONG], 1, 1, dtype, first=True)
+    v *= 4000 if dtype == torch.float16 else 1e36
+    a.fill_(0.3)
+    o, S = run(q, k, v, a, [LONG], S0)
+    fits = np.abs(la_reference(f64(q), f64(k), f64(v), f64(a), [LONG], f64(S0))[0]).max() < torch.finfo(dtype).max
+    assert fits
+    check(q, k, v, a, [LONG], S0, o, S)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_states_in_place_of_split_prompts_with_an_infinity(dtype):
+    q, k, v, a, S0 = inputs(9, [LONG], 1, 1, dtype, first=True)
+    k[700, 0, 5] = INF
+    S = S0.clone()
+    o, _ = run(q, k, v, a, [LONG], S, S_out=S)
+    check(q, k, v, a, [LONG], S0, o, S)
