@@ -381,8 +381,9 @@ size_t lq_la_workspace_bytes(const lq_la_config* cfg, int64_t n_seqs, int64_t n_
  * LQ_ERR_INVALID_ARG, LQ_ERR_UNSUPPORTED; nothing is reported from the device, but
  * should a bounded wait inside the kernel for bf16 tokens give up (2 s; it never
  * should), the sequence's outputs and last state are NaN.
- * With bf16 tokens decays outside 0..1 and values that are not finite take a slow
- * path, token by token.
+ * A head of a sequence whose state or outputs are not finite takes a slow path, token by
+ * token (of a split sequence the segment, or the whole where a state between segments is
+ * not finite); with bf16 tokens so do decays outside 0..1 and outputs past 1e18.
  */
 int lq_la_prefill(const lq_la_config* cfg, int64_t n_seqs, int64_t n_tokens, int64_t max_len,
                   const int32_t* cu_seqlens, const void* q, const void* k, const void* v, const float* alpha,

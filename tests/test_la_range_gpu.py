@@ -162,3 +162,55 @@ def test_states_in_place_of_split_prompts_with_an_infinity(dtype):
     S = S0.clone()
     o, _ = run(q, k, v, a, [LONG], S, S_out=S)
     check(q, k, v, a, [LONG], S0, o, S)
+
+
+@pytest.mark.parametrize("lens", [[100], [300]])
+@pytest.mark.parametrize("what", ["state", "scores"])
+def test_chunked_products_that_pass_the_largest_number_before_they_decay(lens, what):
+    """bf16: S q, or q k, is past fp32's largest number, the decays in front of it are not."""
+    q, k, v, a, S0 = inputs(10, lens, 2, 1, torch.bfloat16, first=True)
+    a.fill_(0.5)
+    a[7::16] = 1e-12
+    q *= 1e12
+    if what == "state":
+        S0 *= 1e30
+        v[:7] = 0
+        q[:7] = 0
+    else:
+        k[7::16] *= 1e30
+        q[7::16] = 0
+        v *= 1e-20
+    o, S = run(q, k, v, a, lens, S0)
+    check(q, k, v, a, lens, S0, o, S)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("value", [INF, -INF, float("nan")])
+@pytest.mark.parametrize("n", [10, 100, 300])
+def test_infinite_queries(dtype, value, n):
+    q, k, v, a, S0 = inputs(11, [n], 2, 2, dtype, first=True)
+    q[n // 2, 1, 5] = value
+    q[n - 1, 0, 9] = value
+    o, S = run(q, k, v, a, [n], S0)
+    check(q, k, v, a, [n], S0, o, S)
+
+
+@pytest.mark.parametrize("n", [100, 300])
+def test_infinite_outputs_of_states_in_place(n):
+    """The tokens are taken again from the first state, which must still be there."""
+    q, k, v, a, S0 = inputs(12, [n], 2, 2, torch.bfloat16, first=True)
+    q[n - 1, 0, 9] = INF
+    S = S0.clone()
+    o, _ = run(q, k, v, a, [n], S, S_out=S)
+    check(q, k, v, a, [n], S0, o, S)
+
+
+def test_infinities_next_to_a_ragged_end_change_nothing_there():
+    """The tokens behind a prompt's last chunk are another prompt's: its infinite queries leave the first one's bits."""
+    lens = [70, 80]
+    q, k, v, a, S0 = inputs(13, lens, 2, 2, torch.bfloat16, first=True)
+    clean_o, clean_S = run(q, k, v, a, lens, S0)
+    q[70:, :, 3] = INF
+    o, S = run(q, k, v, a, lens, S0)
+    check(q, k, v, a, lens, S0, o, S)
+    assert torch.equal(o[:70], clean_o[:70]) and torch.equal(S[0], clean_S[0])
