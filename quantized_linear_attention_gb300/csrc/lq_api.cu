@@ -714,12 +714,14 @@ int lq_la_prefill(const lq_la_config* cfg, int64_t n_seqs, int64_t n_tokens, int
   const size_t nk = la_extent(n_tokens, cfg->k_stride, (int64_t)cfg->key_heads * kD, e);
   const size_t nv = la_extent(n_tokens, cfg->v_stride, (int64_t)cfg->heads * kD, e);
   const size_t no = la_extent(n_tokens, cfg->o_stride, (int64_t)cfg->heads * kD, e);
+  const size_t na = la_extent(n_tokens, cfg->alpha_stride, cfg->heads, 4), nc = cu_seqlens ? (size_t)(n_seqs + 1) * 4 : 0;
   if (S_out && S_out != S0 && S0 && overlaps(S_out, sb, S0, sb))
     return fail(LQ_ERR_INVALID_ARG, "S_out overlaps S0 (it may only be S0 itself)");
   if (S_out && (overlaps(S_out, sb, q, nq) || overlaps(S_out, sb, k, nk) || overlaps(S_out, sb, v, nv) ||
-                overlaps(S_out, sb, o, no) ||
-                overlaps(S_out, sb, alpha, la_extent(n_tokens, cfg->alpha_stride, cfg->heads, 4))))
+                overlaps(S_out, sb, o, no) || overlaps(S_out, sb, alpha, na)))
     return fail(LQ_ERR_INVALID_ARG, "S_out overlaps a token array");
+  if (overlaps(cu_seqlens, nc, o, no) || (S_out && overlaps(cu_seqlens, nc, S_out, sb)))
+    return fail(LQ_ERR_INVALID_ARG, "cu_seqlens overlaps o or S_out");
   if (S0 && overlaps(S0, sb, o, no)) return fail(LQ_ERR_INVALID_ARG, "o overlaps S0");
   lqi::LaParams p = la_params(cfg, q, k, v, alpha, o);
   lqi::la_plan(cfg, n_seqs, n_tokens, max_len, &p.seg, &p.slots);
@@ -730,7 +732,8 @@ int lq_la_prefill(const lq_la_config* cfg, int64_t n_seqs, int64_t n_tokens, int
       return fail(LQ_ERR_INVALID_ARG, "workspace has %zu bytes, %zu are needed", workspace_bytes, need);
     if (overlaps(workspace, need, o, no) || (S_out && overlaps(workspace, need, S_out, sb)) ||
         (S0 && overlaps(workspace, need, S0, sb)) || overlaps(workspace, need, q, nq) ||
-        overlaps(workspace, need, k, nk) || overlaps(workspace, need, v, nv))
+        overlaps(workspace, need, k, nk) || overlaps(workspace, need, v, nv) || overlaps(workspace, need, alpha, na) ||
+        overlaps(workspace, need, cu_seqlens, nc))
       return fail(LQ_ERR_INVALID_ARG, "workspace overlaps another argument");
   }
   int dev = 0;
