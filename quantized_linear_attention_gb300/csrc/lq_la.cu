@@ -334,6 +334,9 @@ __device__ __forceinline__ void scan_sequence(const LaParams& p, int64_t b, int 
 
 __global__ void __launch_bounds__(256, 5) k_la_scan(LaParams p) {
   cudaTriggerProgrammaticLaunchCompletion();
+  // Where no sequence is split, one CTA still waits for the first pass: the kernel after this one, and what the
+  // caller does next in the stream, count on that pass' end when this grid has ended.
+  if (blockIdx.x + blockIdx.y + blockIdx.z == 0) cudaGridDependencySynchronize();
   for (int64_t b = blockIdx.z; b < p.n_seqs; b += gridDim.z) scan_sequence(p, b, blockIdx.y);
 }
 
