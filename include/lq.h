@@ -380,7 +380,7 @@ size_t lq_la_workspace_bytes(const lq_la_config* cfg, int64_t n_seqs, int64_t n_
  * overlap an input. Sequences must not overlap one another. Errors:
  * LQ_ERR_INVALID_ARG, LQ_ERR_UNSUPPORTED; nothing is reported from the device, but
  * should a bounded wait inside the kernel for bf16 tokens give up (2 s; it never
- * should), the sequence's outputs and last state are NaN.
+ * should), the outputs of that head's sequence or segment and its last state are NaN.
  * A head of a sequence whose state or outputs are not finite takes a slow path, token by
  * token (of a split sequence the segment, or the whole where a state between segments is
  * not finite); with bf16 tokens so do decays outside 0..1 and outputs past 1e18.
@@ -477,11 +477,12 @@ int lq_version(void);
  *   wait_ns          the bound on each wait (1..1e9 ns; 0 restores the 1 s default);
  *   extra_tx_append  bytes the append kernels (lq_append, lq_decode_step below
  *                    the window's last token, the two-record and RWKV7 steps)
- *                    announce to their barrier beyond those they copy (0..1024);
+ *                    announce to their barrier beyond those they copy (0..1024),
+ *                    and so does lq_la_prefill for each chunk of bf16 tokens;
  *   extra_tx_fold    the same for the kernels that stage the records (the fused
  *                    last token of a window, lq_fold, the list fold, lq_export_state).
  * With an extra byte count the copies all land and the barrier never completes,
- * so the wait runs out after wait_ns. lq_state_init has no such wait (it reads
+ * so the wait runs out after wait_ns (lq_la_prefill: twice that, per wait). lq_state_init has no such wait (it reads
  * S0 with plain loads). The pages have no counterpart; the failure-detection
  * design is this library's. Errors: LQ_ERR_INVALID_ARG for values out of range.
  */

@@ -364,6 +364,8 @@ lqi::LaParams la_params(const lq_la_config* c, const void* q, const void* k, con
   p.v = v;
   p.alpha = alpha;
   p.o = o;
+  p.wait_ns = g_wait_ns;
+  p.dbg_tx = (uint32_t)g_tx_append;
   return p;
 }
 

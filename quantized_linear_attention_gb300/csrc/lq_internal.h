@@ -131,6 +131,8 @@ struct LaParams {
   float* ws_state;  // [slots][heads][128][128]: what a segment adds to the state
   float2* ws_decay; // [slots][heads]: the product of a segment's decays, in two parts
   float* ws_last;   // [n_seqs][heads][128][128]: last states on their way into S where that is S0
+  uint64_t wait_ns;  // half the bound on a wait of the chunked form
+  uint32_t dbg_tx;   // test hook: bytes announced beyond those copied (0 normally)
 };
 
 struct BeamParams {

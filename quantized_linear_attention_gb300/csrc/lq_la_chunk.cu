@@ -80,6 +80,12 @@ constexpr uint32_t kU = 0, kP = 128, kO = 256;
 template <bool OUT>
 constexpr uint32_t kV3 = OUT ? 384 : 256;
 
+// Whether a wait of the CTA has given up, and after how long one does.
+struct Halt {
+  int abort;
+  uint64_t limit_ns;
+};
+
 struct Misc {
   float2 gamma[4];
   // barriers; of a chunk unless it says otherwise
@@ -94,7 +100,8 @@ struct Misc {
   uint64_t vfull[4], vfree[4];  // of a quarter's buffer: parts are in TMEM; products have read them
   uint64_t drain;               // all products are done
   uint32_t tmem;
-  int abort, flag, serial;
+  int flag, serial;
+  Halt halt;
   double prod[2];
   int64_t piece[5];
 };
@@ -203,7 +210,7 @@ __device__ __forceinline__ void arrive(uint64_t* bar) {
 
 // Waits for phase `parity`; false once this or any other wait of the CTA has given up. The clock is read only after
 // a good many tries (a try waits by itself for a while): reading it first held up every wait.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort) {
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Halt* halt) {
 #pragma unroll 1
   for (int i = 0; i < 4096; ++i)
     if (mbar_try_wait(bar, parity)) return true;
@@ -212,17 +219,17 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort)
 #pragma unroll 1
     for (int i = 0; i < 256; ++i)
       if (mbar_try_wait(bar, parity)) return true;
-    if (*reinterpret_cast<volatile int*>(abort)) return false;
-    if (globaltimer_ns() - t0 > 2000000000ull) {
-      *reinterpret_cast<volatile int*>(abort) = 1;
+    if (*reinterpret_cast<volatile int*>(&halt->abort)) return false;
+    if (globaltimer_ns() - t0 > halt->limit_ns) {
+      *reinterpret_cast<volatile int*>(&halt->abort) = 1;
       return false;
     }
   }
 }
 
 // The same for a whole warp: all lanes go on or none does.
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* abort) {
-  return __all_sync(0xffffffffu, wait(bar, parity, abort));
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Halt* halt) {
+  return __all_sync(0xffffffffu, wait(bar, parity, halt));
 }
 
 // 128 tokens x 64 channels into half a tile; tokens past the tensor's end are zeros. x is a multiple of 64.
@@ -354,7 +361,8 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
     mbar_init(&ms.ofree, 256);
     mbar_init(&ms.sready, 256);
     mbar_init(&ms.drain, 1);
-    ms.abort = ms.flag = ms.serial = 0;
+    ms.flag = ms.serial = 0;
+    ms.halt = Halt{0, 2 * p.wait_ns};
     ms.prod[0] = ms.prod[1] = 1.0;
   }
   tc_before();
@@ -378,7 +386,7 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
   const uint32_t tm = ms.tmem, sb = smem_u32(la_smem);
   float* sG = reinterpret_cast<float*>(la_smem + kSums);
   float* sw = sG + 2 * kC;
-  int* ab = &ms.abort;
+  Halt* const ab = &ms.halt;
   using Ti = Tiles<OUT>;
 
   if (OUT ? warp >= 16 && warp < 24 : warp < 8 || (warp >= 16 && warp < 24)) {
@@ -582,7 +590,7 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
     // (odd decays were flagged before their sums were handed over; A's verdict is waited for only where S0 would be lost)
     if (in_place) asm volatile("bar.sync 3, 512;" ::: "memory");
     else asm volatile("bar.sync 1, 256;" ::: "memory");
-    if (S_out && !*reinterpret_cast<volatile int*>(&ms.flag) && !*reinterpret_cast<volatile int*>(ab) &&
+    if (S_out && !*reinterpret_cast<volatile int*>(&ms.flag) && !*reinterpret_cast<volatile int*>(&ab->abort) &&
         !*reinterpret_cast<volatile int*>(&ms.serial)) {
       float* dst = S_out + row * kD + 64 * half;
       if ((uintptr_t)dst % 32 == 0) {
@@ -609,7 +617,7 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
       uint64_t* bar = n == kC ? &ms.full[s] : &ms.land[s];
       if (c >= Ti::kN && !wait_warp(&ms.empty[s], Ti::phase(c - Ti::kN), ab)) break;
       if (n > 0 && lane == 0) {
-        mbar_expect_tx(bar, Ti::kStage);
+        mbar_expect_tx(bar, Ti::kStage + p.dbg_tx);
         for (int x = 0; x < 2; ++x) tma_tile(dst + Ti::kK + 16384 * x, &mk, kh * kD + 64 * x, t0, bar);
         for (int x = 0; x < 2; ++x) tma_tile(dst + Ti::kV + 16384 * x, &mv, h * kD + 64 * x, t0, bar);
       }
@@ -638,8 +646,8 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
     if (OUT && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     // A wait gave up: what was asked for still has to land before the CTA ends. (In a chunk whose Q was not asked
     // for, the barrier cannot complete: that wait runs into its limit.)
-    int ignored = 0;
-    if (*reinterpret_cast<volatile int*>(ab))
+    Halt ignored = {0, ab->limit_ns};
+    if (*reinterpret_cast<volatile int*>(&ab->abort))
       for (int c = max(0, issued - Ti::kN); c < issued; ++c) {
         const bool whole = pc.len >= (int64_t)(c + 1) * kC;
         wait(whole ? &ms.full[Ti::at(c)] : &ms.land[Ti::at(c)], whole ? Ti::phase(c) : 0, &ignored);
@@ -769,7 +777,7 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
       commit(&ms.drain);
     }
     __syncwarp();
-    int ignored = 0;
+    Halt ignored = {0, ab->limit_ns};
     wait_warp(&ms.drain, 0, &ignored);
   }
   __syncwarp();
@@ -791,7 +799,7 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
                               p.S ? p.S + at : nullptr, nullptr);
     return;
   }
-  if (ms.abort) {  // a wait gave up: make that visible (nothing of this CTA is in flight any more)
+  if (ms.halt.abort) {  // a wait gave up: make that visible (nothing of this CTA is in flight any more)
     const bf16 bad = __float2bfloat16_rn(__int_as_float(0x7fc00000));
     if (OUT)
       for (int64_t x = tid; x < pc.len * kD; x += kThreadsLa)
