@@ -9,8 +9,8 @@
 // 128 x 128 x 128 with fp32 accumulators in TMEM:
 //   P  = Q K^T       both operands from shared memory
 //   O  = Q S^T       S rounded to bf16 in shared memory: only o needs this product,
-//                    and o is rounded to bf16 itself
-//   O += P V         P (weighted, masked, rounded to bf16) from TMEM
+//                    and o is rounded to bf16 itself (in two parts where a chunk is all)
+//   O += P V         P (weighted, masked, rounded to bf16 alike) from TMEM
 //   U  = (wV)^T K    the state's growth. wV is an fp32 number; it goes in as three
 //                    bf16 parts that hold all its 24 bits, so the state keeps fp32's
 //                    accuracy (two parts, 16 bits, round to 2.8e-6 of it).
@@ -383,6 +383,9 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
                      : p.ws_state + (slot * p.heads + h) * (kD * kD);
   const bool in_place = OUT && p.S && p.S == p.S0;
   const int nc = (int)((pc.len + kC - 1) / kC);
+  // Where a single chunk is all, o hangs on few weights and one state, whose roundings need not even out: there what
+  // rounding P and S takes off goes in as well. (S's lies in the second stage of tiles, which has no other use then.)
+  const bool two = OUT && nc == 1, two_s = two && (pc.n > 1 || p.S0);
   const uint32_t tm = ms.tmem, sb = smem_u32(la_smem);
   float* sG = reinterpret_cast<float*>(la_smem + kSums);
   float* sw = sG + 2 * kC;
@@ -447,7 +450,7 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
         const float ei = ex2(gi);
         if (!wait_warp(&ms.qk, c & 1, ab)) break;
         tc_after();
-        if (nc == 1) weigh_scores<true>(tl, G, gi, i, quad, half);
+        if (two) weigh_scores<true>(tl, G, gi, i, quad, half);
         else weigh_scores<false>(tl, G, gi, i, quad, half);
         if (!wait_warp(&ms.qs, c & 1, ab)) break;
         tc_after();
@@ -576,6 +579,15 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
             x[f] = pack_bf16(lo, hi);
           }
           *reinterpret_cast<uint4*>(s16 + ((e ^ (row & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+          if (two_s) {
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+              float lo, hi;
+              f2_unpack(S[4 * e + f], lo, hi);
+              x[f] = pack_bf16(__fsub_rn(lo, __uint_as_float(x[f] << 16)), __fsub_rn(hi, __uint_as_float(x[f] & 0xffff0000u)));
+            }
+            *reinterpret_cast<uint4*>(s16 - kS16 + Ti::kStage + ((e ^ (row & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+          }
         }
         fence_proxy_async();
         arrive(&ms.sready);
@@ -730,6 +742,12 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
               if (c && !(ok = wait(&ms.ofree, (c - 1) & 1, ab))) break;
               tc_after();
               product(tmu + kO, Q, S16);
+              if (two_s) {
+#pragma unroll 1
+                for (int s = 0; s < 8; ++s)
+                  mma_ss<true>(tmu + kO, Q + (s >> 2) * 1024 + (s & 3) * 2,
+                               S16 - kS16 / 16 + Ti::kStage / 16 + (s >> 2) * 1024 + (s & 3) * 2, kIdesc);
+              }
               commit(&ms.qs);
             }
             if (!(ok = wait(&ms.vfull[buf], use & 1, ab))) break;
@@ -754,9 +772,7 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
 #pragma unroll
             for (int s = 0; s < 8; ++s)
               mma_ts<true>(tmu + kO, tmu + kP + 16 * s, Vc + s * 128, kIdescMn);
-            // Where a single chunk is all, o hangs on few weights, whose roundings need not even out: there what
-            // rounding P took off is added.
-            if (nc == 1) {
+            if (two) {
 #pragma unroll 1
               for (int s = 0; s < 8; ++s)
                 mma_ts<true>(tmu + kO, tmu + kP + 16 * s + 8, Vc + s * 128, kIdescMn);
