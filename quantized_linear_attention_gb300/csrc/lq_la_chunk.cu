@@ -522,8 +522,7 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
     {
       if (OUT && p.seg) cudaGridDependencySynchronize();
       const float* from = OUT ? start_state(p, pc, slot, h) : nullptr;
-      // (o waits for this thread's part of S, and looks at the note after that)
-      if (OUT && serial && tid == 256 && serial->x != 0.f) *reinterpret_cast<volatile int*>(&ms.serial) = 1;
+      const float note = OUT && serial && tid == 256 ? serial->x : 0.f;
 #pragma unroll
       for (int e = 0; e < 32; ++e) S[e] = 0ull;
       if (from) {  // a lane has a row: 32 bytes at a time where the address allows
@@ -538,6 +537,23 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
             S[e] = x.x, S[e + 1] = x.y;
           }
         }
+      }
+      // (o waits for this thread's part of S, and looks at this after that)
+      if (note != 0.f) *reinterpret_cast<volatile int*>(&ms.serial) = 1;
+    }
+    char* const s16 = la_smem + kS16 + half * 16384 + row * 128;
+    if (two_s) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        uint32_t x[4];
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+          float lo, hi;
+          f2_unpack(S[4 * e + f], lo, hi);
+          const uint32_t y = pack_bf16(lo, hi);
+          x[f] = pack_bf16(__fsub_rn(lo, __uint_as_float(y << 16)), __fsub_rn(hi, __uint_as_float(y & 0xffff0000u)));
+        }
+        *reinterpret_cast<uint4*>(s16 - kS16 + Ti::kStage + ((e ^ (row & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
       }
     }
     for (int c = 0; c <= nc; ++c) {
@@ -568,7 +584,6 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
       if (!OUT && c + 1 < nc && !wait_warp(&ms.sums[(c + 1) & 1], ((c + 1) >> 1) & 1, ab)) break;
       arrive(&ms.uread[c & 1]);
       if (OUT) {
-        char* s16 = la_smem + kS16 + half * 16384 + row * 128;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           uint32_t x[4];
@@ -579,15 +594,6 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
             x[f] = pack_bf16(lo, hi);
           }
           *reinterpret_cast<uint4*>(s16 + ((e ^ (row & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
-          if (two_s) {
-#pragma unroll
-            for (int f = 0; f < 4; ++f) {
-              float lo, hi;
-              f2_unpack(S[4 * e + f], lo, hi);
-              x[f] = pack_bf16(__fsub_rn(lo, __uint_as_float(x[f] << 16)), __fsub_rn(hi, __uint_as_float(x[f] & 0xffff0000u)));
-            }
-            *reinterpret_cast<uint4*>(s16 - kS16 + Ti::kStage + ((e ^ (row & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
-          }
         }
         fence_proxy_async();
         arrive(&ms.sready);
