@@ -308,7 +308,6 @@ __device__ __forceinline__ void scan_sequence(const LaParams& p, int64_t b, int 
   float* w = p.ws_state + (first * p.heads + h) * (kD * kD) + at;
   const int64_t pitch = (int64_t)p.heads * (kD * kD);
   constexpr int kAhead = 4;
-  float odd = 0.f;  // NaN once a state is not finite
   for (int64_t i = 0; i < n; i += kAhead) {
     float u[kAhead][4];
     float2 d[kAhead];
@@ -325,10 +324,10 @@ __device__ __forceinline__ void scan_sequence(const LaParams& p, int64_t b, int 
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[e] = __fmaf_rn(s[e], d[x].x, __fmaf_rn(s[e], d[x].y, u[x][e]));
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) odd = __fmaf_rn(s[e], 0.f, odd);  // (S0 among them)
     }
   }
+  // (a state that is not finite, S0 among them, never comes back: the last one tells)
+  const float odd = __fmaf_rn(s[0], 0.f, __fmaf_rn(s[1], 0.f, __fmaf_rn(s[2], 0.f, s[3] * 0.f)));
   if (odd != 0.f) p.ws_decay[(first + n - 1) * p.heads + h] = make_float2(1.f, 0.f);
 }
 
