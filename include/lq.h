@@ -359,8 +359,10 @@ size_t lq_la_workspace_bytes(const lq_la_config* cfg, int64_t n_seqs, int64_t n_
  * Linear attention over prompts: sequence b is tokens cu_seqlens[b] ..
  * cu_seqlens[b+1]-1 of the packed arrays; it starts from S0[b] (zero if S0 is
  * NULL) and leaves its last state in S_out[b] (not written if S_out is NULL).
- * S_out in the order [n_seqs][heads] can be handed to lq_state_init_range,
- * lq_fp32_decode_step or lq_la_decode_step as it is.
+ * lq_la_decode_step continues the same recurrence from S_out, in the order
+ * [n_seqs][heads], as it is. The layout is also what lq_state_init, lq_state_init_range
+ * and lq_fp32_decode_step take, but their tokens are delta-rule tokens, another
+ * recurrence: hand them S_out only where a model changes over at that point.
  *   cu_seqlens int32 [n_seqs + 1] on the device, or NULL for one sequence of
  *              n_tokens; a sequence may be empty (its S_out is then its S0). A
  *              sequence whose bounds are not 0 <= begin <= end <= n_tokens, or

@@ -2,8 +2,8 @@
 //   scores[b] + logits[b][t] - log sum_t' exp(logits[b][t'])
 // over its beams b and tokens t, equal scores to the lowest b * vocab + t.
 //
-// Two kernels. k_beam_scan reads the logits once, the only large traffic (HBM
-// bounds it): a CTA holds one slice of one row in registers, sums its
+// Two kernels. k_beam_scan reads the logits once, the only large
+// traffic: a CTA holds one slice of one row in registers, sums its
 // exponentials and keeps its n_best largest logits. Inside a row the order of the
 // scores is the order of the logits, so no score is needed there. k_beam_pick
 // joins a request's slices: log-sum-exps and scores in 64 bits, because the
@@ -12,8 +12,8 @@
 // that leaves certain, their rows' sums are taken again, to 1e-10, and the choice is made anew.
 //
 // The sum of a slice: with m = ceil(max * log2 e), a whole number, each term is
-// 2^(x log2 e - m), its exponent formed by two fmas from a two-part log2 e (one
-// rounding, relative to the exponent itself). Threads' sums join as whole numbers of
+// 2^(x log2 e - m), its exponent formed by two fmas from a two-part log2 e (two
+// roundings, relative to the exponent itself). Threads' sums join as whole numbers of
 // 2^-40 and slices by shifts: exact, and 64-bit floating point is slow here. A slice's sum stays below
 // 2^55, but a row of 2^24 terms of 1 passes 2^64: slices join in two words, their upper and lower 32 bits.
 // Rows with equal contents sum in the same order whatever their place in memory, so equal hypotheses tie exactly.
@@ -25,7 +25,7 @@
 // about 18. Where ties make them more than the list holds, a bisection over
 // (value, index) finds the exact n_best-th key.
 //
-// Measured at 64 x 8 x 131,071 bf16: 53 us, the scan 38 (134 MB, 52% of the copy
+// Measured at 64 x 8 x 131,071 bf16: 52 us, the scan 38 (134 MB, 52% of the copy
 // bandwidth), the choice about 13. The scan is bound by instructions: 62% of the issue
 // slots at half of the warps, the exponentials' unit alone 16 us (without them 42 us in
 // all). Smaller slices were slower, 64 us, by what every slice does once.

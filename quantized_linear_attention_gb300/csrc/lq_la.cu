@@ -31,12 +31,11 @@ namespace {
 // where S and v do not, and an infinity in s becomes NaN by the second part of A: where the state or an output comes
 // out not finite, the CTA takes its tokens again as the recurrence is written (redo).
 //
-// 2,764 fp32 tokens of 4 sequences x 16 heads: 174 us, 55 in the first pass and 117 in the second. The packed FMAs
+// 2,764 fp32 tokens of 4 sequences x 16 heads: 172 us, 54 in the first pass and 117 in the second. The packed FMAs
 // alone are 60 of those 117; with 16 warps to an SM the shuffles' and shared memory's latencies are not all covered.
 constexpr int kRecTok = 8;  // tokens staged at a time
-// Prompts of bf16 tokens up to this length go token by token too: about 6 us and half a microsecond a token against
-// 12.3 us for a first chunk with 4 head-sequences (10.3 at 8 tokens, 14.4 at 16), 39 + 3 to 5 us a token against 136
-// us with 2,048 (64 us at 8 tokens, 103 at 16, 145 at 24).
+// Prompts of bf16 tokens up to this length go token by token too. Replayed from a graph with 4 head-sequences: 5.3 us for
+// 3 tokens, 7.9 for 8, 9.9 for 12, against 9.9 for a chunk; with 2,048: 39 us + 3 to 5 a token against 136.
 constexpr int kShort = 12;
 
 struct RecTok {
@@ -352,7 +351,8 @@ __global__ void k_copy_states(LaParams p, const float* from) {
 // a row, 16 columns each (a warp instruction reads four rows x 128 consecutive
 // bytes); keys and queries come straight from global memory, each lane its own 16
 // channels, so nothing waits on a barrier. P CTAs share a head-state. 16,384 states of
-// bf16 tokens: 322 us for 2.16 GB, 99% of the copy bandwidth; 32 states 4.1 us.
+// bf16 tokens: 324 us for 2.16 GB, 98% of the copy bandwidth; 32 states 2 us replayed from a graph (11 to 14 a call,
+// which is the host's time).
 template <typename T, int P>
 __global__ void __launch_bounds__(256) k_la_step(LaParams p) {
   constexpr int NR = 4 / P;  // row groups of a thread
@@ -424,8 +424,8 @@ cudaError_t prefill(const LaParams& p0, cudaStream_t st) {
 template <typename T>
 cudaError_t step(const LaParams& p, cudaStream_t st) {
   const int64_t n = p.n_seqs * p.heads;
-  // Few head-states: four CTAs share one, so that the loads spread over the SMs (8 and 32 head-states 2.1 us against
-  // 3.1; 128 3.1 either way; 256 4.9 against 4.6, 512 7.7 either way).
+  // Few head-states: four CTAs share one, so that the loads spread over the SMs (replayed from a graph, 8 and 32
+  // head-states 2.1 us against 3.1; 128 3.1 either way; 256 4.9 against 4.6, 512 7.7 either way).
   if (n < 128) k_la_step<T, 4><<<(unsigned)(4 * n), 256, 0, st>>>(p);
   else k_la_step<T, 1><<<(unsigned)n, 256, 0, st>>>(p);
   return cudaGetLastError();

@@ -141,7 +141,8 @@ __device__ __forceinline__ float2* serial_note(const LaParams& p, const Piece& p
 // A piece again token by token, exactly as the recurrence is written: the first NT threads of the CTA (all of it come here), four
 // lanes to a row, 32 columns each, TOK tokens staged at a time in sm, (3 kD + 1) TOK floats. `from` NULL: from zero.
 // OUT: with outputs. decay, if not NULL, gets the product of the decays. For pieces in which a faster form's own
-// intermediate values have left fp32's range, or may have: their number counts, not their time.
+// intermediate values have left fp32's range, or may have: 0.8 to 0.9 us a token (20,000 tokens of one head: 16 ms bf16,
+// 18 ms fp32), bound by a token's latency through shared memory and two barriers for each TOK.
 template <typename T, bool OUT, int NT, int TOK>
 __device__ __noinline__ void redo(const LaParams& p, int64_t begin, int64_t len, int h, const float* from, float* sm,
                                   float* S_out, float2* decay) {

@@ -30,7 +30,7 @@
 // the phase after the next can end: every wait below comes before an arrival of
 // the same warp that this next phase needs. (Slow loads bring a mistake in this to light.)
 //
-// What bounds it, at 32,768 tokens x 32 heads: 333 us, 112 in the first pass and 217 in
+// What bounds it, at 32,768 tokens x 32 heads: 332 us, 110 in the first pass and 217 in
 // the second, 1.9 and 3.5 us a chunk of an SM. Of these the tensor cores take 0.8 and
 // 1.6, HBM at its full rate would take 1.5 and 2.9. The chain's hand-overs make up the rest;
 // taking out the exponentials, the loads of V or the stores, one at a time,

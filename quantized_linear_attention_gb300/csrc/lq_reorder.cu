@@ -7,9 +7,9 @@
 //
 // Bound by HBM: the sources are read once (a source of several beams comes from
 // L1), the moved beams written once, the rest stays where it is; of the record
-// planes only the records held move. 16,384 quantized states in groups of four: 106 us for
-// 603 MB, 84% of the copy bandwidth; 4,096 fp32 states in groups of eight: 68 us for
-// 398 MB, 86%. One CTA takes one (outer, group, inner)
+// planes only the records held move. 16,384 quantized states in groups of four: 105 to 109 us for
+// 603 MB, 81 to 85% of the copy bandwidth; 4,096 fp32 states in groups of eight: 69 to 76 us for
+// 398 MB, 77 to 85%. One CTA takes one (outer, group, inner)
 // position: it alone reads and rewrites the record counts of its beams, so the
 // counts need no second kernel.
 #include <cuda_runtime.h>
