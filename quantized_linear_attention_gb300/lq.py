@@ -369,6 +369,9 @@ def beam_select(logits, scores, out_scores, out_parent, out_token, workspace, st
     workspace: uint8 tensor of ``beam_workspace_bytes``."""
     import torch
 
+    if logits.dim() != 3 or out_scores.dim() != 2:
+        raise ValueError(f"logits must be [batch][beams][vocab] and out_scores [batch][n_best], got {tuple(logits.shape)} "
+                         f"and {tuple(out_scores.shape)}")
     batch, beams, vocab = logits.shape
     s0, s1, s2 = logits.stride()
     if not logits.is_cuda:
@@ -387,7 +390,8 @@ def beam_select(logits, scores, out_scores, out_parent, out_token, workspace, st
     _check(load().lq_beam_select(_dtype_id(logits.dtype), batch, beams, vocab, n_best, logits.data_ptr(), s1,
                                  _ptr(scores, "scores", f), _ptr(out_scores, "out_scores", f),
                                  _ptr(out_parent, "out_parent", i), _ptr(out_token, "out_token", i),
-                                 _ptr(workspace, "workspace"), workspace.nbytes, _stream(stream)))
+                                 _ptr(workspace, "workspace"), 0 if workspace is None else workspace.nbytes,
+                                 _stream(stream)))
 
 
 def _parents(parent):
