@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(kThreadsLa, 1)
     float s0, s1;
     f2_unpack(sum, s0, s1);
     if (s0 != 0.f || s1 != 0.f) ms.flag = 1;
-    // (odd decays were flagged before their sums were handed over; A's verdict is waited for only where S0 would be lost)
+    // (odd decays were flagged before their sums were handed over; what A finds is waited for only where S0 would be lost)
     if (in_place) asm volatile("bar.sync 3, 512;" ::: "memory");
     else asm volatile("bar.sync 1, 256;" ::: "memory");
     if (S_out && !*reinterpret_cast<volatile int*>(&ms.flag) && !*reinterpret_cast<volatile int*>(&ab->abort) &&
