@@ -450,6 +450,134 @@ int lq_state_reorder(const lq_config* cfg, void* state, int64_t n_states, int64_
 int lq_fp32_state_reorder(float* S, int64_t n_states, int64_t outer, int64_t groups, int32_t beams, int64_t inner,
                           const int32_t* parent, lq_stream_t stream);
 
+/* ------------------------------------------------------------------------------
+ * State space layers: the short causal convolution in front of a recurrence, and the
+ * selective scan, over packed prompts (lq_conv_prefill, lq_ssm_prefill) and for single
+ * tokens on their own states (lq_conv_decode_step, lq_ssm_decode_step); and what a
+ * model's logits say about given tokens (lq_token_logprobs).
+ *
+ * Packed sequences are lq_la_prefill's: sequence b is tokens cu_seqlens[b] ..
+ * cu_seqlens[b+1]-1 (int32 [n_seqs + 1] on the device; NULL: one sequence of n_tokens).
+ * A sequence may be empty; one whose bounds are not 0 <= begin <= end <= n_tokens, or
+ * that is longer than a stated max_len, is treated as empty: its last state is its first
+ * one. Tokens that belong to no sequence get no output, and sequences must not overlap
+ * one another. Outputs must not overlap inputs, except where a state may be in place.
+ * Token arrays, weights and states of these calls need the alignment of their elements
+ * only; 16-byte aligned arrays and strides are faster where the text says so.
+ * Errors of these calls: LQ_ERR_INVALID_ARG, LQ_ERR_UNSUPPORTED, LQ_ERR_CUDA; nothing is
+ * reported from the device.
+ * ------------------------------------------------------------------------------ */
+
+typedef struct {
+  int32_t channels;           /* 1..2^20                                                              */
+  int32_t width;              /* W: taps, 2..4                                                         */
+  int32_t dtype;              /* lq_dtype of x, y and the states                                       */
+  int32_t silu;               /* 1: y = s / (1 + e^-s) of the sum s; 0: the sum itself                 */
+  int64_t x_stride, y_stride; /* elements from one token to the next, at least channels                */
+} lq_conv_config;
+
+/* Dense token arrays. */
+void lq_conv_config_default(lq_conv_config* cfg, int32_t channels, int32_t width, int32_t dtype, int32_t silu);
+
+/*
+ * Causal convolution of every channel over packed prompts:
+ *   y[t][c] = act(bias[c] + sum_j weight[c][j] x[t - (W-1) + j][c]),   j = 0..W-1,
+ * where the inputs before a sequence are S0[b] (zero if NULL), its W-1 inputs before
+ * the first, oldest first.
+ *   x, y       [n_tokens][channels] of cfg->dtype (tokens may lie apart)
+ *   weight     fp32 [channels][width];  bias fp32 [channels] or NULL
+ *   S0, S_out  [n_seqs][W-1][channels] of cfg->dtype, or NULL; S_out gets the last W-1
+ *              inputs of each sequence, S0's among them where it has fewer tokens; it may
+ *              be S0 itself
+ * Sums are kept in fp32; y is rounded once. Faster where x, y, S0, S_out, weight and the
+ * strides are multiples of 16 bytes and so is a row of channels.
+ */
+int lq_conv_prefill(const lq_conv_config* cfg, int64_t n_seqs, int64_t n_tokens, int64_t max_len,
+                    const int32_t* cu_seqlens, const void* x, const float* weight, const float* bias, const void* S0,
+                    void* S_out, void* y, lq_stream_t stream);
+
+/*
+ * One token for each of n_seqs sequences: x, y [n_seqs][channels]; S [n_seqs][W-1][channels]
+ * holds each sequence's last inputs, oldest first, and takes x in place of the oldest.
+ */
+int lq_conv_decode_step(const lq_conv_config* cfg, void* S, int64_t n_seqs, const void* x, const float* weight,
+                        const float* bias, void* y, lq_stream_t stream);
+
+typedef struct {
+  int32_t channels, n_state; /* 1..2^20 channels of 1..64 states                                          */
+  int32_t groups;            /* B and C are shared by channels / groups channels in a row; a divisor        */
+  int32_t dtype;             /* lq_dtype of x, dt, z, B, C and y                                             */
+  int32_t softplus;          /* 1: d = log(1 + e^(dt + dt_bias)); 0: d = dt + dt_bias                         */
+  int32_t reserved;          /* 0                                                                            */
+  int64_t x_stride, dt_stride, z_stride, y_stride; /* elements from one token to the next: at least channels */
+  int64_t b_stride, c_stride;                      /* at least groups x n_state                              */
+} lq_ssm_config;
+
+/* Dense token arrays. */
+void lq_ssm_config_default(lq_ssm_config* cfg, int32_t channels, int32_t n_state, int32_t groups, int32_t dtype,
+                           int32_t softplus);
+
+/*
+ * Bytes of workspace that are enough for lq_ssm_prefill with up to n_seqs sequences and
+ * n_tokens tokens in all, none longer than max_len (0: not known); 0 when no such call
+ * needs any or when an argument is invalid. Host only.
+ */
+size_t lq_ssm_workspace_bytes(const lq_ssm_config* cfg, int64_t n_seqs, int64_t n_tokens, int64_t max_len);
+
+/*
+ * Selective state space scan over packed prompts. For channel c of group g = c / (channels
+ * / groups) and its states n, with d = softplus(dt[t][c] + dt_bias[c]) (or without it):
+ *   h[n] <- exp(d A[c][n]) h[n] + d x[t][c] B[t][g][n],
+ *   y[t][c] = (sum_n C[t][g][n] h[n] + D[c] x[t][c]) * z / (1 + e^-z),   z = z[t][c]
+ * (the last factor only where z is given).
+ *   x, dt, z, y  [n_tokens][channels] of cfg->dtype (tokens may lie apart); z may be NULL
+ *   B, C         [n_tokens][groups][n_state] of cfg->dtype; a token's are dense
+ *   A            fp32 [channels][n_state]; D, dt_bias fp32 [channels] or NULL (zero)
+ *   S0, S_out    fp32 [n_seqs][channels][n_state] or NULL (a zero first state, no last
+ *                one); S_out may be S0 itself
+ *   workspace    256-byte aligned, lq_ssm_workspace_bytes(...) bytes for these sizes or
+ *                larger ones (NULL if that is 0); its contents need not be kept
+ * States and sums are kept in fp32; y is rounded once. Any value is taken as the recurrence
+ * takes it; a token's value reaches its own and later tokens of its sequence only. Long
+ * sequences are split into segments; channels with a positive A, a negative or infinite d,
+ * or values past 1e30 pass from segment to segment token by token, which is slow.
+ */
+int lq_ssm_prefill(const lq_ssm_config* cfg, int64_t n_seqs, int64_t n_tokens, int64_t max_len,
+                   const int32_t* cu_seqlens, const void* x, const void* dt, const float* A, const void* B,
+                   const void* C, const float* D, const void* z, const float* dt_bias, const float* S0, float* S_out,
+                   void* y, void* workspace, size_t workspace_bytes, lq_stream_t stream);
+
+/*
+ * The recurrent form: one token for each of n_seqs sequences on fp32 states
+ * S [n_seqs][channels][n_state], in place. Token arrays as above with one token per
+ * sequence (strides between sequences).
+ */
+int lq_ssm_decode_step(const lq_ssm_config* cfg, float* S, int64_t n_seqs, const void* x, const void* dt,
+                       const float* A, const void* B, const void* C, const float* D, const void* z,
+                       const float* dt_bias, void* y, lq_stream_t stream);
+
+/*
+ * What each row of logits says, with lse = log sum_t exp(logits[r][t]):
+ *   logprob[r]   = logits[r][tokens[r]] - lse: 0 where tokens[r] is negative (no token
+ *                  asked for), NaN where it is not below vocab
+ *   entropy[r]   = -sum_t p_t log p_t, p_t = exp(logits[r][t] - lse), in nats
+ *   top_token[r][i], top_logprob[r][i]: the n_top largest logits, largest first, equal
+ *                  ones in the order of their index, and their log probabilities
+ *   logits       [rows][vocab] of dtype; row_stride elements from one row to the next
+ *                (>= vocab; any alignment)
+ *   tokens       int32 [rows], or NULL with logprob NULL; entropy fp32 [rows] or NULL;
+ *                top_logprob fp32 and top_token int32 [rows][n_top], NULL if n_top is 0
+ *   vocab 1..2^31-1, n_top 0..32 and at most vocab
+ * Masked tokens (-inf) have probability 0 and log probability -inf, and are among the
+ * n_top only when the others run out. A row without a distribution (all -inf, a NaN or a
+ * +inf among it) gets NaN for every number and -1 for its top tokens (0 still where no
+ * token is asked for). Sums are kept in fp32. Rows whose largest logits are very many equal
+ * ones, or come in rising order, take longer.
+ */
+int lq_token_logprobs(int32_t dtype, int64_t rows, int64_t vocab, int32_t n_top, const void* logits,
+                      int64_t row_stride, const int32_t* tokens, float* logprob, float* entropy, float* top_logprob,
+                      int32_t* top_token, lq_stream_t stream);
+
 /*
  * Synchronize `stream`, then read the state buffer's status word: LQ_OK or the
  * first device-side error recorded since lq_state_init / lq_clear_status.

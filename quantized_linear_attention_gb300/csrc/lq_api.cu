@@ -407,6 +407,142 @@ int check_reorder(int64_t n_states, int64_t outer, int64_t groups, int32_t beams
   return LQ_OK;
 }
 
+// Sizes of packed prompts.
+int check_packed(int64_t n_seqs, int64_t n_tokens, int64_t max_len, const int32_t* cu) {
+  if (n_seqs < 0 || n_seqs > 0x7fffffff || n_tokens < 0 || n_tokens > 0x7fffffff || max_len < 0)
+    return fail(LQ_ERR_INVALID_ARG, "n_seqs and n_tokens must be 0..%d, max_len must not be negative", 0x7fffffff);
+  if (n_seqs == 0) return LQ_OK;
+  if (!cu && n_seqs != 1) return fail(LQ_ERR_INVALID_ARG, "cu_seqlens is NULL with n_seqs > 1");
+  if (!cu && max_len > 0 && max_len < n_tokens)
+    return fail(LQ_ERR_INVALID_ARG, "max_len is less than n_tokens, the length of the only sequence");
+  return LQ_OK;
+}
+
+int check_dtype(int32_t dtype) {
+  if (dtype != LQ_F32 && dtype != LQ_BF16 && dtype != LQ_F16)
+    return fail(LQ_ERR_INVALID_ARG, "dtype must be LQ_F32, LQ_BF16 or LQ_F16 (got %d)", dtype);
+  return LQ_OK;
+}
+
+int check_stride(int64_t stride, int64_t row, const char* name) {
+  if (stride < row || stride > ((int64_t)1 << 38))
+    return fail(LQ_ERR_INVALID_ARG, "%s must be at least %lld (got %lld)", name, (long long)row, (long long)stride);
+  return LQ_OK;
+}
+
+constexpr int32_t kMaxChannels = 1 << 20;
+
+int check_conv(const lq_conv_config* c) {
+  if (!c) return fail(LQ_ERR_INVALID_ARG, "cfg is NULL");
+  if (c->channels < 1 || c->channels > kMaxChannels)
+    return fail(LQ_ERR_INVALID_ARG, "channels must be 1..%d (got %d)", kMaxChannels, c->channels);
+  if (c->width < 2 || c->width > lqi::kMaxWidth)
+    return fail(LQ_ERR_UNSUPPORTED, "width must be 2..%d (got %d)", lqi::kMaxWidth, c->width);
+  if (c->silu != 0 && c->silu != 1) return fail(LQ_ERR_INVALID_ARG, "silu must be 0 or 1 (got %d)", c->silu);
+  int rc = check_dtype(c->dtype);
+  if (rc || (rc = check_stride(c->x_stride, c->channels, "x_stride")) ||
+      (rc = check_stride(c->y_stride, c->channels, "y_stride")))
+    return rc;
+  return LQ_OK;
+}
+
+int check_ssm(const lq_ssm_config* c) {
+  if (!c) return fail(LQ_ERR_INVALID_ARG, "cfg is NULL");
+  if (c->channels < 1 || c->channels > kMaxChannels)
+    return fail(LQ_ERR_INVALID_ARG, "channels must be 1..%d (got %d)", kMaxChannels, c->channels);
+  if (c->n_state < 1 || c->n_state > lqi::kMaxNState)
+    return fail(LQ_ERR_UNSUPPORTED, "n_state must be 1..%d (got %d)", lqi::kMaxNState, c->n_state);
+  if (c->groups < 1 || c->channels % c->groups != 0)
+    return fail(LQ_ERR_INVALID_ARG, "groups must divide channels (got %d, %d)", c->groups, c->channels);
+  if (c->softplus != 0 && c->softplus != 1)
+    return fail(LQ_ERR_INVALID_ARG, "softplus must be 0 or 1 (got %d)", c->softplus);
+  if (c->reserved != 0) return fail(LQ_ERR_INVALID_ARG, "reserved must be 0");
+  int rc = check_dtype(c->dtype);
+  const int64_t bc = (int64_t)c->groups * c->n_state;
+  if (rc || (rc = check_stride(c->x_stride, c->channels, "x_stride")) ||
+      (rc = check_stride(c->dt_stride, c->channels, "dt_stride")) ||
+      (rc = check_stride(c->z_stride, c->channels, "z_stride")) ||
+      (rc = check_stride(c->y_stride, c->channels, "y_stride")) || (rc = check_stride(c->b_stride, bc, "b_stride")) ||
+      (rc = check_stride(c->c_stride, bc, "c_stride")))
+    return rc;
+  return LQ_OK;
+}
+
+// One argument of a call: what it is, where, how long, and whether the call writes it.
+struct Arg {
+  const void* p;
+  const char* name;
+  size_t bytes, align;
+  bool optional, written;
+};
+
+// On the host: NULL, alignment, and written arguments that overlap another. Arguments `in` and
+// `out` may be one and the same (a state in place).
+int check_args(const Arg* a, int n, int in = -1, int out = -1) {
+  int rc;
+  for (int i = 0; i < n; ++i)
+    if ((a[i].p || !a[i].optional) && a[i].bytes && (rc = check_addr(a[i].p, a[i].name, a[i].align))) return rc;
+  for (int i = 0; i < n; ++i) {
+    if (!a[i].p || !a[i].written) continue;
+    for (int j = 0; j < n; ++j) {
+      if (j == i || !a[j].p || (a[j].written && j < i)) continue;
+      if (((i == in && j == out) || (i == out && j == in)) && a[i].p == a[j].p) continue;
+      if (a[i].bytes && a[j].bytes && overlaps(a[i].p, a[i].bytes, a[j].p, a[j].bytes))
+        return fail(LQ_ERR_INVALID_ARG, "%s overlaps %s", a[i].name, a[j].name);
+    }
+  }
+  return LQ_OK;
+}
+
+int check_args_device(const Arg* a, int n, int dev) {
+  int rc;
+  for (int i = 0; i < n; ++i)
+    if (a[i].p && a[i].bytes && (rc = check_ptr(a[i].p, a[i].name, a[i].align, dev))) return rc;
+  return LQ_OK;
+}
+
+// CTAs of a launch: one for each block of channels of each slot.
+int check_grid(int64_t slots, int64_t blocks) {
+  if (slots > kMaxStates / blocks)
+    return fail(LQ_ERR_INVALID_ARG, "too many sequences or tokens for one call (%lld x %lld)", (long long)slots,
+                (long long)blocks);
+  return LQ_OK;
+}
+
+lqi::SsmParams ssm_params(const lq_ssm_config* c, const void* x, const void* dt, const float* A, const void* B,
+                          const void* C, const float* D, const void* z, const float* dt_bias, void* y) {
+  lqi::SsmParams p;
+  std::memset(&p, 0, sizeof p);
+  p.channels = c->channels;
+  p.n_state = c->n_state;
+  p.groups = c->groups;
+  p.per_group = c->channels / c->groups;
+  p.dtype = c->dtype;
+  p.softplus = c->softplus;
+  p.sx = c->x_stride;
+  p.sdt = c->dt_stride;
+  p.sz = c->z_stride;
+  p.sb = c->b_stride;
+  p.sc = c->c_stride;
+  p.sy = c->y_stride;
+  p.x = x;
+  p.dt = dt;
+  p.A = A;
+  p.B = B;
+  p.C = C;
+  p.D = D;
+  p.z = z;
+  p.dt_bias = dt_bias;
+  p.y = y;
+  return p;
+}
+
+// Split sequences: what a segment adds to the states, and the sum of its steps.
+size_t ssm_workspace(const lq_ssm_config* c, int64_t slots) {
+  return align256((size_t)slots * c->channels * c->n_state * sizeof(float)) +
+         align256((size_t)slots * c->channels * sizeof(float));
+}
+
 int launched(cudaError_t e, const char* what) { return e == cudaSuccess ? ok() : cuda_fail(e, what); }
 
 }  // namespace
@@ -870,6 +1006,231 @@ int lq_fp32_state_reorder(float* S, int64_t n_states, int64_t outer, int64_t gro
   if ((rc = check_ptr(S, "S", 16, dev)) || (rc = check_ptr(parent, "parent", 4, dev))) return rc;
   const lqi::ReorderParams r = {outer, groups, inner, beams, parent};
   return launched(lqi::launch_fp32_reorder(S, r, (cudaStream_t)stream), "lq_fp32_state_reorder launch");
+}
+
+void lq_conv_config_default(lq_conv_config* cfg, int32_t channels, int32_t width, int32_t dtype, int32_t silu) {
+  if (!cfg) return;
+  std::memset(cfg, 0, sizeof *cfg);
+  cfg->channels = channels;
+  cfg->width = width;
+  cfg->dtype = dtype;
+  cfg->silu = silu;
+  cfg->x_stride = cfg->y_stride = channels;
+}
+
+int lq_conv_prefill(const lq_conv_config* cfg, int64_t n_seqs, int64_t n_tokens, int64_t max_len,
+                    const int32_t* cu_seqlens, const void* x, const float* weight, const float* bias, const void* S0,
+                    void* S_out, void* y, lq_stream_t stream) {
+  int rc = check_conv(cfg);
+  if (rc || (rc = check_packed(n_seqs, n_tokens, max_len, cu_seqlens))) return rc;
+  if (n_seqs == 0) return ok();
+  const size_t e = la_size(cfg->dtype), C = (size_t)cfg->channels;
+  const size_t sb = (size_t)n_seqs * (cfg->width - 1) * C * e;
+  const Arg a[7] = {{x, "x", la_extent(n_tokens, cfg->x_stride, cfg->channels, e), e, false, false},
+                    {y, "y", la_extent(n_tokens, cfg->y_stride, cfg->channels, e), e, false, true},
+                    {weight, "weight", C * cfg->width * 4, 4, false, false},
+                    {bias, "bias", C * 4, 4, true, false},
+                    {S0, "S0", sb, e, true, false},
+                    {S_out, "S_out", sb, e, true, true},
+                    {cu_seqlens, "cu_seqlens", cu_seqlens ? (size_t)(n_seqs + 1) * 4 : 0, 4, true, false}};
+  if ((rc = check_args(a, 7, 4, 5))) return rc;
+  lqi::ConvParams p;
+  std::memset(&p, 0, sizeof p);
+  p.channels = cfg->channels;
+  p.width = cfg->width;
+  p.dtype = cfg->dtype;
+  p.silu = cfg->silu;
+  p.sx = cfg->x_stride;
+  p.sy = cfg->y_stride;
+  p.n_seqs = n_seqs;
+  p.n_tokens = n_tokens;
+  p.max_len = max_len;
+  p.cu = cu_seqlens;
+  p.x = x;
+  p.weight = weight;
+  p.bias = bias;
+  p.S0 = S0;
+  p.S = S_out;
+  p.y = y;
+  lqi::conv_plan(p);
+  if ((rc = check_grid(p.slots, (cfg->channels + 127) / 128))) return rc;
+  int dev = 0;
+  if ((rc = current_device(&dev)) || (rc = check_stream(stream, dev)) || (rc = check_args_device(a, 7, dev))) return rc;
+  return launched(lqi::launch_conv_prefill(p, (cudaStream_t)stream), "lq_conv_prefill launch");
+}
+
+int lq_conv_decode_step(const lq_conv_config* cfg, void* S, int64_t n_seqs, const void* x, const float* weight,
+                        const float* bias, void* y, lq_stream_t stream) {
+  int rc = check_conv(cfg);
+  if (rc) return rc;
+  if (n_seqs < 0) return fail(LQ_ERR_INVALID_ARG, "n_seqs must not be negative");
+  if ((rc = check_grid(n_seqs, (cfg->channels + 127) / 128))) return rc;
+  if (n_seqs == 0) return ok();
+  const size_t e = la_size(cfg->dtype), C = (size_t)cfg->channels;
+  const Arg a[5] = {{x, "x", la_extent(n_seqs, cfg->x_stride, cfg->channels, e), e, false, false},
+                    {y, "y", la_extent(n_seqs, cfg->y_stride, cfg->channels, e), e, false, true},
+                    {weight, "weight", C * cfg->width * 4, 4, false, false},
+                    {bias, "bias", C * 4, 4, true, false},
+                    {S, "S", (size_t)n_seqs * (cfg->width - 1) * C * e, e, false, true}};
+  if ((rc = check_args(a, 5))) return rc;
+  int dev = 0;
+  if ((rc = current_device(&dev)) || (rc = check_stream(stream, dev)) || (rc = check_args_device(a, 5, dev))) return rc;
+  lqi::ConvParams p;
+  std::memset(&p, 0, sizeof p);
+  p.channels = cfg->channels;
+  p.width = cfg->width;
+  p.dtype = cfg->dtype;
+  p.silu = cfg->silu;
+  p.sx = cfg->x_stride;
+  p.sy = cfg->y_stride;
+  p.n_seqs = p.n_tokens = n_seqs;
+  p.x = x;
+  p.weight = weight;
+  p.bias = bias;
+  p.S = S;
+  p.y = y;
+  return launched(lqi::launch_conv_step(p, (cudaStream_t)stream), "lq_conv_decode_step launch");
+}
+
+void lq_ssm_config_default(lq_ssm_config* cfg, int32_t channels, int32_t n_state, int32_t groups, int32_t dtype,
+                           int32_t softplus) {
+  if (!cfg) return;
+  std::memset(cfg, 0, sizeof *cfg);
+  cfg->channels = channels;
+  cfg->n_state = n_state;
+  cfg->groups = groups;
+  cfg->dtype = dtype;
+  cfg->softplus = softplus;
+  cfg->x_stride = cfg->dt_stride = cfg->z_stride = cfg->y_stride = channels;
+  cfg->b_stride = cfg->c_stride = (int64_t)groups * n_state;
+}
+
+size_t lq_ssm_workspace_bytes(const lq_ssm_config* cfg, int64_t n_seqs, int64_t n_tokens, int64_t max_len) {
+  const int32_t some = 0;
+  if (check_ssm(cfg) || check_packed(n_seqs, n_tokens, max_len, &some) || n_seqs == 0) return 0;
+  const int64_t slots = lqi::ssm_most_slots(cfg, n_seqs, n_tokens, max_len);
+  return slots ? ssm_workspace(cfg, slots) : 0;
+}
+
+int lq_ssm_prefill(const lq_ssm_config* cfg, int64_t n_seqs, int64_t n_tokens, int64_t max_len,
+                   const int32_t* cu_seqlens, const void* x, const void* dt, const float* A, const void* B,
+                   const void* C, const float* D, const void* z, const float* dt_bias, const float* S0, float* S_out,
+                   void* y, void* workspace, size_t workspace_bytes, lq_stream_t stream) {
+  int rc = check_ssm(cfg);
+  if (rc || (rc = check_packed(n_seqs, n_tokens, max_len, cu_seqlens))) return rc;
+  if (n_seqs == 0) return ok();
+  lqi::SsmParams p = ssm_params(cfg, x, dt, A, B, C, D, z, dt_bias, y);
+  lqi::ssm_plan(cfg, n_seqs, n_tokens, max_len, &p.seg, &p.slots);
+  const size_t need = p.seg ? ssm_workspace(cfg, p.slots) : 0;
+  const size_t e = la_size(cfg->dtype), ch = (size_t)cfg->channels, N = (size_t)cfg->n_state;
+  const int64_t row = cfg->channels, bc = (int64_t)cfg->groups * cfg->n_state;
+  const size_t sb = (size_t)n_seqs * ch * N * 4;
+  const Arg a[13] = {{x, "x", la_extent(n_tokens, cfg->x_stride, row, e), e, false, false},
+                     {dt, "dt", la_extent(n_tokens, cfg->dt_stride, row, e), e, false, false},
+                     {z, "z", la_extent(n_tokens, cfg->z_stride, row, e), e, true, false},
+                     {B, "B", la_extent(n_tokens, cfg->b_stride, bc, e), e, false, false},
+                     {C, "C", la_extent(n_tokens, cfg->c_stride, bc, e), e, false, false},
+                     {y, "y", la_extent(n_tokens, cfg->y_stride, row, e), e, false, true},
+                     {A, "A", ch * N * 4, 4, false, false},
+                     {D, "D", ch * 4, 4, true, false},
+                     {dt_bias, "dt_bias", ch * 4, 4, true, false},
+                     {S0, "S0", sb, 4, true, false},
+                     {S_out, "S_out", sb, 4, true, true},
+                     {cu_seqlens, "cu_seqlens", cu_seqlens ? (size_t)(n_seqs + 1) * 4 : 0, 4, true, false},
+                     {need ? workspace : nullptr, "workspace", need, 256, false, true}};
+  if ((rc = check_args(a, 13, 9, 10))) return rc;
+  if (need && workspace_bytes < need)
+    return fail(LQ_ERR_INVALID_ARG, "workspace has %zu bytes, %zu are needed", workspace_bytes, need);
+  if ((rc = check_grid(p.slots, lqi::ssm_blocks(cfg))) ||
+      (rc = check_grid(n_seqs, (int64_t)(ch * N + 255) / 256)))
+    return rc;
+  int dev = 0;
+  if ((rc = current_device(&dev)) || (rc = check_stream(stream, dev)) || (rc = check_args_device(a, 13, dev)))
+    return rc;
+  p.n_seqs = n_seqs;
+  p.n_tokens = n_tokens;
+  p.max_len = max_len;
+  p.cu = cu_seqlens;
+  p.S0 = S0;
+  p.S = S_out;
+  p.ws_state = static_cast<float*>(workspace);
+  p.ws_step = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256((size_t)p.slots * ch * N * 4));
+  return launched(lqi::launch_ssm_prefill(p, (cudaStream_t)stream), "lq_ssm_prefill launch");
+}
+
+int lq_ssm_decode_step(const lq_ssm_config* cfg, float* S, int64_t n_seqs, const void* x, const void* dt,
+                       const float* A, const void* B, const void* C, const float* D, const void* z,
+                       const float* dt_bias, void* y, lq_stream_t stream) {
+  int rc = check_ssm(cfg);
+  if (rc) return rc;
+  if (n_seqs < 0) return fail(LQ_ERR_INVALID_ARG, "n_seqs must not be negative");
+  if ((rc = check_grid(n_seqs, (int64_t)cfg->channels))) return rc;
+  if (n_seqs == 0) return ok();
+  const size_t e = la_size(cfg->dtype), ch = (size_t)cfg->channels, N = (size_t)cfg->n_state;
+  const int64_t row = cfg->channels, bc = (int64_t)cfg->groups * cfg->n_state;
+  const Arg a[10] = {{x, "x", la_extent(n_seqs, cfg->x_stride, row, e), e, false, false},
+                     {dt, "dt", la_extent(n_seqs, cfg->dt_stride, row, e), e, false, false},
+                     {z, "z", la_extent(n_seqs, cfg->z_stride, row, e), e, true, false},
+                     {B, "B", la_extent(n_seqs, cfg->b_stride, bc, e), e, false, false},
+                     {C, "C", la_extent(n_seqs, cfg->c_stride, bc, e), e, false, false},
+                     {y, "y", la_extent(n_seqs, cfg->y_stride, row, e), e, false, true},
+                     {A, "A", ch * N * 4, 4, false, false},
+                     {D, "D", ch * 4, 4, true, false},
+                     {dt_bias, "dt_bias", ch * 4, 4, true, false},
+                     {S, "S", (size_t)n_seqs * ch * N * 4, 4, false, true}};
+  if ((rc = check_args(a, 10))) return rc;
+  int dev = 0;
+  if ((rc = current_device(&dev)) || (rc = check_stream(stream, dev)) || (rc = check_args_device(a, 10, dev)))
+    return rc;
+  lqi::SsmParams p = ssm_params(cfg, x, dt, A, B, C, D, z, dt_bias, y);
+  p.n_seqs = p.n_tokens = n_seqs;
+  p.S = S;
+  return launched(lqi::launch_ssm_step(p, (cudaStream_t)stream), "lq_ssm_decode_step launch");
+}
+
+int lq_token_logprobs(int32_t dtype, int64_t rows, int64_t vocab, int32_t n_top, const void* logits,
+                      int64_t row_stride, const int32_t* tokens, float* logprob, float* entropy, float* top_logprob,
+                      int32_t* top_token, lq_stream_t stream) {
+  int rc = check_dtype(dtype);
+  if (rc) return rc;
+  if (rows < 0 || rows > kMaxStates / 8)
+    return fail(LQ_ERR_INVALID_ARG, "rows must be 0..%lld (got %lld)", (long long)(kMaxStates / 8), (long long)rows);
+  if (vocab < 1 || vocab > 0x7fffffff)
+    return fail(LQ_ERR_INVALID_ARG, "vocab must be 1..%d (got %lld)", 0x7fffffff, (long long)vocab);
+  if (n_top < 0 || n_top > lqi::kMaxTop || n_top > vocab)
+    return fail(LQ_ERR_INVALID_ARG, "n_top must be 0..%d and at most vocab (got %d)", lqi::kMaxTop, n_top);
+  if (row_stride < vocab || row_stride > ((int64_t)1 << 40))
+    return fail(LQ_ERR_INVALID_ARG, "row_stride must be at least vocab (got %lld)", (long long)row_stride);
+  if ((tokens == nullptr) != (logprob == nullptr))
+    return fail(LQ_ERR_INVALID_ARG, "tokens and logprob go together: one of them is NULL");
+  if (n_top == 0 && (top_logprob || top_token))
+    return fail(LQ_ERR_INVALID_ARG, "top_logprob and top_token must be NULL where n_top is 0");
+  if (rows == 0) return ok();
+  if (!logprob && !entropy && !n_top) return fail(LQ_ERR_INVALID_ARG, "no output is asked for");
+  const size_t e = la_size(dtype), r4 = (size_t)rows * 4;
+  const Arg a[6] = {{logits, "logits", la_extent(rows, row_stride, vocab, e), e, false, false},
+                    {tokens, "tokens", r4, 4, true, false},
+                    {logprob, "logprob", r4, 4, true, true},
+                    {entropy, "entropy", r4, 4, true, true},
+                    {top_logprob, "top_logprob", r4 * n_top, 4, false, true},
+                    {top_token, "top_token", r4 * n_top, 4, false, true}};
+  if ((rc = check_args(a, 6))) return rc;
+  int dev = 0;
+  if ((rc = current_device(&dev)) || (rc = check_stream(stream, dev)) || (rc = check_args_device(a, 6, dev))) return rc;
+  lqi::LogprobParams p;
+  std::memset(&p, 0, sizeof p);
+  p.dtype = dtype;
+  p.n_top = n_top;
+  p.rows = rows;
+  p.vocab = vocab;
+  p.row_stride = row_stride;
+  p.logits = logits;
+  p.tokens = tokens;
+  p.logprob = logprob;
+  p.entropy = entropy;
+  p.top_logprob = top_logprob;
+  p.top_token = top_token;
+  return launched(lqi::launch_token_logprobs(p, (cudaStream_t)stream), "lq_token_logprobs launch");
 }
 
 int lq_get_status(const void* state, int64_t* bad_state, lq_stream_t stream) {

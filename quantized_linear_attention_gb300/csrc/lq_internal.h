@@ -135,6 +135,62 @@ struct LaParams {
   uint32_t dbg_tx;   // test hook: bytes announced beyond those copied (0 normally)
 };
 
+// Short causal convolution (lq_conv_prefill, lq_conv_decode_step).
+struct ConvParams {
+  int channels, width, dtype, silu;
+  int64_t sx, sy;  // elements between tokens
+  int64_t n_seqs, n_tokens, max_len;
+  int64_t seg;     // tokens per tile
+  int64_t slots;   // upper bound of the tiles of all sequences
+  const int32_t* cu;  // NULL: one sequence of n_tokens
+  const void* x;
+  const float* weight;  // [channels][width]
+  const float* bias;    // may be NULL
+  const void* S0;       // may be NULL (zero)
+  void* S;              // prefill: last inputs (may be NULL); decode step: in place
+  void* y;
+};
+
+// Selective state space scan (lq_ssm_prefill, lq_ssm_decode_step).
+struct SsmParams {
+  int channels, n_state, groups, per_group;  // per_group: channels of a group
+  int dtype, softplus;
+  int64_t sx, sdt, sz, sb, sc, sy;  // elements between tokens
+  int64_t n_seqs, n_tokens, max_len;
+  int64_t seg;    // tokens per segment of a split sequence; 0: sequences are not split
+  int64_t slots;  // upper bound of the segments of all sequences
+  const int32_t* cu;  // NULL: one sequence of n_tokens
+  const void* x;
+  const void* dt;
+  const void* z;  // may be NULL
+  const void* B;
+  const void* C;
+  const float* A;        // [channels][n_state]
+  const float* D;        // may be NULL
+  const float* dt_bias;  // may be NULL
+  const float* S0;       // may be NULL (zero)
+  float* S;              // prefill: last states (may be NULL); decode step: in place
+  void* y;
+  float* ws_state;  // [slots][channels][n_state]
+  float* ws_step;   // [slots][channels]
+};
+
+constexpr int kMaxWidth = 4;    // taps of a convolution
+constexpr int kMaxNState = 64;  // states of a channel
+constexpr int kMaxTop = 32;     // alternatives of a row
+
+// Log probabilities of given tokens (lq_token_logprobs).
+struct LogprobParams {
+  int dtype, n_top;
+  int64_t rows, vocab, row_stride;
+  const void* logits;
+  const int32_t* tokens;  // may be NULL
+  float* logprob;         // NULL with tokens
+  float* entropy;         // may be NULL
+  float* top_logprob;     // [rows][n_top]
+  int32_t* top_token;
+};
+
 struct BeamParams {
   int dtype, beams, n_best, splits;
   int64_t batch, vocab, row_stride;
@@ -159,6 +215,18 @@ int64_t la_most_slots(const lq_la_config* c, int64_t n_seqs, int64_t n_tokens, i
 size_t beam_workspace(int64_t batch, int beams, int64_t vocab, int n_best);
 int beam_splits(int dtype, int64_t vocab);
 
+// Tokens per segment (0: whole sequences) and the segments there can be, by size; and the most of any smaller call.
+void ssm_plan(const lq_ssm_config* c, int64_t n_seqs, int64_t n_tokens, int64_t max_len, int64_t* seg, int64_t* slots);
+int64_t ssm_most_slots(const lq_ssm_config* c, int64_t n_seqs, int64_t n_tokens, int64_t max_len);
+
+int64_t ssm_blocks(const lq_ssm_config* c);  // CTAs of a slot
+void conv_plan(ConvParams& p);               // seg and slots, by size
+
+cudaError_t launch_conv_prefill(const ConvParams& p, cudaStream_t st);
+cudaError_t launch_conv_step(const ConvParams& p, cudaStream_t st);
+cudaError_t launch_ssm_prefill(const SsmParams& p, cudaStream_t st);
+cudaError_t launch_ssm_step(const SsmParams& p, cudaStream_t st);
+cudaError_t launch_token_logprobs(const LogprobParams& p, cudaStream_t st);
 cudaError_t launch_la_prefill(const LaParams& p, cudaStream_t st);
 cudaError_t launch_la_step(const LaParams& p, cudaStream_t st);
 cudaError_t launch_beam_select(const BeamParams& p, cudaStream_t st);

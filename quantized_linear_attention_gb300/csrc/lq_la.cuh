@@ -46,7 +46,8 @@ __device__ __forceinline__ void ld4(const T* p, float d[4]) {
 
 // The bounds of sequence b; one whose bounds are not 0 <= begin <= end <= n_tokens,
 // or that is longer than a stated max_len, counts as empty.
-__device__ __forceinline__ void bounds(const LaParams& p, int64_t b, int64_t& begin, int64_t& len) {
+template <typename P>
+__device__ __forceinline__ void bounds(const P& p, int64_t b, int64_t& begin, int64_t& len) {
   begin = 0;
   int64_t end = p.n_tokens;
   if (p.cu) {

@@ -1,0 +1,119 @@
+// Packed sequences cut into slots, and the elementwise functions of the state space layers (sm_103a).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "lq_internal.h"
+#include "lq_la.cuh"
+
+namespace lqi {
+
+constexpr float kLog2E = 1.44269504088896340736f;
+
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// x / (1 + e^-x), to about 2^-21 of itself; 0 where e^-x passes fp32's largest number.
+__device__ __forceinline__ float silu(float x) {
+  return __fmul_rn(x, rcp_approx(__fadd_rn(1.0f, ex2_approx(__fmul_rn(x, -kLog2E)))));
+}
+
+// log(1 + e^v) = max(v, 0) + log(1 + e) with e = e^-|v| <= 1, and log(1 + e) = 2 artanh(s) = 2 (s + s^3/3 + s^5/5 + ...)
+// with s = e / (2 + e) <= 1/3: seven terms leave 2e-8 of it. So small steps keep their relative accuracy (log of the
+// rounded 1 + e would not); about 2^-21 of the result.
+__device__ __forceinline__ float softplus(float v) {
+  const float e = ex2_approx(__fmul_rn(fabsf(v), -kLog2E));
+  const float s = __fmul_rn(e, rcp_approx(__fadd_rn(2.0f, e))), q = __fmul_rn(s, s);
+  float r = 2.0f / 13.0f;
+  r = __fmaf_rn(r, q, 2.0f / 11.0f);
+  r = __fmaf_rn(r, q, 2.0f / 9.0f);
+  r = __fmaf_rn(r, q, 2.0f / 7.0f);
+  r = __fmaf_rn(r, q, 2.0f / 5.0f);
+  r = __fmaf_rn(r, q, 2.0f / 3.0f);
+  r = __fmaf_rn(r, q, 2.0f);
+  return __fmaf_rn(r, s, v > 0.0f ? v : (v <= 0.0f ? 0.0f : v));
+}
+
+// Slot -> piece of a sequence, for a whole CTA of NT threads (all of them come here and get the same). Sequence b has
+// max(1, ceil(len / seg)) slots, one after the other (one each where seg is 0); NT sequences are counted at a time.
+template <int NT, typename P>
+__device__ __forceinline__ Piece find_slot(const P& p, int64_t slot) {
+  Piece r;
+  r.b = -1;
+  r.begin = r.len = r.i = 0;
+  r.n = 1;
+  if (p.seg == 0 || !p.cu) {
+    if (p.seg == 0 ? slot < p.n_seqs : true) {
+      int64_t begin, len;
+      r.b = p.seg == 0 ? slot : 0;
+      bounds(p, r.b, begin, len);
+      r.begin = begin;
+      r.len = len;
+      if (p.seg) {
+        r.n = len > p.seg ? (len + p.seg - 1) / p.seg : 1;
+        r.i = slot;
+        if (slot >= r.n) r.b = -1;
+        r.begin = begin + slot * p.seg;
+        r.len = min(p.seg, len - slot * p.seg);
+      }
+    }
+    return r;
+  }
+  constexpr int NW = NT / 32;
+  __shared__ int wsum[NW];
+  __shared__ Piece found;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) found = r;
+  int64_t before = 0;
+  for (int64_t b0 = 0; b0 < p.n_seqs; b0 += NT) {
+    const int64_t b = b0 + tid;
+    int64_t begin = 0, len = 0;
+    int n = 0;
+    if (b < p.n_seqs) {
+      bounds(p, b, begin, len);
+      n = len > p.seg ? (int)((len + p.seg - 1) / p.seg) : 1;
+    }
+    int sum = n;  // (at most 2^31 / seg + NT in a round of sequences that do not overlap; those that do may wrap
+                  // and are not served)
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += x;
+    }
+    __syncthreads();
+    if (lane == 31) wsum[warp] = sum;
+    __syncthreads();
+    int64_t mine = before, total = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      if (w < warp) mine += wsum[w];
+      total += wsum[w];
+    }
+    const int64_t i = slot - (mine + sum - n);
+    if (n && i >= 0 && i < n) {
+      found.b = b;
+      found.i = i;
+      found.n = n;
+      found.begin = begin + i * p.seg;
+      found.len = min(p.seg, len - i * p.seg);
+    }
+    before += total;
+    if (before > slot) break;  // (the same for all threads)
+  }
+  __syncthreads();
+  return found;
+}
+
+}  // namespace lqi

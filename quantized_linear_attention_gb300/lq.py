@@ -34,7 +34,9 @@ STATUS_NAMES = {0: "LQ_OK", -1: "LQ_ERR_INVALID_ARG", -2: "LQ_ERR_UNSUPPORTED", 
 EXPORTS = ("lq_config_default", "lq_state_bytes", "lq_layout", "lq_state_init", "lq_state_init_range", "lq_append",
            "lq_fold", "lq_decode_step", "lq_decode_step_noalloc", "lq_decode_step2", "lq_decode_step_rwkv7", "lq_export_state",
            "lq_fp32_decode_step", "lq_la_config_default", "lq_la_workspace_bytes", "lq_la_prefill", "lq_la_decode_step",
-           "lq_beam_workspace_bytes", "lq_beam_select", "lq_state_reorder", "lq_fp32_state_reorder", "lq_get_status",
+           "lq_beam_workspace_bytes", "lq_beam_select", "lq_state_reorder", "lq_fp32_state_reorder",
+           "lq_conv_config_default", "lq_conv_prefill", "lq_conv_decode_step", "lq_ssm_config_default",
+           "lq_ssm_workspace_bytes", "lq_ssm_prefill", "lq_ssm_decode_step", "lq_token_logprobs", "lq_get_status",
            "lq_clear_status", "lq_last_error", "lq_version", "lq_debug_set_wait")
 
 
@@ -56,6 +58,16 @@ class Layout(ctypes.Structure):
 class LaConfig(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("d_k", "d_v", "heads", "key_heads", "dtype", "reserved")] + \
                [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride", "o_stride", "alpha_stride")]
+
+
+class ConvConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("channels", "width", "dtype", "silu")] + \
+               [(n, ctypes.c_int64) for n in ("x_stride", "y_stride")]
+
+
+class SsmConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("channels", "n_state", "groups", "dtype", "softplus", "reserved")] + \
+               [(n, ctypes.c_int64) for n in ("x_stride", "dt_stride", "z_stride", "y_stride", "b_stride", "c_stride")]
 
 
 class LQError(RuntimeError):
@@ -106,6 +118,15 @@ def load():
         "lq_beam_select": (ctypes.c_int, [i32, i64, i32, i64, i32, P, i64, P, P, P, P, P, ctypes.c_size_t, P]),
         "lq_state_reorder": (ctypes.c_int, [cfgp, P, i64, i64, i64, i32, i64, P, P]),
         "lq_fp32_state_reorder": (ctypes.c_int, [P, i64, i64, i64, i32, i64, P, P]),
+        "lq_conv_config_default": (None, [ctypes.POINTER(ConvConfig), i32, i32, i32, i32]),
+        "lq_conv_prefill": (ctypes.c_int, [ctypes.POINTER(ConvConfig), i64, i64, i64, P, P, P, P, P, P, P, P]),
+        "lq_conv_decode_step": (ctypes.c_int, [ctypes.POINTER(ConvConfig), P, i64, P, P, P, P, P]),
+        "lq_ssm_config_default": (None, [ctypes.POINTER(SsmConfig), i32, i32, i32, i32, i32]),
+        "lq_ssm_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(SsmConfig), i64, i64, i64]),
+        "lq_ssm_prefill": (ctypes.c_int, [ctypes.POINTER(SsmConfig), i64, i64, i64, P, P, P, P, P, P, P, P, P, P, P, P,
+                                          P, ctypes.c_size_t, P]),
+        "lq_ssm_decode_step": (ctypes.c_int, [ctypes.POINTER(SsmConfig), P, i64, P, P, P, P, P, P, P, P, P, P]),
+        "lq_token_logprobs": (ctypes.c_int, [i32, i64, i64, i32, P, i64, P, P, P, P, P, P]),
         "lq_get_status": (ctypes.c_int, [P, ctypes.POINTER(ctypes.c_int64), P]),
         "lq_clear_status": (ctypes.c_int, [P, P]),
         "lq_last_error": (ctypes.c_char_p, []),
@@ -415,6 +436,168 @@ def fp32_state_reorder(S, parent, outer=1, inner=1, stream=None):
     p, groups, beams = _parents(parent)
     _check(load().lq_fp32_state_reorder(_ptr(S, "S", _f32()), S.numel() // (128 * 128), outer, groups, beams, inner, p,
                                         _stream(stream)))
+
+
+# ---------------------------------------------------------------------------- state space layers
+def conv_config(channels, width=4, dtype=None, silu=True) -> ConvConfig:
+    """A short causal convolution: channels, taps, the tokens' type (bfloat16 unless given), silu or none."""
+    if dtype is None:
+        import torch
+
+        dtype = torch.bfloat16
+    c = ConvConfig()
+    load().lq_conv_config_default(ctypes.byref(c), int(channels), int(width), _dtype_id(dtype), int(bool(silu)))
+    return c
+
+
+def ssm_config(channels, n_state=16, groups=1, dtype=None, softplus=True) -> SsmConfig:
+    """A selective state space scan: channels and their states, groups of B and C, the tokens' type (bfloat16 unless
+    given), whether steps go through a softplus."""
+    if dtype is None:
+        import torch
+
+        dtype = torch.bfloat16
+    c = SsmConfig()
+    load().lq_ssm_config_default(ctypes.byref(c), int(channels), int(n_state), int(groups), _dtype_id(dtype),
+                                 int(bool(softplus)))
+    return c
+
+
+def ssm_workspace_bytes(cfg: SsmConfig, n_seqs: int, n_tokens: int, max_len: int = 0) -> int:
+    """Bytes that are enough for ``ssm_prefill`` with up to these sizes (0: no such call needs any)."""
+    return int(load().lq_ssm_workspace_bytes(ctypes.byref(cfg), n_seqs, n_tokens, max_len))
+
+
+def _token_rows(t, name, tid, *row):
+    """(address, token stride, tokens) of a token array [tokens][*row] whose tokens may lie apart."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if _dtype_id(t.dtype) != tid:
+        raise ValueError(f"{name} must have the configuration's dtype, got {t.dtype}")
+    if tuple(t.shape[1:]) != row or t.dim() != 1 + len(row):
+        raise ValueError(f"{name} must be [tokens]{list(row)}, got {tuple(t.shape)}")
+    n, dense, strides = t.shape[0], 1, t.stride()
+    if n:
+        for i in range(len(row), 0, -1):
+            if row[i - 1] > 1 and strides[i] != dense:
+                raise ValueError(f"{name}: a token's elements must be contiguous")
+            dense *= row[i - 1]
+    else:
+        for r in row:
+            dense *= r
+    return t.data_ptr(), (strides[0] if n > 1 else dense), n
+
+
+def _shaped(t, name, dtype, *shape):
+    """Address of a contiguous tensor of this shape, or NULL."""
+    if t is None:
+        return None
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {tuple(t.shape)}")
+    return _ptr(t, name, dtype)
+
+
+def _same_tokens(**counts):
+    if len(set(counts.values())) > 1:
+        raise ValueError("token arrays must have the same number of tokens, got " +
+                         ", ".join(f"{k} {v}" for k, v in counts.items()))
+    return next(iter(counts.values()))
+
+
+def _conv_tokens(cfg, x, weight, y, bias):
+    px, sx, n = _token_rows(x, "x", cfg.dtype, cfg.channels)
+    py, sy, ny = _token_rows(y, "y", cfg.dtype, cfg.channels)
+    _same_tokens(x=n, y=ny)
+    c = ConvConfig(cfg.channels, cfg.width, cfg.dtype, cfg.silu, sx, sy)
+    f = _f32()
+    return (c, px, _shaped(weight, "weight", f, cfg.channels, cfg.width), _shaped(bias, "bias", f, cfg.channels), py, n,
+            (cfg.width - 1, cfg.channels))
+
+
+def conv_prefill(cfg: ConvConfig, x, weight, y, bias=None, cu_seqlens=None, max_len=0, S0=None, S_out=None, stream=None):
+    """Causal convolution of every channel over packed prompts: x, y [tokens][channels] (strided tokens allowed),
+    weight fp32 [channels][width], bias fp32 [channels], cu_seqlens int32 [n_seqs + 1] on the device (None: one
+    sequence), S0, S_out [n_seqs][width - 1][channels] of the tokens' type: a sequence's inputs before its first token
+    and its last ones, oldest first."""
+    import torch
+
+    c, px, pw, pb, py, n, state = _conv_tokens(cfg, x, weight, y, bias)
+    n_seqs = 1 if cu_seqlens is None else cu_seqlens.numel() - 1
+    _check(load().lq_conv_prefill(ctypes.byref(c), n_seqs, n, int(max_len), _ptr(cu_seqlens, "cu_seqlens", torch.int32),
+                                  px, pw, pb, _shaped(S0, "S0", x.dtype, n_seqs, *state),
+                                  _shaped(S_out, "S_out", x.dtype, n_seqs, *state), py, _stream(stream)))
+
+
+def conv_decode_step(cfg: ConvConfig, S, x, weight, y, bias=None, stream=None):
+    """One token for each sequence: x, y [n_seqs][channels]; S [n_seqs][width - 1][channels] holds the last inputs,
+    oldest first, and takes x in place of the oldest."""
+    c, px, pw, pb, py, n, state = _conv_tokens(cfg, x, weight, y, bias)
+    _check(load().lq_conv_decode_step(ctypes.byref(c), _shaped(S, "S", x.dtype, n, *state), n, px, pw, pb, py,
+                                      _stream(stream)))
+
+
+def _ssm_tokens(cfg, x, dt, A, B, C, y, D, z, dt_bias):
+    """A copy of cfg with the token arrays' strides, the call's addresses and the number of tokens."""
+    ch, N, G, tid = cfg.channels, cfg.n_state, cfg.groups, cfg.dtype
+    px, sx, n = _token_rows(x, "x", tid, ch)
+    pd, sd, nd = _token_rows(dt, "dt", tid, ch)
+    pb, sb, nb = _token_rows(B, "B", tid, G, N)
+    pc, sc, nc = _token_rows(C, "C", tid, G, N)
+    py, sy, ny = _token_rows(y, "y", tid, ch)
+    pz, sz, nz = (None, ch, n) if z is None else _token_rows(z, "z", tid, ch)
+    _same_tokens(x=n, dt=nd, B=nb, C=nc, y=ny, z=nz)
+    f = _f32()
+    return (SsmConfig(ch, N, G, tid, cfg.softplus, cfg.reserved, sx, sd, sz, sy, sb, sc), n, px, pd,
+            _shaped(A, "A", f, ch, N), pb, pc, _shaped(D, "D", f, ch), pz, _shaped(dt_bias, "dt_bias", f, ch), py)
+
+
+def ssm_prefill(cfg: SsmConfig, x, dt, A, B, C, y, D=None, z=None, dt_bias=None, cu_seqlens=None, max_len=0, S0=None,
+                S_out=None, workspace=None, stream=None):
+    """Selective state space scan over packed prompts: x, dt, z, y [tokens][channels], B, C [tokens][groups][n_state]
+    (strided tokens allowed), A fp32 [channels][n_state], D, dt_bias fp32 [channels], cu_seqlens int32 [n_seqs + 1] on
+    the device (None: one sequence), S0, S_out fp32 [n_seqs][channels][n_state]. workspace: uint8 tensor of
+    ``ssm_workspace_bytes`` for these sizes or larger ones."""
+    import torch
+
+    c, n, px, pd, pA, pB, pC, pD, pz, pbias, py = _ssm_tokens(cfg, x, dt, A, B, C, y, D, z, dt_bias)
+    n_seqs, f = (1 if cu_seqlens is None else cu_seqlens.numel() - 1), torch.float32
+    shape = (n_seqs, c.channels, c.n_state)
+    _check(load().lq_ssm_prefill(ctypes.byref(c), n_seqs, n, int(max_len), _ptr(cu_seqlens, "cu_seqlens", torch.int32),
+                                 px, pd, pA, pB, pC, pD, pz, pbias, _shaped(S0, "S0", f, *shape),
+                                 _shaped(S_out, "S_out", f, *shape), py, _ptr(workspace, "workspace"),
+                                 0 if workspace is None else workspace.nbytes, _stream(stream)))
+
+
+def ssm_decode_step(cfg: SsmConfig, S, x, dt, A, B, C, y, D=None, z=None, dt_bias=None, stream=None):
+    """One token for each sequence on fp32 states S [n_seqs][channels][n_state], in place; token arrays as
+    ``ssm_prefill`` with one token per sequence."""
+    c, n, px, pd, pA, pB, pC, pD, pz, pbias, py = _ssm_tokens(cfg, x, dt, A, B, C, y, D, z, dt_bias)
+    _check(load().lq_ssm_decode_step(ctypes.byref(c), _shaped(S, "S", _f32(), n, c.channels, c.n_state), n, px, pd, pA,
+                                     pB, pC, pD, pz, pbias, py, _stream(stream)))
+
+
+def token_logprobs(logits, tokens=None, logprob=None, entropy=None, top_logprob=None, top_token=None, stream=None):
+    """What each row of logits [rows][vocab] (rows may be padded) says: logprob fp32 [rows] of the given tokens (int32
+    [rows]; 0 where one is negative), entropy fp32 [rows] in nats, and the n_top = top_token.shape[1] most likely tokens
+    (int32 [rows][n_top]) with their log probabilities (fp32), best first. What is None is left out."""
+    import torch
+
+    if logits.dim() != 2 or not logits.is_cuda:
+        raise ValueError(f"logits must be a CUDA tensor [rows][vocab], got {tuple(logits.shape)}")
+    rows, vocab = logits.shape
+    s0, s1 = logits.stride()
+    if logits.numel() and vocab > 1 and s1 != 1:
+        raise ValueError("logits: a row must be contiguous")
+    if (top_logprob is None) != (top_token is None):
+        raise ValueError("top_logprob and top_token go together: one of them is None")
+    n_top = 0 if top_token is None else top_token.shape[-1]
+    f, i = torch.float32, torch.int32
+    tops = [None, None] if n_top == 0 else [_shaped(top_logprob, "top_logprob", f, rows, n_top),
+                                            _shaped(top_token, "top_token", i, rows, n_top)]
+    _check(load().lq_token_logprobs(_dtype_id(logits.dtype), rows, vocab, n_top, logits.data_ptr(),
+                                    s0 if rows > 1 else max(vocab, 1), _shaped(tokens, "tokens", i, rows),
+                                    _shaped(logprob, "logprob", f, rows), _shaped(entropy, "entropy", f, rows), *tops,
+                                    _stream(stream)))
 
 
 def get_status(state, stream=None):
