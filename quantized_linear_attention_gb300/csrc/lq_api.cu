@@ -1142,7 +1142,7 @@ int lq_ssm_prefill(const lq_ssm_config* cfg, int64_t n_seqs, int64_t n_tokens, i
   if (need && workspace_bytes < need)
     return fail(LQ_ERR_INVALID_ARG, "workspace has %zu bytes, %zu are needed", workspace_bytes, need);
   if ((rc = check_grid(p.slots, lqi::ssm_blocks(cfg))) ||
-      (p.seg && (rc = check_grid(p.slots, (int64_t)(ch * N + 255) / 256))))
+      (p.seg && (rc = check_grid(n_seqs, (int64_t)(ch * N + 255) / 256))))
     return rc;
   int dev = 0;
   if ((rc = current_device(&dev)) || (rc = check_stream(stream, dev)) || (rc = check_args_device(a, 13, dev)))

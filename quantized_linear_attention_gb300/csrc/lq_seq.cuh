@@ -30,20 +30,30 @@ __device__ __forceinline__ float silu(float x) {
   return __fmul_rn(x, rcp_approx(__fadd_rn(1.0f, ex2_approx(__fmul_rn(x, -kLog2E)))));
 }
 
-// log(1 + e^v) = max(v, 0) + log(1 + e) with e = e^-|v| <= 1, and log(1 + e) = 2 artanh(s) = 2 (s + s^3/3 + s^5/5 + ...)
-// with s = e / (2 + e) <= 1/3: seven terms leave 2e-8 of it. So small steps keep their relative accuracy (log of the
-// rounded 1 + e would not); about 2^-21 of the result.
+// log(1 + e^v) = max(v, 0) + log(1 + e) with e = e^-|v| <= 1, and log(1 + e) = 2 artanh(s) with s = e / (2 + e) <= 1/3: an
+// odd function of s, here s times a polynomial of degree 4 in s^2, fitted by exchange to 2e-8 of it (the power series takes
+// two terms more). So small steps keep their relative accuracy, as the logarithm of a rounded 1 + e would not; about 2^-21.
 __device__ __forceinline__ float softplus(float v) {
   const float e = ex2_approx(__fmul_rn(fabsf(v), -kLog2E));
   const float s = __fmul_rn(e, rcp_approx(__fadd_rn(2.0f, e))), q = __fmul_rn(s, s);
-  float r = 2.0f / 13.0f;
-  r = __fmaf_rn(r, q, 2.0f / 11.0f);
-  r = __fmaf_rn(r, q, 2.0f / 9.0f);
-  r = __fmaf_rn(r, q, 2.0f / 7.0f);
-  r = __fmaf_rn(r, q, 2.0f / 5.0f);
-  r = __fmaf_rn(r, q, 2.0f / 3.0f);
+  float r = 0.296150803565979f;
+  r = __fmaf_rn(r, q, 0.27632495760917664f);
+  r = __fmaf_rn(r, q, 0.4004742205142975f);
+  r = __fmaf_rn(r, q, 0.6666590571403503f);
   r = __fmaf_rn(r, q, 2.0f);
-  return __fmaf_rn(r, s, v > 0.0f ? v : (v <= 0.0f ? 0.0f : v));
+  return __fmaf_rn(r, s, fmaxf(v, 0.0f));  // (a NaN comes through r)
+}
+
+// Copies of 16 bytes into shared memory that do not hold the thread up; the first `bytes` are read, the rest is zero.
+__device__ __forceinline__ void copy16(void* to, const void* from, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // Slot -> piece of a sequence, for a whole CTA of NT threads (all of them come here and get the same). Sequence b has
@@ -114,6 +124,26 @@ __device__ __forceinline__ Piece find_slot(const P& p, int64_t slot) {
   }
   __syncthreads();
   return found;
+}
+
+// The first slot of sequence b, counted by a whole CTA of NT threads (all get it).
+template <int NT, typename P>
+__device__ __forceinline__ int64_t first_slot(const P& p, int64_t b) {
+  __shared__ int64_t part[NT / 32];
+  int64_t n = 0;
+  for (int64_t x = threadIdx.x; x < b; x += NT) {
+    int64_t begin, len;
+    bounds(p, x, begin, len);
+    n += len > p.seg ? (len + p.seg - 1) / p.seg : 1;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = n;
+  __syncthreads();
+  n = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) n += part[w];
+  return n;
 }
 
 }  // namespace lqi
