@@ -18,7 +18,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 
 CUDA_SOURCES = ["lq_kernels.cu", "lq_append.cu", "lq_step.cu", "lq_fp32.cu", "lq_la.cu", "lq_la_chunk.cu",
-                "lq_beam.cu", "lq_reorder.cu", "lq_conv.cu", "lq_ssm.cu", "lq_logprob.cu", "lq_api.cu"]
+                "lq_beam.cu", "lq_reorder.cu", "lq_conv.cu", "lq_ssm.cu", "lq_ssm_f32.cu",
+                "lq_ssm_bf16.cu", "lq_ssm_f16.cu", "lq_logprob.cu", "lq_api.cu"]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
     "-O3", "-lineinfo", "-std=c++17",

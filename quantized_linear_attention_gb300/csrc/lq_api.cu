@@ -1120,7 +1120,12 @@ int lq_ssm_prefill(const lq_ssm_config* cfg, int64_t n_seqs, int64_t n_tokens, i
   if (rc || (rc = check_packed(n_seqs, n_tokens, max_len, cu_seqlens))) return rc;
   if (n_seqs == 0) return ok();
   lqi::SsmParams p = ssm_params(cfg, x, dt, A, B, C, D, z, dt_bias, y);
-  lqi::ssm_plan(cfg, n_seqs, n_tokens, max_len, &p.seg, &p.slots);
+  lqi::SsmPlan plan;
+  lqi::ssm_plan(cfg, n_seqs, n_tokens, max_len, &plan);
+  p.spt = plan.spt;
+  p.lpc = plan.lpc;
+  p.seg = plan.seg;
+  p.slots = plan.slots;
   const size_t need = p.seg ? ssm_workspace(cfg, p.slots) : 0;
   const size_t e = la_size(cfg->dtype), ch = (size_t)cfg->channels, N = (size_t)cfg->n_state;
   const int64_t row = cfg->channels, bc = (int64_t)cfg->groups * cfg->n_state;
@@ -1141,7 +1146,7 @@ int lq_ssm_prefill(const lq_ssm_config* cfg, int64_t n_seqs, int64_t n_tokens, i
   if ((rc = check_args(a, 13, 9, 10))) return rc;
   if (need && workspace_bytes < need)
     return fail(LQ_ERR_INVALID_ARG, "workspace has %zu bytes, %zu are needed", workspace_bytes, need);
-  if ((rc = check_grid(p.slots, lqi::ssm_blocks(cfg))) ||
+  if ((rc = check_grid(p.slots, plan.blocks)) ||
       (p.seg && (rc = check_grid(n_seqs, (int64_t)(ch * N + 255) / 256))))
     return rc;
   int dev = 0;

@@ -152,9 +152,17 @@ struct ConvParams {
 };
 
 // Selective state space scan (lq_ssm_prefill, lq_ssm_decode_step).
+struct SsmPlan {
+  int spt, lpc;    // states a thread, lanes a channel
+  int64_t seg;     // tokens per segment of a split sequence; 0: sequences are not split
+  int64_t slots;   // upper bound of the segments of all sequences
+  int64_t blocks;  // CTAs of a segment
+};
+
 struct SsmParams {
   int channels, n_state, groups, per_group;  // per_group: channels of a group
   int dtype, softplus;
+  int spt, lpc;  // states a thread, lanes a channel
   int64_t sx, sdt, sz, sb, sc, sy;  // elements between tokens
   int64_t n_seqs, n_tokens, max_len;
   int64_t seg;    // tokens per segment of a split sequence; 0: sequences are not split
@@ -215,12 +223,11 @@ int64_t la_most_slots(const lq_la_config* c, int64_t n_seqs, int64_t n_tokens, i
 size_t beam_workspace(int64_t batch, int beams, int64_t vocab, int n_best);
 int beam_splits(int dtype, int64_t vocab);
 
-// Tokens per segment (0: whole sequences) and the segments there can be, by size; and the most of any smaller call.
-void ssm_plan(const lq_ssm_config* c, int64_t n_seqs, int64_t n_tokens, int64_t max_len, int64_t* seg, int64_t* slots);
+// How a scan of these sizes runs; and the most segments of any call of these sizes or smaller ones (0: none is split).
+void ssm_plan(const lq_ssm_config* c, int64_t n_seqs, int64_t n_tokens, int64_t max_len, SsmPlan* plan);
 int64_t ssm_most_slots(const lq_ssm_config* c, int64_t n_seqs, int64_t n_tokens, int64_t max_len);
 
-int64_t ssm_blocks(const lq_ssm_config* c);  // CTAs of a slot
-void conv_plan(ConvParams& p);               // seg and slots, by size
+void conv_plan(ConvParams& p);  // seg and slots, by size
 
 cudaError_t launch_conv_prefill(const ConvParams& p, cudaStream_t st);
 cudaError_t launch_conv_step(const ConvParams& p, cudaStream_t st);

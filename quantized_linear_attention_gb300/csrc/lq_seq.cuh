@@ -7,6 +7,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "lq_device.cuh"
 #include "lq_internal.h"
 #include "lq_la.cuh"
 
@@ -29,26 +30,45 @@ __device__ __forceinline__ float rcp_approx(float x) {
 __device__ __forceinline__ float silu(float x) {
   return __fmul_rn(x, rcp_approx(__fadd_rn(1.0f, ex2_approx(__fmul_rn(x, -kLog2E)))));
 }
+__device__ __forceinline__ f32x2 silu2(f32x2 x) {
+  float a, b;
+  f2_unpack(f2_mul(x, f2_dup(-kLog2E)), a, b);
+  f2_unpack(f2_add(f2_pack(ex2_approx(a), ex2_approx(b)), f2_dup(1.0f)), a, b);
+  return f2_mul(x, f2_pack(rcp_approx(a), rcp_approx(b)));
+}
 
 // log(1 + e^v) = max(v, 0) + log(1 + e) with e = e^-|v| <= 1, and log(1 + e) = 2 artanh(s) with s = e / (2 + e) <= 1/3: an
 // odd function of s, here s times a polynomial of degree 4 in s^2, fitted by exchange to 2e-8 of it (the power series takes
 // two terms more). So small steps keep their relative accuracy, as the logarithm of a rounded 1 + e would not; about 2^-21.
+// The single and the paired form round alike.
+constexpr float kArtanh8 = 0.296150803565979f, kArtanh6 = 0.27632495760917664f, kArtanh4 = 0.4004742205142975f,
+                kArtanh2 = 0.6666590571403503f;
 __device__ __forceinline__ float softplus(float v) {
   const float e = ex2_approx(__fmul_rn(fabsf(v), -kLog2E));
   const float s = __fmul_rn(e, rcp_approx(__fadd_rn(2.0f, e))), q = __fmul_rn(s, s);
-  float r = 0.296150803565979f;
-  r = __fmaf_rn(r, q, 0.27632495760917664f);
-  r = __fmaf_rn(r, q, 0.4004742205142975f);
-  r = __fmaf_rn(r, q, 0.6666590571403503f);
-  r = __fmaf_rn(r, q, 2.0f);
-  return __fmaf_rn(r, s, fmaxf(v, 0.0f));  // (a NaN comes through r)
+  const float r = __fmaf_rn(__fmaf_rn(__fmaf_rn(kArtanh8, q, kArtanh6), q, kArtanh4), q, kArtanh2);
+  return __fmaf_rn(__fmaf_rn(r, q, 2.0f), s, fmaxf(v, 0.0f));  // (a NaN comes through s)
+}
+__device__ __forceinline__ f32x2 softplus2(f32x2 v) {
+  float a, b, c, d;
+  f2_unpack(v, a, b);
+  f2_unpack(f2_mul(f2_pack(fabsf(a), fabsf(b)), f2_dup(-kLog2E)), c, d);
+  const f32x2 e = f2_pack(ex2_approx(c), ex2_approx(d));
+  f2_unpack(f2_add(e, f2_dup(2.0f)), c, d);
+  const f32x2 s = f2_mul(e, f2_pack(rcp_approx(c), rcp_approx(d))), q = f2_mul(s, s);
+  const f32x2 r = f2_fma(f2_fma(f2_fma(f2_dup(kArtanh8), q, f2_dup(kArtanh6)), q, f2_dup(kArtanh4)), q, f2_dup(kArtanh2));
+  return f2_fma(f2_fma(r, q, f2_dup(2.0f)), s, f2_pack(fmaxf(a, 0.0f), fmaxf(b, 0.0f)));
 }
 
-// Copies of 16 bytes into shared memory that do not hold the thread up; the first `bytes` are read, the rest is zero.
-__device__ __forceinline__ void copy16(void* to, const void* from, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from),
-               "r"(bytes)
-               : "memory");
+// Copies of 4, 8 or 16 bytes into shared memory that do not hold the thread up; the first `bytes` are read, the rest is
+// zero.
+template <int SIZE>
+__device__ __forceinline__ void copy_ahead(void* to, const void* from, int bytes) {
+  const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
+  if (SIZE == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from), "r"(bytes) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(at), "l"(from), "n"(SIZE), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
