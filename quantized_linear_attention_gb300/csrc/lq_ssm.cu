@@ -7,54 +7,117 @@ namespace {
 
 // --------------------------------------------------------------------------------------------
 // Single tokens.
-template <typename T, int N>
-__device__ __forceinline__ void token(const SsmParams& p, int64_t t, int c, int g, const float (&A)[N], float bias,
-                                      float D, float (&h)[N]) {
-  const float d = p.softplus ? step_of<T, true>(static_cast<const T*>(p.dt)[t * p.sdt + c], bias)
-                             : step_of<T, false>(static_cast<const T*>(p.dt)[t * p.sdt + c], bias);
-  const float x = to_f(static_cast<const T*>(p.x)[t * p.sx + c]), dx = __fmul_rn(d, x);
-  const T* B = static_cast<const T*>(p.B) + t * p.sb + (int64_t)g * p.n_state;
-  const T* C = static_cast<const T*>(p.C) + t * p.sc + (int64_t)g * p.n_state;
-  float y = 0.0f;
+// Bound by memory: a state is read and written, 8 bytes for about six operations. A lane holds four neighbouring states of a
+// channel (V4: by 16 bytes), LPC lanes a channel; a CTA takes one block of channels and K sequences after K others, whose
+// loads are all begun before the first is used, so that A is read once for all of them.
+template <typename T, int LPC, bool V4, int K>
+__device__ __forceinline__ void tokens(const SsmParams& p, int64_t b, int c, int g, bool live, const float (&A)[4],
+                                       float bias, float D) {
+  const int part = (threadIdx.x & 31) / (32 / LPC), n0 = 4 * part;
+  const int64_t row = (int64_t)p.channels * p.n_state;
+  float* const S = p.S + b * row + (int64_t)c * p.n_state + n0;
+  const T* const Bp = static_cast<const T*>(p.B) + b * p.sb + (int64_t)g * p.n_state + n0;
+  const T* const Cp = static_cast<const T*>(p.C) + b * p.sc + (int64_t)g * p.n_state + n0;
+  const bool in = n0 < p.n_state;
+  float h[K][4], B[K][4], C[K][4];
+  T dt[K], x[K], z[K];
 #pragma unroll
-  for (int n = 0; n < N; ++n) {
-    if (n >= p.n_state) break;
-    h[n] = __fmaf_rn(ex2_approx(__fmul_rn(d, A[n])), h[n], __fmul_rn(dx, to_f(B[n])));
-    y = __fmaf_rn(to_f(C[n]), h[n], y);
-  }
-  y = __fmaf_rn(D, x, y);
-  if (p.z) y = __fmul_rn(y, silu(to_f(static_cast<const T*>(p.z)[t * p.sz + c])));
-  static_cast<T*>(p.y)[t * p.sy + c] = from_f<T>(y);
-}
-
-template <typename T, int N>
-__global__ void __launch_bounds__(kNT) k_ssm_step(SsmParams p, int blocks) {
-  const int64_t b = blockIdx.x / (unsigned)blocks;
-  const int c = (int)(blockIdx.x % (unsigned)blocks) * kNT + threadIdx.x;
-  if (c >= p.channels) return;
-  const int64_t at = (b * p.channels + c) * p.n_state;
-  float A[N], h[N];
+  for (int k = 0; k < K; ++k) {
+    dt[k] = static_cast<const T*>(p.dt)[(b + k) * p.sdt + c];
+    x[k] = static_cast<const T*>(p.x)[(b + k) * p.sx + c];
+    z[k] = p.z ? static_cast<const T*>(p.z)[(b + k) * p.sz + c] : x[k];
 #pragma unroll
-  for (int n = 0; n < N; ++n) {
-    A[n] = h[n] = 0.0f;
-    if (n < p.n_state) {
-      A[n] = __fmul_rn(p.A[(int64_t)c * p.n_state + n], kLog2E);
-      h[n] = p.S[at + n];
+    for (int e = 0; e < 4; ++e) h[k][e] = B[k][e] = C[k][e] = 0.0f;
+    if (V4) {
+      if (in) {
+        const float4 v = __ldcs(reinterpret_cast<const float4*>(S + k * row));
+        h[k][0] = v.x, h[k][1] = v.y, h[k][2] = v.z, h[k][3] = v.w;
+        ld4(Bp + k * p.sb, B[k]);
+        ld4(Cp + k * p.sc, C[k]);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (n0 + e < p.n_state) {
+          h[k][e] = S[k * row + e];
+          B[k][e] = to_f(Bp[k * p.sb + e]);
+          C[k][e] = to_f(Cp[k * p.sc + e]);
+        }
+      }
     }
   }
-  token<T, N>(p, b, c, c / p.per_group, A, p.dt_bias ? p.dt_bias[c] : 0.0f, p.D ? p.D[c] : 0.0f, h);
 #pragma unroll
-  for (int n = 0; n < N; ++n)
-    if (n < p.n_state) p.S[at + n] = h[n];
+  for (int k = 0; k < K; ++k) {
+    const float d = p.softplus ? step_of<T, true>(dt[k], bias) : step_of<T, false>(dt[k], bias);
+    const float xv = to_f(x[k]), dx = __fmul_rn(d, xv);
+    float y = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      h[k][e] = __fmaf_rn(ex2_approx(__fmul_rn(d, A[e])), h[k][e], __fmul_rn(dx, B[k][e]));
+      y = __fmaf_rn(C[k][e], h[k][e], y);
+    }
+    if (V4 && in && live) {
+      __stcs(reinterpret_cast<float4*>(S + k * row), make_float4(h[k][0], h[k][1], h[k][2], h[k][3]));
+    } else if (!V4 && live) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n0 + e < p.n_state) S[k * row + e] = h[k][e];
+    }
+#pragma unroll
+    for (int s = 32 / LPC; s < 32; s <<= 1) y = __fadd_rn(y, __shfl_xor_sync(0xffffffffu, y, s));
+    y = __fmaf_rn(D, xv, y);
+    if (p.z) y = __fmul_rn(y, silu(to_f(z[k])));
+    if (part == 0 && live) static_cast<T*>(p.y)[(b + k) * p.sy + c] = from_f<T>(y);
+  }
+}
+
+// Consecutive lanes hold consecutive channels, the parts of a channel lie 32 / LPC lanes apart.
+template <typename T, int LPC, bool V4>
+__global__ void __launch_bounds__(kNT) k_ssm_step(SsmParams p, int blocks, int seqs) {
+  constexpr int CW = 32 / LPC, K = 4;
+  const int lane = threadIdx.x & 31, part = lane / CW;
+  const int at = (int)(blockIdx.x % (unsigned)blocks) * (kNT / LPC) + (threadIdx.x >> 5) * CW + lane % CW;
+  const bool live = at < p.channels;
+  const int c = live ? at : 0;
+  float A[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int n = 4 * part + e;
+    A[e] = n < p.n_state ? __fmul_rn(p.A[(int64_t)c * p.n_state + n], kLog2E) : 0.0f;
+  }
+  const float bias = p.dt_bias ? p.dt_bias[c] : 0.0f, D = p.D ? p.D[c] : 0.0f;
+  const int g = c / p.per_group;
+  int64_t b = (int64_t)(blockIdx.x / (unsigned)blocks) * seqs;
+  const int64_t end = min(b + seqs, p.n_seqs);
+  for (; b + K <= end; b += K) tokens<T, LPC, V4, K>(p, b, c, g, live, A, bias, D);
+  for (; b < end; ++b) tokens<T, LPC, V4, 1>(p, b, c, g, live, A, bias, D);
+}
+
+template <typename T, int LPC, bool V4>
+cudaError_t launch_lanes(const SsmParams& p, cudaStream_t st) {
+  const int blocks = (int)(((int64_t)p.channels * LPC + kNT - 1) / kNT);
+  // one sequence a CTA until they fill the GPU twice over, then up to eight
+  int seqs = 1;
+  while (seqs < 8 && p.n_seqs * blocks >= (int64_t)seqs * 2 * 152 * 16) seqs *= 2;
+  const unsigned grid = (unsigned)((p.n_seqs + seqs - 1) / seqs * blocks);
+  k_ssm_step<T, LPC, V4><<<grid, kNT, 0, st>>>(p, blocks, seqs);
+  return cudaGetLastError();
+}
+
+template <typename T, bool V4>
+cudaError_t launch_step(const SsmParams& p, cudaStream_t st) {
+  if (p.n_state <= 4) return launch_lanes<T, 1, V4>(p, st);
+  if (p.n_state <= 8) return launch_lanes<T, 2, V4>(p, st);
+  if (p.n_state <= 16) return launch_lanes<T, 4, V4>(p, st);
+  if (p.n_state <= 32) return launch_lanes<T, 8, V4>(p, st);
+  return launch_lanes<T, 16, V4>(p, st);
 }
 
 template <typename T>
 cudaError_t launch_token(const SsmParams& p, cudaStream_t st) {
-  const int blocks = (p.channels + kNT - 1) / kNT;
-  const unsigned grid = (unsigned)(p.n_seqs * blocks);
-  if (p.n_state <= 16) k_ssm_step<T, 16><<<grid, kNT, 0, st>>>(p, blocks);
-  else k_ssm_step<T, 64><<<grid, kNT, 0, st>>>(p, blocks);
-  return cudaGetLastError();
+  const uint64_t four = (uint64_t)p.B | (uint64_t)p.C | (uint64_t)(p.sb | p.sc) * sizeof(T);
+  const bool v4 = p.n_state % 4 == 0 && (uint64_t)p.S % 16 == 0 && four % (4 * sizeof(T)) == 0;
+  return v4 ? launch_step<T, true>(p, st) : launch_step<T, false>(p, st);
 }
 
 // --------------------------------------------------------------------------------------------
@@ -64,11 +127,16 @@ struct Shape {
 };
 
 // What a token costs: ns of an SM with nothing else to do, and ns each of many CTAs on it. Measured with 8 to 64 states, bf16 and
-// fp32: 106 to 136 and 98 to 110 with 16 states a thread, 69 to 112 and 50 to 63 with 8, 50 to 71 and 33 to 36 with 4.
+// fp32: 106 to 136 and 98 to 110 with 16 states a thread, 97 to 112 and 50 to 63 with 8 (eight lanes a channel: 69 and 56),
+// 50 to 71 and 33 to 36 with 4.
 struct Cost {
   double alone, many;
 };
-Cost cost_of(int spt) { return spt == 16 ? Cost{125, 99} : spt == 8 ? Cost{100, 54} : Cost{56, 33}; }
+Cost cost_of(Shape s) {
+  if (s.spt == 16) return {125, 99};
+  if (s.spt == 8) return {s.lpc == 8 ? 72.0 : 102.0, 54};
+  return {s.lpc == 4 ? 52.0 : 65.0, 35};
+}
 
 int padded(int n_state) { return n_state <= 8 ? 8 : n_state <= 16 ? 16 : n_state <= 32 ? 32 : 64; }
 int most_states(int n_state) { return padded(n_state) < 16 ? padded(n_state) : 16; }
@@ -92,8 +160,8 @@ int64_t segment(int64_t n_tokens, int64_t ctas, int64_t blocks) {
 }  // namespace
 
 // Of the shapes and of whole and split sequences what should take the least time. Whole sequences take as long as the
-// longest one alone or as all tokens of all CTAs together, and some of the other as well; split ones 1.55 times the latter
-// (the first pass has no outputs) or two segments one after the other, and 8 us for two more launches. Measured against the other
+// longest one alone or as all tokens of all CTAs together, and some of the other as well; split ones two segments one after
+// the other and most of 1.55 times all tokens (the first pass has no outputs), and 14 us for two more launches. Measured against the other
 // choices: one sequence of 16,384 tokens x 4,096 channels of 16 states 490 us split with 16 states a thread, 833 whole with
 // four; 16 ragged ones of up to 1,500 150 and 129; one of 300 x 2,048 channels 33 and 19.
 void ssm_plan(const lq_ssm_config* c, int64_t n_seqs, int64_t n_tokens, int64_t max_len, SsmPlan* plan) {
@@ -102,7 +170,7 @@ void ssm_plan(const lq_ssm_config* c, int64_t n_seqs, int64_t n_tokens, int64_t 
   for (int spt = most_states(c->n_state); spt >= 4; spt /= 2) {
     const Shape s = {spt, padded(c->n_state) / spt};
     if (s.lpc > 8) break;
-    const Cost cost = cost_of(spt);
+    const Cost cost = cost_of(s);
     const int64_t blocks = blocks_of(c, s), seg = segment(n_tokens, ctas_of(s), blocks);
     const double alone = cost.alone * (double)longest, all = cost.many * (double)n_tokens * (double)blocks / kSms;
     const double whole = (alone > all ? alone + 0.3 * all : all + 0.3 * alone) + 3000;
@@ -112,7 +180,7 @@ void ssm_plan(const lq_ssm_config* c, int64_t n_seqs, int64_t n_tokens, int64_t 
     }
     if (longest < 3 * seg) continue;
     const double two = 2 * cost.alone * (double)seg, both = 1.55 * all;
-    const double split = (two > both ? two : both) + 11000 + 60.0 * (double)(longest / seg);
+    const double split = two + 0.6 * both + 14000 + 60.0 * (double)(longest / seg);
     if (split < best) {
       best = split;
       *plan = {s.spt, s.lpc, seg, n_tokens / seg + n_seqs, blocks};
