@@ -135,7 +135,7 @@ struct Cost {
 Cost cost_of(Shape s) {
   if (s.spt == 16) return {125, 99};
   if (s.spt == 8) return {s.lpc == 8 ? 72.0 : 102.0, 54};
-  return {s.lpc == 4 ? 52.0 : 65.0, 35};
+  return {s.lpc == 4 ? 52.0 : 65.0, 34};
 }
 
 int padded(int n_state) { return n_state <= 8 ? 8 : n_state <= 16 ? 16 : n_state <= 32 ? 32 : 64; }
@@ -161,7 +161,7 @@ int64_t segment(int64_t n_tokens, int64_t ctas, int64_t blocks) {
 
 // Of the shapes and of whole and split sequences what should take the least time. Whole sequences take as long as the
 // longest one alone or as all tokens of all CTAs together, and some of the other as well; split ones two segments one after
-// the other and most of 1.55 times all tokens (the first pass has no outputs), and 14 us for two more launches. Measured against the other
+// the other and most of 1.55 times all tokens (the first pass has no outputs), and 16 us for two more launches. Measured against the other
 // choices: one sequence of 16,384 tokens x 4,096 channels of 16 states 490 us split with 16 states a thread, 833 whole with
 // four; 16 ragged ones of up to 1,500 150 and 129; one of 300 x 2,048 channels 33 and 19.
 void ssm_plan(const lq_ssm_config* c, int64_t n_seqs, int64_t n_tokens, int64_t max_len, SsmPlan* plan) {
@@ -180,7 +180,7 @@ void ssm_plan(const lq_ssm_config* c, int64_t n_seqs, int64_t n_tokens, int64_t 
     }
     if (longest < 3 * seg) continue;
     const double two = 2 * cost.alone * (double)seg, both = 1.55 * all;
-    const double split = two + 0.6 * both + 14000 + 60.0 * (double)(longest / seg);
+    const double split = two + 0.6 * both + 16000 + 60.0 * (double)(longest / seg);
     if (split < best) {
       best = split;
       *plan = {s.spt, s.lpc, seg, n_tokens / seg + n_seqs, blocks};
