@@ -468,50 +468,58 @@ def ssm_workspace_bytes(cfg: SsmConfig, n_seqs: int, n_tokens: int, max_len: int
     return int(load().lq_ssm_workspace_bytes(ctypes.byref(cfg), n_seqs, n_tokens, max_len))
 
 
-def _token_rows(t, name, tid, *row):
-    """(address, token stride, tokens) of a token array [tokens][*row] whose tokens may lie apart."""
+def _refuse_rows(t, name, tid, row):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if _dtype_id(t.dtype) != tid:
         raise ValueError(f"{name} must have the configuration's dtype, got {t.dtype}")
     if tuple(t.shape[1:]) != row or t.dim() != 1 + len(row):
         raise ValueError(f"{name} must be [tokens]{list(row)}, got {tuple(t.shape)}")
-    n, dense, strides = t.shape[0], 1, t.stride()
-    if n:
-        for i in range(len(row), 0, -1):
-            if row[i - 1] > 1 and strides[i] != dense:
-                raise ValueError(f"{name}: a token's elements must be contiguous")
-            dense *= row[i - 1]
-    else:
-        for r in row:
-            dense *= r
-    return t.data_ptr(), (strides[0] if n > 1 else dense), n
+    raise ValueError(f"{name}: a token's elements must be contiguous")
+
+
+def _rows_of(t, name, tid, ch):
+    """(address, token stride, tokens) of a token array [tokens][ch] whose tokens may lie apart."""
+    shape, s = t.shape, t.stride()
+    if len(shape) != 2 or shape[1] != ch or not t.is_cuda or _dtypes.get(t.dtype) != tid or \
+            (s[1] != 1 and ch > 1 and shape[0]):
+        _refuse_rows(t, name, tid, (ch,))
+    n = shape[0]
+    return t.data_ptr(), s[0] if n > 1 else ch, n
+
+
+def _group_rows_of(t, name, tid, groups, each):
+    """The same for a token array [tokens][groups][each]."""
+    shape, s = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != groups or shape[2] != each or not t.is_cuda or _dtypes.get(t.dtype) != tid or \
+            (shape[0] and (s[2] != 1 and each > 1 or s[1] != each and groups > 1)):
+        _refuse_rows(t, name, tid, (groups, each))
+    n = shape[0]
+    return t.data_ptr(), s[0] if n > 1 else groups * each, n
 
 
 def _shaped(t, name, dtype, *shape):
-    """Address of a contiguous tensor of this shape, or NULL."""
+    """Address of a contiguous CUDA tensor of this shape and type, or NULL."""
     if t is None:
         return None
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {tuple(t.shape)}")
-    return _ptr(t, name, dtype)
-
-
-def _same_tokens(**counts):
-    if len(set(counts.values())) > 1:
-        raise ValueError("token arrays must have the same number of tokens, got " +
-                         ", ".join(f"{k} {v}" for k, v in counts.items()))
-    return next(iter(counts.values()))
+    if not (t.is_cuda and t.dtype == dtype and t.is_contiguous()):
+        return _ptr(t, name, dtype)  # (says what is wrong)
+    return t.data_ptr()
 
 
 def _conv_tokens(cfg, x, weight, y, bias):
-    px, sx, n = _token_rows(x, "x", cfg.dtype, cfg.channels)
-    py, sy, ny = _token_rows(y, "y", cfg.dtype, cfg.channels)
-    _same_tokens(x=n, y=ny)
-    c = ConvConfig(cfg.channels, cfg.width, cfg.dtype, cfg.silu, sx, sy)
+    ch, W, tid = cfg.channels, cfg.width, cfg.dtype
+    if not _dtypes:
+        _dtype_id(x.dtype)
+    px, sx, n = _rows_of(x, "x", tid, ch)
+    py, sy, ny = _rows_of(y, "y", tid, ch)
+    if n != ny:
+        raise ValueError(f"x and y must have the same number of tokens, got {n} and {ny}")
     f = _f32()
-    return (c, px, _shaped(weight, "weight", f, cfg.channels, cfg.width), _shaped(bias, "bias", f, cfg.channels), py, n,
-            (cfg.width - 1, cfg.channels))
+    return (ConvConfig(ch, W, tid, cfg.silu, sx, sy), px, _shaped(weight, "weight", f, ch, W),
+            _shaped(bias, "bias", f, ch), py, n, W - 1, ch)
 
 
 def conv_prefill(cfg: ConvConfig, x, weight, y, bias=None, cu_seqlens=None, max_len=0, S0=None, S_out=None, stream=None):
@@ -521,31 +529,34 @@ def conv_prefill(cfg: ConvConfig, x, weight, y, bias=None, cu_seqlens=None, max_
     and its last ones, oldest first."""
     import torch
 
-    c, px, pw, pb, py, n, state = _conv_tokens(cfg, x, weight, y, bias)
+    c, px, pw, pb, py, n, w, ch = _conv_tokens(cfg, x, weight, y, bias)
     n_seqs = 1 if cu_seqlens is None else cu_seqlens.numel() - 1
     _check(load().lq_conv_prefill(ctypes.byref(c), n_seqs, n, int(max_len), _ptr(cu_seqlens, "cu_seqlens", torch.int32),
-                                  px, pw, pb, _shaped(S0, "S0", x.dtype, n_seqs, *state),
-                                  _shaped(S_out, "S_out", x.dtype, n_seqs, *state), py, _stream(stream)))
+                                  px, pw, pb, _shaped(S0, "S0", x.dtype, n_seqs, w, ch),
+                                  _shaped(S_out, "S_out", x.dtype, n_seqs, w, ch), py, _stream(stream)))
 
 
 def conv_decode_step(cfg: ConvConfig, S, x, weight, y, bias=None, stream=None):
     """One token for each sequence: x, y [n_seqs][channels]; S [n_seqs][width - 1][channels] holds the last inputs,
     oldest first, and takes x in place of the oldest."""
-    c, px, pw, pb, py, n, state = _conv_tokens(cfg, x, weight, y, bias)
-    _check(load().lq_conv_decode_step(ctypes.byref(c), _shaped(S, "S", x.dtype, n, *state), n, px, pw, pb, py,
+    c, px, pw, pb, py, n, w, ch = _conv_tokens(cfg, x, weight, y, bias)
+    _check(load().lq_conv_decode_step(ctypes.byref(c), _shaped(S, "S", x.dtype, n, w, ch), n, px, pw, pb, py,
                                       _stream(stream)))
 
 
 def _ssm_tokens(cfg, x, dt, A, B, C, y, D, z, dt_bias):
     """A copy of cfg with the token arrays' strides, the call's addresses and the number of tokens."""
     ch, N, G, tid = cfg.channels, cfg.n_state, cfg.groups, cfg.dtype
-    px, sx, n = _token_rows(x, "x", tid, ch)
-    pd, sd, nd = _token_rows(dt, "dt", tid, ch)
-    pb, sb, nb = _token_rows(B, "B", tid, G, N)
-    pc, sc, nc = _token_rows(C, "C", tid, G, N)
-    py, sy, ny = _token_rows(y, "y", tid, ch)
-    pz, sz, nz = (None, ch, n) if z is None else _token_rows(z, "z", tid, ch)
-    _same_tokens(x=n, dt=nd, B=nb, C=nc, y=ny, z=nz)
+    if not _dtypes:
+        _dtype_id(x.dtype)
+    px, sx, n = _rows_of(x, "x", tid, ch)
+    pd, sd, nd = _rows_of(dt, "dt", tid, ch)
+    pb, sb, nb = _group_rows_of(B, "B", tid, G, N)
+    pc, sc, nc = _group_rows_of(C, "C", tid, G, N)
+    py, sy, ny = _rows_of(y, "y", tid, ch)
+    pz, sz, nz = (None, ch, n) if z is None else _rows_of(z, "z", tid, ch)
+    if not (n == nd == nb == nc == ny == nz):
+        raise ValueError(f"x, dt, B, C, y and z must have the same number of tokens, got {n}, {nd}, {nb}, {nc}, {ny}, {nz}")
     f = _f32()
     return (SsmConfig(ch, N, G, tid, cfg.softplus, cfg.reserved, sx, sd, sz, sy, sb, sc), n, px, pd,
             _shaped(A, "A", f, ch, N), pb, pc, _shaped(D, "D", f, ch), pz, _shaped(dt_bias, "dt_bias", f, ch), py)
@@ -572,8 +583,8 @@ def ssm_decode_step(cfg: SsmConfig, S, x, dt, A, B, C, y, D=None, z=None, dt_bia
     """One token for each sequence on fp32 states S [n_seqs][channels][n_state], in place; token arrays as
     ``ssm_prefill`` with one token per sequence."""
     c, n, px, pd, pA, pB, pC, pD, pz, pbias, py = _ssm_tokens(cfg, x, dt, A, B, C, y, D, z, dt_bias)
-    _check(load().lq_ssm_decode_step(ctypes.byref(c), _shaped(S, "S", _f32(), n, c.channels, c.n_state), n, px, pd, pA,
-                                     pB, pC, pD, pz, pbias, py, _stream(stream)))
+    _check(load().lq_ssm_decode_step(ctypes.byref(c), _shaped(S, "S", _f32(), n, cfg.channels, cfg.n_state), n, px, pd,
+                                     pA, pB, pC, pD, pz, pbias, py, _stream(stream)))
 
 
 def token_logprobs(logits, tokens=None, logprob=None, entropy=None, top_logprob=None, top_token=None, stream=None):
