@@ -1,7 +1,10 @@
 // Short causal convolution of every channel (sm_103a), over packed prompts and for single tokens:
 //   y[t][c] = act(bias[c] + sum_j weight[c][j] x[t - (W-1) + j][c]).
-// Bound by memory: an element is read and written once, for W fmas and a silu. A thread has V neighbouring channels, 16 bytes
-// of a token (one where arrays or strides are not aligned to that), in packed pairs, and their weights in registers.
+// Bound by memory: an element is read and written once, for W fmas and a silu. A thread has V neighbouring channels, 8 bytes
+// of a prompt's token or 16 of a single one (one channel where arrays or strides are not aligned to 16 bytes), in packed pairs,
+// and their weights in registers.
+#include <type_traits>
+
 #include "lq_device.cuh"
 #include "lq_seq.cuh"
 
@@ -11,32 +14,25 @@ namespace {
 
 constexpr int kNT = 128;
 
-// V neighbouring channels as they lie in memory, and as floats in pairs (the last one's other half is 0 where V is 1).
+// V neighbouring channels as they lie in memory (one, or 8 or 16 bytes of them, kept as words), and as floats in pairs (where V
+// is 1 the other half of the only pair is 0).
 template <typename T, int V>
 struct Raw {
-  uint4 v;
-};
-template <typename T>
-struct Raw<T, 1> {
-  T v;
+  using Word = typename std::conditional<V == 1, T, typename std::conditional<V * sizeof(T) == 16, uint4, uint2>::type>::type;
+  Word v;
 };
 template <typename T, int V>
 __device__ __forceinline__ Raw<T, V> load(const T* p) {
-  Raw<T, V> r;
-  if constexpr (V == 1) r.v = *p;
-  else r.v = *reinterpret_cast<const uint4*>(p);
-  return r;
+  return {*reinterpret_cast<const typename Raw<T, V>::Word*>(p)};
 }
 template <typename T, int V>
 __device__ __forceinline__ void store(T* p, const Raw<T, V>& r) {
-  if constexpr (V == 1) *p = r.v;
-  else *reinterpret_cast<uint4*>(p) = r.v;
+  *reinterpret_cast<typename Raw<T, V>::Word*>(p) = r.v;
 }
 template <typename T, int V>
 __device__ __forceinline__ Raw<T, V> nothing() {
   Raw<T, V> r;
-  if constexpr (V == 1) r.v = from_f<T>(0.0f);
-  else r.v = make_uint4(0, 0, 0, 0);
+  memset(&r, 0, sizeof r);
   return r;
 }
 
@@ -45,28 +41,23 @@ constexpr int kPairs = (V + 1) / 2;
 
 template <typename T, int V>
 __device__ __forceinline__ void unpack(const Raw<T, V>& r, f32x2 (&f)[kPairs<V>]) {
-  if constexpr (V == 1) {
-    f[0] = f2_pack(to_f(r.v), 0.0f);
-  } else {
-    T t[V];
-    memcpy(t, &r.v, 16);
+  T t[V];
+  memcpy(t, &r, sizeof t);
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) f[i] = f2_pack(to_f(t[2 * i]), to_f(t[2 * i + 1]));
-  }
+  for (int i = 0; i < kPairs<V>; ++i) f[i] = f2_pack(to_f(t[2 * i]), 2 * i + 1 < V ? to_f(t[(2 * i + 1) % V]) : 0.0f);
 }
 template <typename T, int V>
 __device__ __forceinline__ Raw<T, V> pack(const f32x2 (&f)[kPairs<V>]) {
-  Raw<T, V> r;
-  T t[2 * kPairs<V>];
+  T t[V];
 #pragma unroll
   for (int i = 0; i < kPairs<V>; ++i) {
     float a, b;
     f2_unpack(f[i], a, b);
     t[2 * i] = from_f<T>(a);
-    t[2 * i + 1] = from_f<T>(b);
+    if (2 * i + 1 < V) t[(2 * i + 1) % V] = from_f<T>(b);
   }
-  if constexpr (V == 1) r.v = t[0];
-  else memcpy(&r.v, t, 16);
+  Raw<T, V> r;
+  memcpy(&r, t, sizeof t);
   return r;
 }
 
@@ -115,7 +106,8 @@ struct Taps {
   }
 };
 
-// One thread: V channels' tokens of one tile, the last W - 1 inputs in registers, eight tokens' loads at a time.
+// One thread: V channels' tokens of one tile, the last W - 1 inputs in registers, the next eight tokens on
+// their way.
 template <typename T, int W, int V>
 __global__ void __launch_bounds__(kNT) k_conv(ConvParams p, int blocks) {
   constexpr int U = 8, P = kPairs<V>;
@@ -132,9 +124,15 @@ __global__ void __launch_bounds__(kNT) k_conv(ConvParams p, int blocks) {
     if (t >= 0) return load<T, V>(x + (begin + t) * p.sx);
     return S0 ? load<T, V>(S0 + (t + W - 1) * C) : nothing<T, V>();
   };
-  Raw<T, V> first[W - 1];
+  const int n = (int)pc.len;
+  const T* from = x + pc.begin * p.sx;
+  T* to = static_cast<T*>(p.y) + c + pc.begin * p.sy;
+  Raw<T, V> first[W - 1], r[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) r[u] = u < n ? load<T, V>(from + u * p.sx) : nothing<T, V>();
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) first[j] = input(pc.begin - at, at - (W - 1) + j);
+  from += U * p.sx;
   Taps<W, V> taps;
   taps.read(p, c);
   if (p.S && pc.i == 0) {
@@ -151,18 +149,13 @@ __global__ void __launch_bounds__(kNT) k_conv(ConvParams p, int blocks) {
   f32x2 in[W][P];
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) unpack<T, V>(first[j], in[j]);
-  const T* from = x + pc.begin * p.sx;
-  T* to = static_cast<T*>(p.y) + c + pc.begin * p.sy;
-  const int n = (int)pc.len;
   for (int t0 = 0; t0 < n; t0 += U) {
-    Raw<T, V> r[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) r[u] = t0 + u < n ? load<T, V>(from + u * p.sx) : nothing<T, V>();
-    from += U * p.sx;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (t0 + u >= n) break;
       unpack<T, V>(r[u], in[W - 1]);
+      if (t0 + u + U < n) r[u] = load<T, V>(from);
+      from += p.sx;
       store<T, V>(to, taps.template out<T>(in, p.silu));
       to += p.sy;
 #pragma unroll
@@ -204,24 +197,30 @@ __global__ void __launch_bounds__(kNT) k_conv_step(ConvParams p, int blocks, int
   }
 }
 
+// Bytes of a token that a thread of a prompt has: 16 take 128 registers and more, which leaves 12 warps an SM (4,132 tokens of
+// 16 sequences x 8,192 channels, bf16: 29.9 us, 68% of the copy bandwidth; 33.0 with 16 bytes).
+constexpr int kPrompt = 8;
+
 template <typename T, int W, int V>
-cudaError_t launch_taps(const ConvParams& p, bool step, cudaStream_t st) {
+cudaError_t launch_prompts(const ConvParams& p, cudaStream_t st) {
   const int blocks = (p.channels + kNT * V - 1) / (kNT * V);
-  if (!step) {
-    k_conv<T, W, V><<<(unsigned)(p.slots * blocks), kNT, 0, st>>>(p, blocks);
-  } else {
-    int seqs = 1;  // one a CTA until they fill the GPU twice over, then up to eight
-    while (seqs < 8 && p.n_seqs * blocks >= (int64_t)seqs * 2 * 152 * 4) seqs *= 2;
-    k_conv_step<T, W, V><<<(unsigned)((p.n_seqs + seqs - 1) / seqs * blocks), kNT, 0, st>>>(p, blocks, seqs);
-  }
+  k_conv<T, W, V><<<(unsigned)(p.slots * blocks), kNT, 0, st>>>(p, blocks);
   return cudaGetLastError();
 }
 
-template <typename T, int V>
-cudaError_t launch_width(const ConvParams& p, bool step, cudaStream_t st) {
-  if (p.width == 2) return launch_taps<T, 2, V>(p, step, st);
-  if (p.width == 3) return launch_taps<T, 3, V>(p, step, st);
-  return launch_taps<T, 4, V>(p, step, st);
+template <typename T, int W, int V>
+cudaError_t launch_tokens(const ConvParams& p, cudaStream_t st) {
+  const int blocks = (p.channels + kNT * V - 1) / (kNT * V);
+  int seqs = 1;  // one a CTA until they fill the GPU twice over, then up to eight
+  while (seqs < 8 && p.n_seqs * blocks >= (int64_t)seqs * 2 * 152 * 4) seqs *= 2;
+  k_conv_step<T, W, V><<<(unsigned)((p.n_seqs + seqs - 1) / seqs * blocks), kNT, 0, st>>>(p, blocks, seqs);
+  return cudaGetLastError();
+}
+
+template <typename T, int W>
+cudaError_t launch_width(const ConvParams& p, bool step, bool vec, cudaStream_t st) {
+  if (step) return vec ? launch_tokens<T, W, 16 / (int)sizeof(T)>(p, st) : launch_tokens<T, W, 1>(p, st);
+  return vec ? launch_prompts<T, W, kPrompt / (int)sizeof(T)>(p, st) : launch_prompts<T, W, 1>(p, st);
 }
 
 int wide(const ConvParams& p) {  // channels of 16 bytes, or 1
@@ -232,7 +231,10 @@ int wide(const ConvParams& p) {  // channels of 16 bytes, or 1
 
 template <typename T>
 cudaError_t launch(const ConvParams& p, bool step, cudaStream_t st) {
-  return wide(p) > 1 ? launch_width<T, 16 / sizeof(T)>(p, step, st) : launch_width<T, 1>(p, step, st);
+  const bool vec = wide(p) > 1;
+  if (p.width == 2) return launch_width<T, 2>(p, step, vec, st);
+  if (p.width == 3) return launch_width<T, 3>(p, step, vec, st);
+  return launch_width<T, 4>(p, step, vec, st);
 }
 
 cudaError_t launch_any(const ConvParams& p, bool step, cudaStream_t st) {
@@ -245,9 +247,10 @@ cudaError_t launch_any(const ConvParams& p, bool step, cudaStream_t st) {
 
 // Tiles of 64 tokens, or of fewer down to 8 where those would not fill the GPU.
 void conv_plan(ConvParams& p) {
-  const int64_t blocks = (p.channels + kNT * wide(p) - 1) / (kNT * wide(p));
+  const int v = wide(p) > 1 ? wide(p) * kPrompt / 16 : 1;
+  const int64_t blocks = (p.channels + kNT * v - 1) / (kNT * v);
   p.seg = 64;
-  while (p.seg > 8 && p.n_tokens / p.seg * blocks < 152 * 6) p.seg /= 2;
+  while (p.seg > 8 && p.n_tokens / p.seg * blocks < 152 * 12) p.seg /= 2;
   p.slots = p.n_tokens / p.seg + p.n_seqs;
 }
 

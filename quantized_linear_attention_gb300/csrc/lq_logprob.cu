@@ -6,13 +6,15 @@
 // the exponentials and the sum of the exponentials times their exponents; 32 elements at a time are compared with
 // the largest, so the sums are rescaled by one rare branch.
 //
-// The n_top largest without a sort: after the first tile, and whenever twice as many have gone by, the CTA looks at the
-// maxima of 64 groups of four threads: at least n_top elements are not below the n_top-th largest of those. Elements at or
+// The n_top largest without a sort: after the first tile, and whenever eight times as many have gone by, the CTA looks at the
+// maxima of 8 or 64 groups of its threads: at least n_top elements are not below the n_top-th largest of those. Elements at or
 // above that bound are collected as they go by, a few times n_top in all; those that still are when the slice is through
 // are ranked by counting. Where rising or very many equal logits make them more than the list holds, the slice is read
 // again: a bisection over the values finds one that few enough are not below, or, where equal ones are too many, the exact
 // n_top-th value, of which those with the lowest indices are taken in order.
 #include <cooperative_groups.h>
+
+#include <type_traits>
 
 #include "lq_device.cuh"
 #include "lq_seq.cuh"
@@ -27,6 +29,7 @@ constexpr int kNT = 256;
 constexpr int kLoads = 4;     // 16-byte loads in flight
 constexpr int kList = 1024;   // elements collected
 constexpr int kRank = 512;    // of which at most so many are ranked
+constexpr int kFew = 64;      // ranked without another look at the bound
 constexpr int kMaxCluster = 8;
 constexpr float kLn2 = 0.693147180559945309417f;
 
@@ -127,6 +130,7 @@ struct Shared {
   uint64_t best[32];  // kMaxTop of this CTA's elements in order, 0 past the last
   float groups[64];
   Sum part[kNT / 32], all;
+  float refs[kNT / 32];
   int warp_count[kNT / 32];
   float bound;
   int count, kept;
@@ -145,12 +149,28 @@ __device__ __forceinline__ int count_all(Shared& sm, int c) {
   return n;
 }
 
-// The bound from the maxima of 64 groups of four threads: the k-th largest (-inf if fewer have any).
+// The k-th largest of the maxima of groups of threads (-inf if fewer have any): a warp each for k up to 8, else four threads.
 __device__ __forceinline__ float new_bound(Shared& sm, float mine, int k) {
   const int tid = threadIdx.x;
   if (!(mine >= -INFINITY)) mine = -INFINITY;  // (a row with a NaN has no answer: any bound will do)
   mine = fmaxf(mine, __shfl_xor_sync(0xffffffffu, mine, 1));
   mine = fmaxf(mine, __shfl_xor_sync(0xffffffffu, mine, 2));
+  if (k <= kNT / 32) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) mine = fmaxf(mine, __shfl_xor_sync(0xffffffffu, mine, o));
+    __syncthreads();
+    if ((tid & 31) == 0) sm.groups[tid >> 5] = mine;
+    __syncthreads();
+    const float me = sm.groups[tid & 7];
+    int rank = 0;
+#pragma unroll
+    for (int j = 0; j < kNT / 32; ++j) {
+      const float y = sm.groups[j];
+      rank += (y > me || (y == me && j < (tid & 7))) ? 1 : 0;
+    }
+    const unsigned at = __ballot_sync(0xffffffffu, rank == k - 1);
+    return __shfl_sync(0xffffffffu, me, __ffs((int)at) - 1);
+  }
   __syncthreads();
   if ((tid & 3) == 0) sm.groups[tid >> 2] = mine;
   __syncthreads();
@@ -269,21 +289,23 @@ __global__ void __launch_bounds__(kNT) k_logprob(LogprobParams p, int cluster) {
     edge = to_f(x[edge_at]);
   }
 
-  int64_t next = 1;  // tiles before the bound is looked at again
-  int64_t tile = 0;
-  for (int64_t v = v0; v < v1; v += kLoads * kNT) {
-    uint4 w[kLoads];
+  int64_t next = 1, tile = 0;  // tiles before the bound is looked at again
+  // J vectors of every thread, kNT apart; WHOLE: all of them are the slice's.
+  auto take = [&](int64_t v, auto count, auto whole) {
+    constexpr int J = decltype(count)::value;
+    constexpr bool WHOLE = decltype(whole)::value;
+    uint4 w[J];
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j) {
+    for (int j = 0; j < J; ++j) {
       const int64_t at = v + j * kNT + tid;
-      w[j] = at < v1 ? __ldcs(body + at) : all_masked<T>();
+      w[j] = WHOLE || at < v1 ? __ldcs(body + at) : all_masked<T>();
     }
-    float big[kLoads], now;
+    float big[J], now;
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j) big[j] = largest(w[j], T());
+    for (int j = 0; j < J; ++j) big[j] = largest(w[j], T());
     now = big[0];
 #pragma unroll
-    for (int j = 1; j < kLoads; ++j) now = max_nan(now, big[j]);
+    for (int j = 1; j < J; ++j) now = max_nan(now, big[j]);
     if (!(now <= m.ref)) {  // a new largest (or a NaN, which stays)
       if (m.ref > -INFINITY) {
         const float u = __fmul_rn(__fsub_rn(m.ref, now), kLog2E);
@@ -298,7 +320,7 @@ __global__ void __launch_bounds__(kNT) k_logprob(LogprobParams p, int cluster) {
     if (m.ref > -INFINITY || m.ref != m.ref) {
       const f32x2 ref2 = f2_dup(-m.ref), l2 = f2_dup(kLog2E);
 #pragma unroll
-      for (int j = 0; j < kLoads; ++j) {
+      for (int j = 0; j < J; ++j) {
         f32x2 f[P];
         floats4(w[j], f, T());
 #pragma unroll
@@ -317,12 +339,12 @@ __global__ void __launch_bounds__(kNT) k_logprob(LogprobParams p, int cluster) {
     if (TOP) {
       top = fmaxf(top, now);
       if (++tile == next) {
-        next *= 2;
+        next *= 8;
         bound = new_bound(sm, fmaxf(top, edge), p.n_top);
       }
       if (now >= bound && now > -INFINITY) {
 #pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
+        for (int j = 0; j < J; ++j) {
           if (!(big[j] >= bound)) continue;
           const T* const el = reinterpret_cast<const T*>(&w[j]);
 #pragma unroll
@@ -336,63 +358,87 @@ __global__ void __launch_bounds__(kNT) k_logprob(LogprobParams p, int cluster) {
         }
       }
     }
-  }
-  {
+  };
+  int64_t v = v0;
+  for (; v + kLoads * kNT <= v1; v += kLoads * kNT) take(v, std::integral_constant<int, kLoads>(), std::true_type());
+  for (; v < v1; v += kNT) take(v, std::integral_constant<int, 1>(), std::false_type());
+
+  // The CTA's largest, and the threads' sums relative to it
+  if (!(edge <= -INFINITY)) {
     float a, b;
     f2_unpack(s2, a, b);
     m.s = __fadd_rn(a, b);
     f2_unpack(e2, a, b);
     m.e = __fadd_rn(a, b);
-    if (!(edge <= -INFINITY)) m = join(m, {edge, 1.0f, 0.0f});
+    m = join(m, {edge, 1.0f, 0.0f});
+    s2 = f2_pack(m.s, 0.0f);
+    e2 = f2_pack(m.e, 0.0f);
+  }
+  float all = m.ref;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) all = max_nan(all, __shfl_xor_sync(0xffffffffu, all, o));
+  if (lane == 0) sm.refs[warp] = all;
+  if (TOP) top = fmaxf(top, edge);
+  __syncthreads();
+  if (TOP && edge >= bound && edge > -INFINITY) {
+    const int c = atomicAdd(&sm.count, 1);
+    if (c < kList) sm.list[c] = key_of(edge, edge_at);
   }
 #pragma unroll
-  for (int o = 16; o; o >>= 1)
-    m = join(m, {__shfl_xor_sync(0xffffffffu, m.ref, o), __shfl_xor_sync(0xffffffffu, m.s, o),
-                 __shfl_xor_sync(0xffffffffu, m.e, o)});
-  if (lane == 0) sm.part[warp] = m;
-  if (TOP) {
-    top = fmaxf(top, edge);
-    bound = new_bound(sm, top, p.n_top);  // (its barriers are also behind what was collected, and in front of its use)
-    if (edge >= bound && edge > -INFINITY) {
-      const int c = atomicAdd(&sm.count, 1);
-      if (c < kList) sm.list[c] = key_of(edge, edge_at);
+  for (int w = 0; w < kNT / 32; ++w) all = max_nan(all, sm.refs[w]);
+  {
+    float a, b, s, e;
+    f2_unpack(s2, a, b);
+    s = __fadd_rn(a, b);
+    f2_unpack(e2, a, b);
+    e = __fadd_rn(a, b);
+    if (m.ref == -INFINITY) {
+      s = e = 0.0f;  // (nothing met; a NaN is in the reference)
+    } else {
+      const float u = __fmul_rn(__fsub_rn(m.ref, all), kLog2E), f = ex2_approx(u);
+      e = __fmul_rn(f, __fmaf_rn(fmaxf(u, -1e30f), s, e));
+      s = __fmul_rn(f, s);
     }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
+      e = __fadd_rn(e, __shfl_xor_sync(0xffffffffu, e, o));
+    }
+    if (lane == 0) sm.part[warp] = {all, s, e};
   }
   __syncthreads();
-  m = sm.part[0];
-  for (int w = 1; w < kNT / 32; ++w) m = join(m, sm.part[w]);
-  if (tid == 0) sm.all = m;
+  if (tid == 0) {
+    m = sm.part[0];
+#pragma unroll
+    for (int w = 1; w < kNT / 32; ++w) {
+      m.s = __fadd_rn(m.s, sm.part[w].s);
+      m.e = __fadd_rn(m.e, sm.part[w].e);
+    }
+    sm.all = m;
+  }
 
   if (TOP) {
-    // Of the elements collected those not below the last bound, ranked by counting.
+    // The elements collected are ranked by counting: where they are many, those that are not below a last bound.
     int n = sm.count;
-    const bool over = n > kList;
-    uint64_t mine[kList / kNT];
-    if (!over) {
+    if (n > kFew) {
+      const bool over = n > kList;
+      bound = new_bound(sm, top, p.n_top);
+      if (!over) {
+        uint64_t mine[kList / kNT];
 #pragma unroll
-      for (int i = 0; i < kList / kNT; ++i) {
-        const int at = i * kNT + tid;
-        mine[i] = at < n ? sm.list[at] : 0;
-        if (mine[i] && value_of(mine[i]) < bound) mine[i] = 0;
+        for (int i = 0; i < kList / kNT; ++i) {
+          const int at = i * kNT + tid;
+          mine[i] = at < n ? sm.list[at] : 0;
+          if (mine[i] && value_of(mine[i]) < bound) mine[i] = 0;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kList / kNT; ++i)
+          if (mine[i]) sm.list[atomicAdd(&sm.kept, 1)] = mine[i];
+        __syncthreads();
+        n = sm.kept;
       }
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kList / kNT; ++i)
-        if (mine[i]) sm.list[atomicAdd(&sm.kept, 1)] = mine[i];
-      __syncthreads();
-      n = sm.kept;
-    }
-    if (over || n > kRank) {
-      const float least = over || n > kRank ? bound : 0.0f;
-      float largest_here = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-#pragma unroll
-      for (int o = 8; o; o >>= 1) largest_here = fmaxf(largest_here, __shfl_xor_sync(0xffffffffu, largest_here, o));
-      __syncthreads();
-      if (lane == 0) sm.groups[warp] = largest_here;
-      __syncthreads();
-#pragma unroll
-      for (int w = 0; w < kNT / 32; ++w) largest_here = fmaxf(largest_here, sm.groups[w]);
-      n = take_again(sm, x + e0, e1 - e0, e0, p.n_top, least, largest_here);
+      if (over || n > kRank) n = take_again(sm, x + e0, e1 - e0, e0, p.n_top, bound, all);
     }
     if (tid < 32) sm.best[tid] = 0;
     __syncthreads();
@@ -409,9 +455,8 @@ __global__ void __launch_bounds__(kNT) k_logprob(LogprobParams p, int cluster) {
     __syncthreads();
   }
   if (rank == 0) {
-    if (tid >= 32) {
-      m = sm.all;
-    } else if (cluster > 1) {
+    m = sm.all;
+    if (tid < 32 && cluster > 1) {
       cg::cluster_group cl = cg::this_cluster();
       m = {-INFINITY, 0.0f, 0.0f};
       if (lane < cluster) m = *cl.map_shared_rank(&sm.all, lane);
@@ -471,11 +516,12 @@ __global__ void __launch_bounds__(kNT) k_logprob(LogprobParams p, int cluster) {
   if (cluster > 1) cg::this_cluster().sync();  // the others' shared memory is read until here
 }
 
-// CTAs for a row: enough to fill the GPU four times over, as long as a slice has a few KB.
+// CTAs for a row: enough for two an SM, as long as a slice has a few KB (128 rows of 131,071 fp32: 25 us with 4
+// CTAs a row, 31 with 8).
 int cluster_of(const LogprobParams& p) {
   const int64_t bytes = p.vocab * (p.dtype == LQ_F32 ? 4 : 2);
   int c = 1;
-  while (c < kMaxCluster && p.rows * c < 4 * 152 && bytes / (2 * c) >= 4096) c *= 2;
+  while (c < kMaxCluster && p.rows * c < 2 * 152 && bytes / (2 * c) >= 4096) c *= 2;
   return c;
 }
 
