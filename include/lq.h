@@ -489,7 +489,7 @@ void lq_conv_config_default(lq_conv_config* cfg, int32_t channels, int32_t width
  *   S0, S_out  [n_seqs][W-1][channels] of cfg->dtype, or NULL; S_out gets the last W-1
  *              inputs of each sequence, S0's among them where it has fewer tokens; it may
  *              be S0 itself
- * Sums are kept in fp32; y is rounded once. Faster where x, y, S0, S_out, weight and the
+ * n_tokens is at most 2^31 - 256. Sums are kept in fp32; y is rounded once. Faster where x, y, S0, S_out, weight and the
  * strides are multiples of 16 bytes and so is a row of channels.
  */
 int lq_conv_prefill(const lq_conv_config* cfg, int64_t n_seqs, int64_t n_tokens, int64_t max_len,
@@ -536,8 +536,9 @@ size_t lq_ssm_workspace_bytes(const lq_ssm_config* cfg, int64_t n_seqs, int64_t 
  *   S0, S_out    fp32 [n_seqs][channels][n_state] or NULL (a zero first state, no last
  *                one); S_out may be S0 itself
  *   workspace    256-byte aligned, lq_ssm_workspace_bytes(...) bytes for these sizes or
- *                larger ones (NULL if that is 0); its contents need not be kept
- * States and sums are kept in fp32; y is rounded once. Any value is taken as the recurrence
+ *                larger ones (NULL if that is 0); its contents need not be kept, but calls
+ *                that may run at the same time (streams, graphs) need one each
+ * n_tokens is at most 2^31 - 256. States and sums are kept in fp32; y is rounded once. Any value is taken as the recurrence
  * takes it; a token's value reaches its own and later tokens of its sequence only. Long
  * sequences are split into segments; channels with a positive A, a negative or infinite d,
  * or values past 1e30 pass from segment to segment token by token, which is slow.

@@ -408,9 +408,12 @@ int check_reorder(int64_t n_states, int64_t outer, int64_t groups, int32_t beams
 }
 
 // Sizes of packed prompts.
+constexpr int64_t kMaxTokens = 0x7fffff00;  // (tokens are counted in 32 bits, some tiles past the last)
+
 int check_packed(int64_t n_seqs, int64_t n_tokens, int64_t max_len, const int32_t* cu) {
-  if (n_seqs < 0 || n_seqs > 0x7fffffff || n_tokens < 0 || n_tokens > 0x7fffffff || max_len < 0)
-    return fail(LQ_ERR_INVALID_ARG, "n_seqs and n_tokens must be 0..%d, max_len must not be negative", 0x7fffffff);
+  if (n_seqs < 0 || n_seqs > 0x7fffffff || n_tokens < 0 || n_tokens > kMaxTokens || max_len < 0)
+    return fail(LQ_ERR_INVALID_ARG, "n_seqs must be 0..%d, n_tokens 0..%lld, max_len must not be negative", 0x7fffffff,
+                (long long)kMaxTokens);
   if (n_seqs == 0) return LQ_OK;
   if (!cu && n_seqs != 1) return fail(LQ_ERR_INVALID_ARG, "cu_seqlens is NULL with n_seqs > 1");
   if (!cu && max_len > 0 && max_len < n_tokens)

@@ -102,7 +102,7 @@ __device__ __forceinline__ Piece find_slot(const P& p, int64_t slot) {
     return r;
   }
   constexpr int NW = NT / 32;
-  __shared__ int wsum[NW];
+  __shared__ int64_t wsum[NW];
   __shared__ Piece found;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) found = r;
@@ -110,16 +110,15 @@ __device__ __forceinline__ Piece find_slot(const P& p, int64_t slot) {
   for (int64_t b0 = 0; b0 < p.n_seqs; b0 += NT) {
     const int64_t b = b0 + tid;
     int64_t begin = 0, len = 0;
-    int n = 0;
+    int64_t n = 0;
     if (b < p.n_seqs) {
       bounds(p, b, begin, len);
-      n = len > p.seg ? (int)((len + p.seg - 1) / p.seg) : 1;
+      n = len > p.seg ? (len + p.seg - 1) / p.seg : 1;
     }
-    int sum = n;  // (at most 2^31 / seg + NT in a round of sequences that do not overlap; those that do may wrap
-                  // and are not served)
+    int64_t sum = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, sum, o);
+      const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += x;
     }
     __syncthreads();

@@ -10,11 +10,12 @@ namespace {
 // Bound by memory: a state is read and written, 8 bytes for about six operations. A lane holds four neighbouring states of a
 // channel (V4: by 16 bytes), LPC lanes a channel; a CTA takes one block of channels and K sequences after K others, whose
 // loads are all begun before the first is used, so that A is read once for all of them. (512 sequences x 4,096 channels of 16
-// states, bf16: 59 us with K = 2 and 32 warps an SM, 66 with 1 and as many, 69 to 71 with 24 warps, 76 with K = 4 and 20.)
+// states, bf16, three batches of states in turn: 63 us with K = 2 and 32 warps an SM, 67% of the copy bandwidth; 66 with 3, 70 with
+// 1 and 48 warps, 77 with 4 and 24 warps; 71 with loads and stores marked as streaming.)
 template <typename T, int LPC, bool V4, int K>
 __device__ __forceinline__ void tokens(const SsmParams& p, int64_t b, int c, int g, bool live, const float (&A)[4],
                                        float bias, float D) {
-  const int part = (threadIdx.x & 31) / (32 / LPC), n0 = 4 * part;
+  const int part = threadIdx.x % LPC, n0 = 4 * part;
   const int64_t row = (int64_t)p.channels * p.n_state;
   float* const S = p.S + b * row + (int64_t)c * p.n_state + n0;
   const T* const Bp = static_cast<const T*>(p.B) + b * p.sb + (int64_t)g * p.n_state + n0;
@@ -31,7 +32,7 @@ __device__ __forceinline__ void tokens(const SsmParams& p, int64_t b, int c, int
     for (int e = 0; e < 4; ++e) h[k][e] = B[k][e] = C[k][e] = 0.0f;
     if (V4) {
       if (in) {
-        const float4 v = __ldcs(reinterpret_cast<const float4*>(S + k * row));
+        const float4 v = *reinterpret_cast<const float4*>(S + k * row);
         h[k][0] = v.x, h[k][1] = v.y, h[k][2] = v.z, h[k][3] = v.w;
         ld4(Bp + k * p.sb, B[k]);
         ld4(Cp + k * p.sc, C[k]);
@@ -58,26 +59,26 @@ __device__ __forceinline__ void tokens(const SsmParams& p, int64_t b, int c, int
       y = __fmaf_rn(C[k][e], h[k][e], y);
     }
     if (V4 && in && live) {
-      __stcs(reinterpret_cast<float4*>(S + k * row), make_float4(h[k][0], h[k][1], h[k][2], h[k][3]));
+      *reinterpret_cast<float4*>(S + k * row) = make_float4(h[k][0], h[k][1], h[k][2], h[k][3]);
     } else if (!V4 && live) {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (n0 + e < p.n_state) S[k * row + e] = h[k][e];
     }
 #pragma unroll
-    for (int s = 32 / LPC; s < 32; s <<= 1) y = __fadd_rn(y, __shfl_xor_sync(0xffffffffu, y, s));
+    for (int s = 1; s < LPC; s <<= 1) y = __fadd_rn(y, __shfl_xor_sync(0xffffffffu, y, s));
     y = __fmaf_rn(D, xv, y);
     if (p.z) y = __fmul_rn(y, silu(to_f(z[k])));
     if (part == 0 && live) static_cast<T*>(p.y)[(b + k) * p.sy + c] = from_f<T>(y);
   }
 }
 
-// Consecutive lanes hold consecutive channels, the parts of a channel lie 32 / LPC lanes apart.
+// Neighbouring lanes hold neighbouring parts of a channel, so that eight lanes' states are 128 bytes in a row.
 template <typename T, int LPC, bool V4>
 __global__ void __launch_bounds__(kNT, 8) k_ssm_step(SsmParams p, int blocks, int seqs) {
-  constexpr int CW = 32 / LPC, K = 2;
-  const int lane = threadIdx.x & 31, part = lane / CW;
-  const int at = (int)(blockIdx.x % (unsigned)blocks) * (kNT / LPC) + (threadIdx.x >> 5) * CW + lane % CW;
+  constexpr int K = 2;
+  const int part = threadIdx.x % LPC;
+  const int at = (int)(blockIdx.x % (unsigned)blocks) * (kNT / LPC) + threadIdx.x / LPC;
   const bool live = at < p.channels;
   const int c = live ? at : 0;
   float A[4];

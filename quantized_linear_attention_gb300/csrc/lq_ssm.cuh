@@ -23,15 +23,22 @@ namespace {
 // --------------------------------------------------------------------------------------------
 // Prompts. A thread holds SPT states of a channel (LPC lanes of a warp share one channel) and takes the tokens of a piece
 // one after the other: per state and token a multiplication and an exponential for the decay, a multiplication and an fma for
-// the state and an fma for y, in packed pairs of states. B and C are the same for all channels of a group: 16 tokens of them
-// at a time lie in shared memory as floats, read by broadcast; x, dt and z come straight into registers, 8 tokens ahead.
+// the state and an fma for y, in packed pairs of states. x, dt and z come into shared memory a tile ahead by asynchronous
+// copies, y goes out from there by 16 bytes; B and C, the same for all channels of a group, lie there as floats.
+//
+// What bounds it: 11 operands from the register file for each state and token, whose two banks give two a cycle: 105 cycles
+// of an SM's quarter for 512 states and a token, measured on these operations alone (their FMAs and their exponentials take
+// 64 each). Steps, gates and copies come on top: 1,024 tokens x 65,536 channels of 16 states (bf16) take 328 us, 180 cycles. With
+// so few channels that an SM has one CTA the waits count instead: 136 ns a token with 16 states a thread, 52 with four
+// and 32 tokens begun together, which is a third slower where there are many.
 //
 // A sequence that would leave most of the GPU idle is split into segments (ssm_plan). The first pass takes
 // every segment but the last from a zero state (the first from its true one, with its outputs) and leaves its last state and
 // the sum of its d; since the decays of a segment multiply to exp(A sum d), k_ssm_join finds the state before each segment,
 // and the second pass takes the segments from there. What that sum over segments does not give as the recurrence does (a
 // positive A or a negative d, where it may overflow though the recurrence does not, infinities, values near fp32's largest
-// number) k_ssm_join takes token by token.
+// number) k_ssm_join takes token by token. 16,384 tokens x 4,096 channels of 16 states (bf16) take 481 us: 207 the first
+// pass, 280 the second, which a single pass that leaves three quarters of the GPU idle cannot match (833).
 constexpr int kNT = 128;
 // Tokens begun together, and in shared memory at a time. More of them hide more of each other's waits (one CTA an SM: 136 ->
 // 52 ns a token with four states a thread and 32 tokens), as far as the registers go.
@@ -349,7 +356,7 @@ __global__ void __launch_bounds__(256, 4) k_ssm_join(SsmParams p, int blocks) {
   if (pc.n == 1) return;
   const int64_t slot = first_slot<256>(p, b);
   cudaGridDependencySynchronize();
-  if (at >= row) return;
+  if (at >= row || slot >= p.slots) return;  // (no such slots where sequences do not overlap)
   const int64_t c = at / p.n_state, segs = min(pc.n, p.slots - slot);
   float* ws = p.ws_state + slot * row + at;
   const float* step = p.ws_step + slot * p.channels + c;
