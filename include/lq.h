@@ -539,7 +539,9 @@ size_t lq_ssm_workspace_bytes(const lq_ssm_config* cfg, int64_t n_seqs, int64_t 
  *                larger ones (NULL if that is 0); its contents need not be kept, but calls
  *                that may run at the same time (streams, graphs) need one each
  * n_tokens is at most 2^31 - 256. States and sums are kept in fp32; y is rounded once. Any value is taken as the recurrence
- * takes it; a token's value reaches its own and later tokens of its sequence only. Long
+ * takes it; a token's value reaches its own and later tokens of its sequence only. (Where
+ * n_state is not 8, 16, 32 or 64, outputs that an infinite x or d makes infinite may be NaN,
+ * here and in lq_ssm_decode_step; states are as the recurrence has them.) Long
  * sequences are split into segments; channels with a positive A, a negative or infinite d,
  * or values past 1e30 pass from segment to segment token by token, which is slow.
  */
