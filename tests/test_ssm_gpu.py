@@ -269,3 +269,25 @@ def test_offsets_past_32_bits():
         call(cfg, b, [T], S)
         assert torch.equal(b["y"], want)
         del far, b
+
+
+@pytest.mark.parametrize("T,N", [(60, 5), (1300, 5), (70, 12), (50, 20)])
+def test_infinities_with_any_number_of_states(T, N):
+    """States are as the recurrence has them; outputs are finite exactly where it has finite ones (an infinite one may be
+    NaN where n_state is not a power of two)."""
+    a = inputs(19, [T], 20, N, 1, torch.float32)
+    a["x"][T // 3, 2], a["x"][T - 2, 3], a["S0"][0, 7, N - 1] = INF, -INF, INF
+    y_r, S_r, _, _ = reference(a, [T], True)
+    S = torch.empty(1, 20, N, device=DEV)
+    call(lq.ssm_config(20, N, 1, torch.float32), a, [T], S, max_len=T)
+    assert np.array_equal(np.isfinite(f64(a["y"])), np.isfinite(y_r))
+    got = f64(S)
+    assert np.array_equal(np.isnan(got), np.isnan(S_r)) and np.array_equal(got[np.isinf(S_r)], S_r[np.isinf(S_r)])
+    one, s1 = torch.empty(1, 20, device=DEV), a["S0"].clone()
+    t = T // 3
+    part = {k: v[t:t + 1] if k in ("x", "dt", "B", "C", "y", "z") else v for k, v in a.items()}
+    y1, S1, _, _ = reference(part, [1], True, s1)
+    lq.ssm_decode_step(lq.ssm_config(20, N, 1, torch.float32), s1, part["x"], part["dt"], a["A"], part["B"], part["C"], one,
+                       D=a["D"], z=part["z"], dt_bias=a["bias"])
+    assert np.array_equal(np.isfinite(f64(one)), np.isfinite(y1))
+    assert np.array_equal(f64(s1)[np.isinf(S1)], S1[np.isinf(S1)]) and not np.isnan(f64(s1)).any()
