@@ -192,3 +192,14 @@ def test_offsets_past_32_bits():
     assert torch.equal(a["y"], want)
     lq.conv_prefill(cfg, a["x"], a["weight"], far, bias=a["bias"])
     assert torch.equal(far, want)
+
+
+def test_without_tokens_states_are_kept():
+    cfg = lq.conv_config(24, 4, torch.bfloat16)
+    a = inputs(13, [0, 0], 24, 4, torch.bfloat16)
+    S = torch.zeros_like(a["S0"])
+    lq.conv_prefill(cfg, a["x"], a["weight"], a["y"], cu_seqlens=cu_of([0, 0]), S0=a["S0"], S_out=S)
+    assert torch.equal(S, a["S0"])
+    lq.conv_prefill(cfg, a["x"], a["weight"], a["y"], cu_seqlens=cu_of([0, 0]), S_out=S)
+    assert bool((S == 0).all())
+    lq.conv_decode_step(cfg, S[:0], a["x"], a["weight"], a["y"])

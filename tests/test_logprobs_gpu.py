@@ -223,3 +223,8 @@ def test_agrees_with_beam_selection():
     assert torch.equal(t, ti)
     # both are within their own errors of the same numbers
     assert float((s - tl).abs().max()) <= 2.0 ** -22 + float(logprob_bounds(30011, tl.cpu().numpy(), np.zeros(1))[0].max())
+
+
+def test_no_rows():
+    e = torch.empty(0, 50, device=DEV)
+    lq.token_logprobs(e, torch.empty(0, dtype=torch.int32, device=DEV), torch.empty(0, device=DEV))
