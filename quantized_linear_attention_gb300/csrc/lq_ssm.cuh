@@ -348,6 +348,9 @@ template <typename T, bool PLUS>
 __global__ void __launch_bounds__(256, 4) k_ssm_join(SsmParams p, int blocks) {
   constexpr int U = 8;  // segments read at a time
   cudaTriggerProgrammaticLaunchCompletion();
+  // Where no sequence is longer than a segment every CTA leaves below. One waits for the first pass all the same: the second
+  // pass, and what the caller does next in the stream, count on that pass' end when this grid has ended.
+  if (blockIdx.x == 0) cudaGridDependencySynchronize();
   const int64_t b = blockIdx.x / (unsigned)blocks, row = (int64_t)p.channels * p.n_state;
   const int64_t at = (int64_t)(blockIdx.x % (unsigned)blocks) * 256 + threadIdx.x;
   Piece pc;
