@@ -130,14 +130,14 @@ struct Shape {
 
 // What a token costs: ns of an SM with nothing else to do, and ns each of many CTAs on it. Measured with 8 to 64 states, bf16 and
 // fp32: 106 to 136 and 98 to 110 with 16 states a thread, 97 to 112 and 50 to 63 with 8 (eight lanes a channel: 69 and 56),
-// 50 to 71 and 33 to 36 with 4.
+// 50 to 71 and 33 to 36 with 4 (eight lanes: 61 to 63 alone, 78 and 94 where some SMs have two CTAs).
 struct Cost {
   double alone, many;
 };
 Cost cost_of(Shape s) {
   if (s.spt == 16) return {125, 99};
   if (s.spt == 8) return {s.lpc == 8 ? 72.0 : 102.0, 54};
-  return {s.lpc == 4 ? 52.0 : 65.0, 34};
+  return {s.lpc == 4 ? 52.0 : s.lpc == 8 ? 70.0 : 65.0, 34};
 }
 
 int padded(int n_state) { return n_state <= 8 ? 8 : n_state <= 16 ? 16 : n_state <= 32 ? 32 : 64; }
