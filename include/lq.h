@@ -532,7 +532,7 @@ size_t lq_ssm_workspace_bytes(const lq_ssm_config* cfg, int64_t n_seqs, int64_t 
  * (the last factor only where z is given).
  *   x, dt, z, y  [n_tokens][channels] of cfg->dtype (tokens may lie apart); z may be NULL
  *   B, C         [n_tokens][groups][n_state] of cfg->dtype; a token's are dense
- *   A            fp32 [channels][n_state]; D, dt_bias fp32 [channels] or NULL (zero)
+ *   A            fp32 [channels][n_state]; D, dt_bias fp32 [channels] or NULL (no such term)
  *   S0, S_out    fp32 [n_seqs][channels][n_state] or NULL (a zero first state, no last
  *                one); S_out may be S0 itself
  *   workspace    256-byte aligned, lq_ssm_workspace_bytes(...) bytes for these sizes or

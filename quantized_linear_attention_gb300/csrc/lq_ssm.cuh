@@ -103,7 +103,7 @@ __device__ __forceinline__ void scan_piece(const SsmParams& p, const Piece& pc, 
   constexpr int NP = SPT * LPC, CW = 32 / LPC, CH = kNT / LPC, TT = kTile<T, SPT, LPC>, kUnroll = kGroup<T, SPT, LPC>, PER = (TT * NP + kNT - 1) / kNT, H = SPT / 2;
   const int tid = threadIdx.x, part = (tid & 31) / CW, n0 = part * SPT, col = (tid >> 5) * CW + (tid & 31) % CW;
   const int len = (int)pc.len;
-  const bool live = col < ch.left, gate = p.z != nullptr;
+  const bool live = col < ch.left, gate = p.z != nullptr, skip = p.D != nullptr;
   const int c = ch.c0 + (live ? col : 0);
   const T* x = static_cast<const T*>(p.x) + pc.begin * p.sx + ch.c0;
   const T* dt = static_cast<const T*>(p.dt) + pc.begin * p.sdt + ch.c0;
@@ -111,7 +111,7 @@ __device__ __forceinline__ void scan_piece(const SsmParams& p, const Piece& pc, 
   T* y = static_cast<T*>(p.y) + pc.begin * p.sy + ch.c0;
   const T* B = static_cast<const T*>(p.B) + pc.begin * p.sb + (int64_t)ch.g * p.n_state;
   const T* C = static_cast<const T*>(p.C) + pc.begin * p.sc + (int64_t)ch.g * p.n_state;
-  const float bias = p.dt_bias ? p.dt_bias[c] : 0.0f, D = p.D ? p.D[c] : 0.0f;
+  const float bias = p.dt_bias ? p.dt_bias[c] : 0.0f, D = skip ? p.D[c] : 0.0f;
   const T zero = from_f<T>(0.0f);
 
   // B and C of a tile: element i * kNT + tid of [token][state], into registers and from there into shared memory
@@ -246,18 +246,19 @@ __device__ __forceinline__ void scan_piece(const SsmParams& p, const Piece& pc, 
         float r[OWN];
 #pragma unroll
         for (int u = 0; u < OWN; u += OWN > 1 ? 2 : 1) {
-          float v[2], zv[2];
+          float v[2], zv[2], xv[2];
 #pragma unroll
           for (int e = 0; e < (OWN > 1 ? 2 : 1); ++e) {
             const int t = t8 + part * OWN + u + e;
             v[e] = o[u + e];
 #pragma unroll
             for (int q = 1; q < LPC; ++q) v[e] = part == q ? o[q * OWN + u + e] : v[e];
-            v[e] = __fmaf_rn(D, to_f(sm.x[buf][t][col]), v[e]);
+            xv[e] = to_f(sm.x[buf][t][col]);
             zv[e] = to_f(sm.z[buf][t][col]);
           }
           if (OWN > 1) {
             f32x2 g = f2_pack(v[0], v[1]);
+            if (skip) g = f2_fma(f2_dup(D), f2_pack(xv[0], xv[1]), g);
             if (gate) g = f2_mul(g, silu2(f2_pack(zv[0], zv[1])));
             f2_unpack(g, r[u], r[u + (OWN > 1)]);
           } else {

@@ -55,3 +55,21 @@ def test_infinite_outputs(dtype, N, T, ch):
                        z=a["z"][t:t + 1], dt_bias=a["bias"])
     assert (one[0] == INF).nonzero().flatten().tolist() == [2] and bool((s[0, 2] == INF).all())
     assert not bool(torch.isnan(one).any() or torch.isnan(s).any()) and np.isfinite(np.delete(f64(s)[0], 2, axis=0)).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,ch,N", [(60, 16, 16), (60, 24, 64), (1300, 24, 8)])
+def test_an_infinite_x_without_a_skip_term(dtype, T, ch, N):
+    """Without D there is no D x: the token of an infinite x has an infinite output too, not 0 times infinity."""
+    a = positive(inputs(21, [T], ch, N, 1, dtype, D=False))
+    t = T // 3
+    a["x"][t, 2] = INF
+    want = torch.zeros(T, ch, dtype=torch.bool, device=DEV)
+    want[t:, 2] = True
+    cfg, S = lq.ssm_config(ch, N, 1, dtype), torch.empty(1, ch, N, device=DEV)
+    call(cfg, a, [T], S, max_len=T)
+    assert torch.equal(a["y"] == INF, want) and not bool(torch.isnan(a["y"]).any())
+    one, s = torch.empty(1, ch, dtype=dtype, device=DEV), torch.ones(1, ch, N, device=DEV)
+    lq.ssm_decode_step(cfg, s, a["x"][t:t + 1], a["dt"][t:t + 1], a["A"], a["B"][t:t + 1], a["C"][t:t + 1], one, z=a["z"][t:t + 1],
+                       dt_bias=a["bias"])
+    assert (one[0] == INF).nonzero().flatten().tolist() == [2] and not bool(torch.isnan(one).any())
