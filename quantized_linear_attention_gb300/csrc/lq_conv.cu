@@ -100,7 +100,7 @@ struct Taps {
       s[i] = bias[i];
 #pragma unroll
       for (int j = 0; j < W; ++j) s[i] = f2_fma(w[j][i], in[j][i], s[i]);
-      if (act) s[i] = silu2(s[i]);
+      if (act) s[i] = silu2<T>(s[i]);
     }
     return pack<T, V>(s);
   }

@@ -35,7 +35,6 @@ constexpr int kList = 1024;   // elements collected
 constexpr int kRank = 512;    // of which at most so many are ranked
 constexpr int kFew = 64;      // ranked without another look at the bound
 constexpr int kMaxCluster = 8;
-constexpr float kLn2 = 0.693147180559945309417f;
 
 // Floats as unsigned numbers in the same order; -0 counts as +0.
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -78,11 +77,6 @@ struct Vec {
 };
 
 // Largest of four or eight elements; a NaN comes through.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 __device__ __forceinline__ float largest(const uint4& w, float) {
   return max_nan(max_nan(__uint_as_float(w.x), __uint_as_float(w.y)), max_nan(__uint_as_float(w.z), __uint_as_float(w.w)));
 }

@@ -68,7 +68,7 @@ __device__ __forceinline__ void tokens(const SsmParams& p, int64_t b, int c, int
 #pragma unroll
     for (int s = 1; s < LPC; s <<= 1) y = __fadd_rn(y, __shfl_xor_sync(0xffffffffu, y, s));
     if (p.D) y = __fmaf_rn(D, xv, y);
-    if (p.z) y = __fmul_rn(y, silu(to_f(z[k])));
+    if (p.z) y = __fmul_rn(y, silu<T>(to_f(z[k])));
     if (part == 0 && live) static_cast<T*>(p.y)[(b + k) * p.sy + c] = from_f<T>(y);
   }
 }

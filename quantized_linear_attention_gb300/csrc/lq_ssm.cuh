@@ -259,10 +259,10 @@ __device__ __forceinline__ void scan_piece(const SsmParams& p, const Piece& pc, 
           if (OWN > 1) {
             f32x2 g = f2_pack(v[0], v[1]);
             if (skip) g = f2_fma(f2_dup(D), f2_pack(xv[0], xv[1]), g);
-            if (gate) g = f2_mul(g, silu2(f2_pack(zv[0], zv[1])));
+            if (gate) g = f2_mul(g, silu2<T>(f2_pack(zv[0], zv[1])));
             f2_unpack(g, r[u], r[u + (OWN > 1)]);
           } else {
-            r[u] = gate ? __fmul_rn(v[0], silu(zv[0])) : v[0];
+            r[u] = gate ? __fmul_rn(v[0], silu<T>(zv[0])) : v[0];
           }
         }
 #pragma unroll
