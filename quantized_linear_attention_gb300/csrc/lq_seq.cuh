@@ -95,15 +95,10 @@ __device__ __forceinline__ f32x2 softplus2(f32x2 v) {
   return f2_fma(f2_fma(r, q, f2_dup(2.0f)), s, f2_pack(fmaxf(a, 0.0f), fmaxf(b, 0.0f)));
 }
 
-// Copies of 4, 8 or 16 bytes into shared memory that do not hold the thread up; the first `bytes` are read, the rest is
-// zero.
-template <int SIZE>
+// Copies 16 bytes into shared memory without holding the thread up; the first `bytes` are read, the rest is zero.
 __device__ __forceinline__ void copy_ahead(void* to, const void* from, int bytes) {
   const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
-  if (SIZE == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from), "r"(bytes) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(at), "l"(from), "n"(SIZE), "r"(bytes) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>

@@ -77,7 +77,7 @@ __device__ __forceinline__ void stage(T (*to)[CH], const T* from, int64_t stride
     const int at = i * kNT + threadIdx.x, t = at / Q, c = at % Q * E;
     if (TT * Q % kNT && t >= TT) break;
     const int n = t0 + t < len ? min(max(left - c, 0), E) : 0;
-    if (VEC) copy_ahead<16>(&to[t][c], n ? from + (int64_t)(t0 + t) * stride + c : from, n * (int)sizeof(T));
+    if (VEC) copy_ahead(&to[t][c], n ? from + (int64_t)(t0 + t) * stride + c : from, n * (int)sizeof(T));
     else if (n) to[t][c] = from[(int64_t)(t0 + t) * stride + c];
   }
 }
@@ -174,38 +174,34 @@ __device__ __forceinline__ void scan_piece(const SsmParams& p, const Piece& pc, 
     }
     __syncthreads();
     float dpart = 0.0f;
-    // Eight tokens: all steps d first, two tokens to a packed pair, then the recurrence, then the gates; shared memory is
-    // read before it is written, so that the compiler may begin all eight at once. Lanes that share a channel make the
-    // steps and gates of 8 / LPC tokens each and pass them on. CHECK: some of the eight are past the end.
+    // A group of kUnroll tokens: all steps d first, two tokens to a packed pair, then the recurrence, then the gates; shared
+    // memory is read before it is written, so that the compiler may begin the whole group at once. Lanes that share a channel
+    // make the steps and gates of OWN tokens each and pass them on. CHECK: some of the group are past the end.
     constexpr int OWN = kUnroll / LPC;
-    auto group = [&](int t8, auto check) {
+    static_assert(OWN % 2 == 0 && TT % kUnroll == 0, "tokens go in pairs, tiles in whole groups");
+    auto group = [&](int tg, auto check) {
       constexpr bool CHECK = decltype(check)::value;
-      const int n = min(kUnroll, len - t0 - t8);
+      const int n = min(kUnroll, len - t0 - tg);
       float d[OWN], dx[OWN];
 #pragma unroll
-      for (int u = 0; u < OWN; u += OWN > 1 ? 2 : 1) {
-        const int t = t8 + part * OWN + u;
+      for (int u = 0; u < OWN; u += 2) {
+        const int t = tg + part * OWN + u;
         float v[2], xv[2];
 #pragma unroll
-        for (int e = 0; e < (OWN > 1 ? 2 : 1); ++e) {
+        for (int e = 0; e < 2; ++e) {
           v[e] = __fadd_rn(to_f(sm.dt[buf][t + e][col]), bias);
           xv[e] = to_f(sm.x[buf][t + e][col]);
         }
-        if (OWN > 1) {
-          f32x2 d2 = f2_pack(v[0], v[1]);
-          if (PLUS) d2 = softplus2(d2);
-          f2_unpack(d2, d[u], d[u + (OWN > 1)]);
-          f2_unpack(f2_mul(d2, f2_pack(xv[0], xv[1])), dx[u], dx[u + (OWN > 1)]);
-        } else {
-          d[u] = PLUS ? softplus(v[0]) : v[0];
-          dx[u] = __fmul_rn(d[u], xv[0]);
-        }
+        f32x2 d2 = f2_pack(v[0], v[1]);
+        if (PLUS) d2 = softplus2(d2);
+        f2_unpack(d2, d[u], d[u + 1]);
+        f2_unpack(f2_mul(d2, f2_pack(xv[0], xv[1])), dx[u], dx[u + 1]);
       }
       float o[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         if (CHECK && u >= n) break;
-        const int t = t8 + u;
+        const int t = tg + u;
         float du = d[u % OWN], dxu = dx[u % OWN];
         if (LPC > 1) {
           const int lane = u / OWN * CW + (tid & 31) % CW;
@@ -245,36 +241,32 @@ __device__ __forceinline__ void scan_piece(const SsmParams& p, const Piece& pc, 
       if (OUT) {
         float r[OWN];
 #pragma unroll
-        for (int u = 0; u < OWN; u += OWN > 1 ? 2 : 1) {
+        for (int u = 0; u < OWN; u += 2) {
           float v[2], zv[2], xv[2];
 #pragma unroll
-          for (int e = 0; e < (OWN > 1 ? 2 : 1); ++e) {
-            const int t = t8 + part * OWN + u + e;
+          for (int e = 0; e < 2; ++e) {
+            const int t = tg + part * OWN + u + e;
             v[e] = o[u + e];
 #pragma unroll
             for (int q = 1; q < LPC; ++q) v[e] = part == q ? o[q * OWN + u + e] : v[e];
             xv[e] = to_f(sm.x[buf][t][col]);
             zv[e] = to_f(sm.z[buf][t][col]);
           }
-          if (OWN > 1) {
-            f32x2 g = f2_pack(v[0], v[1]);
-            if (skip) g = f2_fma(f2_dup(D), f2_pack(xv[0], xv[1]), g);
-            if (gate) g = f2_mul(g, silu2<T>(f2_pack(zv[0], zv[1])));
-            f2_unpack(g, r[u], r[u + (OWN > 1)]);
-          } else {
-            r[u] = gate ? __fmul_rn(v[0], silu<T>(zv[0])) : v[0];
-          }
+          f32x2 g = f2_pack(v[0], v[1]);
+          if (skip) g = f2_fma(f2_dup(D), f2_pack(xv[0], xv[1]), g);
+          if (gate) g = f2_mul(g, silu2<T>(f2_pack(zv[0], zv[1])));
+          f2_unpack(g, r[u], r[u + 1]);
         }
 #pragma unroll
-        for (int u = 0; u < OWN; ++u) sm.y[t8 + part * OWN + u][col] = from_f<T>(r[u]);  // (past the end nobody reads it)
+        for (int u = 0; u < OWN; ++u) sm.y[tg + part * OWN + u][col] = from_f<T>(r[u]);  // (past the end nobody reads it)
       }
     };
 #pragma unroll 1
-    for (int t8 = 0; t8 < TT; t8 += kUnroll) {
-      if (t0 + t8 + kUnroll <= len) {
-        group(t8, std::false_type());
+    for (int tg = 0; tg < TT; tg += kUnroll) {
+      if (t0 + tg + kUnroll <= len) {
+        group(tg, std::false_type());
       } else {
-        if (t0 + t8 < len) group(t8, std::true_type());
+        if (t0 + tg < len) group(tg, std::true_type());
         break;
       }
     }
