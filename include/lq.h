@@ -519,8 +519,10 @@ void lq_ssm_config_default(lq_ssm_config* cfg, int32_t channels, int32_t n_state
 
 /*
  * Bytes of workspace that are enough for lq_ssm_prefill with up to n_seqs sequences and
- * n_tokens tokens in all, none longer than max_len (0: not known); 0 when no such call
- * needs any or when an argument is invalid. Host only.
+ * n_tokens tokens in all, that state a max_len of at most max_len (0: calls that state
+ * none, or any); 0 when no such call needs any or when an argument is invalid. Host only.
+ * (A call that leaves its max_len out counts as one of n_tokens, however short its
+ * sequences are: ask with 0 for it.)
  */
 size_t lq_ssm_workspace_bytes(const lq_ssm_config* cfg, int64_t n_seqs, int64_t n_tokens, int64_t max_len);
 
@@ -535,12 +537,15 @@ size_t lq_ssm_workspace_bytes(const lq_ssm_config* cfg, int64_t n_seqs, int64_t 
  *   A            fp32 [channels][n_state]; D, dt_bias fp32 [channels] or NULL (no such term)
  *   S0, S_out    fp32 [n_seqs][channels][n_state] or NULL (a zero first state, no last
  *                one); S_out may be S0 itself
+ *   max_len      the longest sequence, or 0 if the caller does not know it: the call is
+ *                then divided as if one sequence had all tokens, which costs it two more
+ *                launches, and up to a quarter of its time where prompts are ragged
  *   workspace    256-byte aligned, lq_ssm_workspace_bytes(...) bytes for these sizes or
  *                larger ones (NULL if that is 0); its contents need not be kept, but calls
  *                that may run at the same time (streams, graphs) need one each
  * n_tokens is at most 2^31 - 256. States and sums are kept in fp32; y is rounded once. Any value is taken as the recurrence
  * takes it; a token's value reaches its own and later tokens of its sequence only. (Where
- * n_state is not 8, 16, 32 or 64, outputs that an infinite x or d makes infinite may be NaN,
+ * n_state is not 8, 16, 32 or 64, outputs that an infinite x, d or d x makes infinite may be NaN,
  * here and in lq_ssm_decode_step; states are as the recurrence has them.) Long
  * sequences are split into segments; channels with a positive A, a negative or infinite d,
  * or values past 1e30 pass from segment to segment token by token, which is slow.

@@ -464,7 +464,8 @@ def ssm_config(channels, n_state=16, groups=1, dtype=None, softplus=True) -> Ssm
 
 
 def ssm_workspace_bytes(cfg: SsmConfig, n_seqs: int, n_tokens: int, max_len: int = 0) -> int:
-    """Bytes that are enough for ``ssm_prefill`` with up to these sizes (0: no such call needs any)."""
+    """Bytes that are enough for ``ssm_prefill`` with up to these sizes (0: no such call needs any). Calls that do not
+    state ``max_len`` need what a query without it answers."""
     return int(load().lq_ssm_workspace_bytes(ctypes.byref(cfg), n_seqs, n_tokens, max_len))
 
 
@@ -566,7 +567,8 @@ def ssm_prefill(cfg: SsmConfig, x, dt, A, B, C, y, D=None, z=None, dt_bias=None,
                 S_out=None, workspace=None, stream=None):
     """Selective state space scan over packed prompts: x, dt, z, y [tokens][channels], B, C [tokens][groups][n_state]
     (strided tokens allowed), A fp32 [channels][n_state], D, dt_bias fp32 [channels], cu_seqlens int32 [n_seqs + 1] on
-    the device (None: one sequence), S0, S_out fp32 [n_seqs][channels][n_state]. workspace: uint8 tensor of
+    the device (None: one sequence), S0, S_out fp32 [n_seqs][channels][n_state]. max_len: the longest sequence (0: not
+    known; the call is then divided as if one had all tokens, and is slower). workspace: uint8 tensor of
     ``ssm_workspace_bytes`` for these sizes or larger ones."""
     import torch
 

@@ -73,3 +73,36 @@ def test_an_infinite_x_without_a_skip_term(dtype, T, ch, N):
     lq.ssm_decode_step(cfg, s, a["x"][t:t + 1], a["dt"][t:t + 1], a["A"], a["B"][t:t + 1], a["C"][t:t + 1], one, z=a["z"][t:t + 1],
                        dt_bias=a["bias"])
     assert (one[0] == INF).nonzero().flatten().tolist() == [2] and not bool(torch.isnan(one).any())
+
+
+@pytest.mark.parametrize("parts", [1, 60])
+@pytest.mark.parametrize("step", [0.1, 0.01, 0.001])
+def test_long_memories(step, parts):
+    """States that remember from ten to thousands of tokens, in one call (split) and in parts, each going on from the one before.
+
+    d is exact (no softplus, no bias). A decay is off by 4 units of 2^-24 for ex2.approx and |d A| times 2.3 for log2 e, its
+    product with A and that one's with d; d x B by two and the fma by one. Where a call is split a sum of d in groups of up to
+    32 tokens takes the place of its segment's exponents: off by less than 40 + n / 32 times 2^-24 for n of 64 tokens and more,
+    which weighs in by at most 1 / e of that (x e^-x) where the segment's tokens are allowed 4 n."""
+    T, ch, N, u = 3840, 40, 16, 2.0 ** -24
+    a = inputs(22, [T], ch, N, 1, torch.float32, D=False, z=False, bias=False, first=False, plus=False)
+    g = torch.Generator(device=DEV).manual_seed(23)
+    a["dt"].copy_(step * torch.exp(0.5 * torch.randn(T, ch, generator=g, device=DEV)))
+    a["A"].copy_(-0.1 - 1.4 * torch.rand(ch, N, generator=g, device=DEV))
+    for k in ("x", "B"):
+        a[k].copy_(a[k].abs() + 0.1)  # (of one sign: what errors add up to shows)
+    cfg, S = lq.ssm_config(ch, N, 1, torch.float32, softplus=False), torch.zeros(1, ch, N, device=DEV)
+    for t in range(0, T, T // parts):
+        part = {k: v[t:t + T // parts] if k in ("x", "dt", "B", "C", "y") else v for k, v in a.items()}
+        call(cfg, dict(part, S0=S), [T // parts], S, max_len=T // parts)
+    d, x, B, A = f64(a["dt"]), f64(a["x"]), f64(a["B"]), f64(a["A"])
+    h = np.zeros((ch, N))
+    E = np.zeros((ch, N))
+    for t in range(T):
+        e = d[t][:, None] * A
+        add = (d[t] * x[t])[:, None] * B[t]
+        E = np.exp(e) * (E + h * (4 + 2.3 * np.abs(e)) * u) + 2 * u * add
+        h = np.exp(e) * h + add
+        E += u * h
+    err = np.abs(f64(S)[0] - h)
+    assert np.all(err <= E), float((err / E).max())
