@@ -164,8 +164,8 @@ int64_t segment(int64_t n_tokens, int64_t ctas, int64_t blocks) {
 // Of the shapes and of whole and split sequences what should take the least time. Whole sequences take as long as the
 // longest one alone or as all tokens of all CTAs together, and some of the other as well; split ones two segments one after
 // the other and most of 1.55 times all tokens (the first pass has no outputs), and 16 us for two more launches. Measured against the other
-// choices: one sequence of 16,384 tokens x 4,096 channels of 16 states 490 us split with 16 states a thread, 833 whole with
-// four; 16 ragged ones of up to 1,500 150 and 129; one of 300 x 2,048 channels 33 and 19.
+// choices: one sequence of 16,384 tokens x 4,096 channels of 16 states 496 us split with 16 states a thread, 833 whole with
+// four; 16 ragged ones of up to 1,500 150 and 131; one of 300 x 2,048 channels 33 and 19.
 void ssm_plan(const lq_ssm_config* c, int64_t n_seqs, int64_t n_tokens, int64_t max_len, SsmPlan* plan) {
   const int64_t longest = max_len > 0 && max_len < n_tokens ? max_len : n_tokens;
   double best = 0;

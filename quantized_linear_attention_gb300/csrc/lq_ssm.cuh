@@ -28,17 +28,24 @@ namespace {
 //
 // What bounds it: 11 operands from the register file for each state and token, whose two banks give two a cycle: 105 cycles
 // of an SM's quarter for 512 states and a token, measured on these operations alone (their FMAs and their exponentials take
-// 64 each). Steps, gates and copies come on top: 1,024 tokens x 65,536 channels of 16 states (bf16) take 328 us, 180 cycles. With
+// 64 each). Steps, gates and copies come on top: 1,024 tokens x 65,536 channels of 16 states (bf16) take 340 us, 187 cycles. With
 // so few channels that an SM has one CTA the waits count instead: 136 ns a token with 16 states a thread, 52 with four
 // and 32 tokens begun together, which is a third slower where there are many.
+//
+// A decay is ex2.approx of d times A log2 e: off by (4 + 2.3 |d A|) 2^-24 of itself, for ex2 and for three roundings of the
+// exponent. What those leave out could be put back as in exp_near, for the unrounded A in as many registers again and two more
+// packed fmas to every five operations of a pair of states, where register operands are what bounds the kernel. Measured
+// after 8,192 tokens against 64 bits (fp32, no softplus; relative L2 of the states, d around 0.1, 0.01, 0.001): 5e-7, 1.2e-6,
+// 1.2e-6 split and 6e-7, 2.8e-6, 1.2e-5 whole, where an fp32 exp of a rounded d A gives 2e-7, 3.9e-6, 2.8e-5: twice to three
+// times its error where memories are short, less where they are long.
 //
 // A sequence that would leave most of the GPU idle is split into segments (ssm_plan). The first pass takes
 // every segment but the last from a zero state (the first from its true one, with its outputs) and leaves its last state and
 // the sum of its d; since the decays of a segment multiply to exp(A sum d), k_ssm_join finds the state before each segment,
 // and the second pass takes the segments from there. What that sum over segments does not give as the recurrence does (a
 // positive A or a negative d, where it may overflow though the recurrence does not, infinities, values near fp32's largest
-// number) k_ssm_join takes token by token. 16,384 tokens x 4,096 channels of 16 states (bf16) take 481 us: 207 the first
-// pass, 280 the second, which a single pass that leaves three quarters of the GPU idle cannot match (833).
+// number) k_ssm_join takes token by token. 16,384 tokens x 4,096 channels of 16 states (bf16) take 496 us: two fifths the first
+// pass, the rest the second, which a single pass that leaves three quarters of the GPU idle cannot match (833).
 constexpr int kNT = 128;
 // Tokens begun together, and in shared memory at a time. More of them hide more of each other's waits (one CTA an SM: 136 ->
 // 52 ns a token with four states a thread and 32 tokens), as far as the registers go. (Four states and eight lanes: 61 to 63 ns
